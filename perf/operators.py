@@ -386,7 +386,7 @@ def _own_handles(st, case):
     else:
         st["p"] = ab.PagedParams(S=case["S"], Hq=case["Hq"], Hkv=case["Hkv"], d=case["d"], page=case["page"], num_pages=st["num_pages"],
                                  max_pages=st["max_pages"], keep_ratio=case.get("keep") or 1.0, recent=case.get("recent", 0))
-        st["ws"] = ab.alloc_paged_workspace(st["p"], "cuda")
+        st["ws"] = ab.alloc_paged_workspace(st["p"], "cuda", select=case["kind"] == "select")
     st["ab"] = ab
 
 
@@ -399,7 +399,7 @@ def _run_own(st, case):
         return {"Q": Q, "K": K, "V": V}
     if kind == "cache":
         ab.ab_paged_plan(p, st["n_new"], st["lens"], st["table"], st["free_pages"], st["free_count"], lens_out=st["lens_out"],
-                         free_count_out=st["free_count_out"], out=(st["cu_new"], st["slots"], st["positions"]), workspace=st["ws"])
+                         free_count_out=st["free_count_out"], out=(st["cu_new"], st["slots"], st["positions"]))
         ab.ab_paged_append(p, st["nr"], st["q"], st["k"], st["v"], st["slots"], st["positions"], st["K"], st["V"], ksum=st["ksum"],
                            out=st["Q"])
         return _cache_outputs(st)

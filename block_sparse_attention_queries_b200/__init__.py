@@ -9,7 +9,11 @@ op without the built library raises ``RuntimeError``.
 
 Names follow the C ABI: ``ab_select`` (IBCS), ``ab_sample`` (SIP),
 ``ab_attention`` (the packed 1/pi-weighted sparse attention),
-``ab_attention_dense``, ``ab_forward`` and ``ab_forward_host``.
+``ab_attention_dense``, ``ab_forward`` and ``ab_forward_host``; before the path
+``ab_qk_norm_rope`` (norms of queries and keys, position rotation) and
+``ab_forward_qkv``; for models that produce their sequences step by step, a paged
+key-value cache: ``ab_paged_plan``, ``ab_paged_append``, ``ab_paged_select``,
+``ab_paged_topk``, ``ab_attention_paged`` and ``ab_paged_forward``.
 """
 from __future__ import annotations
 
@@ -27,7 +31,9 @@ STATUS_NAMES = {0: "AB_OK", 1: "AB_ERR_INVALID_ARG", 2: "AB_ERR_UNSUPPORTED", 3:
 # every symbol include/ab.h declares
 EXPORTS = ("ab_budget", "ab_workspace_size", "ab_select", "ab_sample", "ab_sample_systematic", "ab_sample_topk", "ab_attention",
            "ab_attention_dense", "ab_forward", "ab_forward_host", "ab_get_device_error",
-           "ab_status_string", "ab_select_static", "ab_forward_slice", "ab_select_sample")
+           "ab_status_string", "ab_select_static", "ab_forward_slice", "ab_select_sample",
+           "ab_qk_norm_rope", "ab_forward_qkv", "ab_paged_workspace_size", "ab_paged_plan", "ab_paged_append",
+           "ab_paged_select", "ab_paged_topk", "ab_attention_paged", "ab_paged_forward")
 
 
 class AbError(RuntimeError):
@@ -88,6 +94,95 @@ class Params:
         return Params(**args)
 
 
+class ab_norm_rope(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("n_pos", ctypes.c_int32), ("wq", ctypes.c_void_p), ("wk", ctypes.c_void_p),
+                ("cos_table", ctypes.c_void_p), ("sin_table", ctypes.c_void_p)]
+
+
+class ab_tokens(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch", ctypes.c_int64), ("token", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
+
+
+class ab_paged_params(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("recent", ctypes.c_int32), ("keep_ratio", ctypes.c_float)]
+
+
+NORMS = {"none": 0, "head": 1, "token": 2}
+
+
+class NormRope:
+    """Norm and rotation of queries and keys (mirrors ``ab_norm_rope``): ``norm``
+    is "none", "head" (mean square over each head's d) or "token" (over all
+    heads); ``wq`` and ``wk`` fp32 weights [d] or [heads, d] (None: ones);
+    ``cos`` and ``sin`` fp32 [n_pos, d/2] (both None: no rotation);
+    ``interleaved``: pairs (2i, 2i+1), else (i, i + d/2).  All tensors are
+    contiguous on one CUDA device and are kept."""
+
+    def __init__(self, norm="head", interleaved=True, eps=1e-6, wq=None, wk=None, cos=None, sin=None):
+        import torch
+        if norm not in NORMS:
+            raise ValueError(f"norm must be one of {sorted(NORMS)}, got {norm!r}")
+        if (cos is None) != (sin is None):
+            raise ValueError("cos and sin come together")
+        tensors = [t for t in (wq, wk, cos, sin) if t is not None]
+        for t in tensors:
+            if t.dtype != torch.float32 or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"weights and tables must be contiguous fp32 CUDA tensors, got {t.dtype} on {t.device}")
+            if t.device != tensors[0].device:
+                raise ValueError("weights and tables must be on one device")
+        for t in (wq, wk):
+            if t is not None and t.dim() != (2 if norm == "token" else 1):
+                raise ValueError(f"weights of norm {norm!r} have shape [{'heads, ' if norm == 'token' else ''}d], "
+                                 f"got {tuple(t.shape)}")
+        if cos is not None and (cos.dim() != 2 or cos.shape != sin.shape):
+            raise ValueError("cos and sin must be [n_pos, d/2]")
+        self.norm, self.interleaved, self.eps = norm, bool(interleaved), float(eps)
+        self.wq, self.wk, self.cos, self.sin = wq, wk, cos, sin
+        self.device = tensors[0].device if tensors else None
+        self.n_pos = 0 if cos is None else cos.shape[0]
+        self._c = ab_norm_rope(NORMS[norm], int(self.interleaved), self.eps, self.n_pos,
+                               *(0 if t is None else t.data_ptr() for t in (wq, wk, cos, sin)))
+
+    def check(self, Hq: int, Hk: int, d: int, device):
+        """The weights and tables belong to Hq query and Hk key heads of d on `device`."""
+        for t, H in ((self.wq, Hq), (self.wk, Hk)):
+            if t is not None and tuple(t.shape) != ((H, d) if self.norm == "token" else (d,)):
+                raise ValueError(f"norm weights {tuple(t.shape)} do not fit {H} heads of {d}")
+        if self.cos is not None and self.cos.shape[1] != d // 2:
+            raise ValueError(f"cos and sin have {self.cos.shape[1]} columns, {d // 2} expected")
+        if self.device is not None and self.device != device:
+            raise ValueError(f"weights and tables are on {self.device}, the tokens on {device}")
+
+
+@dataclass(frozen=True)
+class PagedParams:
+    """A paged key-value cache (mirrors ``ab_paged_params``): ``S`` sequences with
+    up to ``max_pages`` of the ``num_pages`` pages of ``page`` tokens each;
+    ``keep_ratio`` and ``recent`` are ``ab_paged_topk``'s."""
+
+    S: int
+    Hq: int
+    Hkv: int
+    d: int
+    page: int
+    num_pages: int
+    max_pages: int
+    keep_ratio: float = 0.1
+    recent: int = 1
+
+    def c(self) -> ab_paged_params:
+        c = self.__dict__.get("_c")
+        if c is None:
+            c = ab_paged_params(self.S, self.Hq, self.Hkv, self.d, self.page, self.num_pages, self.max_pages, self.recent,
+                                float(self.keep_ratio))
+            object.__setattr__(self, "_c", c)
+        return c
+
+
 _lib = None
 
 
@@ -118,6 +213,21 @@ def lib(path: str = LIB_PATH):
         L.ab_get_device_error.argtypes = [vp, ctypes.POINTER(ctypes.c_int32)]
         L.ab_status_string.argtypes = [ctypes.c_int]
         L.ab_status_string.restype = ctypes.c_char_p
+        NR, TK, PP, i32 = (ctypes.POINTER(ab_norm_rope), ctypes.POINTER(ab_tokens), ctypes.POINTER(ab_paged_params),
+                           ctypes.c_int32)
+        L.ab_qk_norm_rope.argtypes = [P, NR, TK, TK, TK, vp, vp, vp, vp, vp, vp]
+        L.ab_forward_qkv.argtypes = [P, NR, TK, TK, TK, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.ab_paged_workspace_size.argtypes = [PP, i32, ctypes.POINTER(ctypes.c_size_t)]
+        L.ab_paged_plan.argtypes = [PP, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.ab_paged_append.argtypes = [PP, NR, i32, TK, TK, TK, vp, vp, vp, vp, vp, vp, vp]
+        L.ab_paged_select.argtypes = [PP, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.ab_paged_topk.argtypes = [PP, vp, vp, vp, vp, vp]
+        L.ab_attention_paged.argtypes = [PP, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.ab_paged_forward.argtypes = [PP, NR, i32, TK, TK, TK, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                       sz, vp]
+        for name in ("ab_qk_norm_rope", "ab_forward_qkv", "ab_paged_workspace_size", "ab_paged_plan",
+                     "ab_paged_append", "ab_paged_select", "ab_paged_topk", "ab_attention_paged", "ab_paged_forward"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("ab_workspace_size", "ab_select", "ab_sample", "ab_sample_systematic", "ab_sample_topk", "ab_attention",
                      "ab_attention_dense",
                      "ab_forward", "ab_forward_host", "ab_get_device_error", "ab_select_static",
@@ -373,6 +483,334 @@ def ab_forward_host(p: Params, Qh, Kh, Vh, Oh, Qd, Kd, Vd, bufs: Buffers, device
                                  _ptr(Kd), _ptr(Vd), _ptr(bufs.P), _ptr(bufs.idx), _ptr(bufs.pi_q32),
                                  _ptr(bufs.count), _ptr(bufs.O), _ptr(bufs.ws), bufs.ws.numel(),
                                  _stream(device)), "ab_forward_host")
+
+
+# ------------------------------------------- norm and rotation, paged cache
+def _check_tensor(t, dtype, shape, device, name):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: expected contiguous {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)}"
+                         f"{'' if t.is_contiguous() else ' (strided)'} on {t.device}")
+
+
+def _call(fn_name, device, *args):
+    """The library's function on `device` and its current stream."""
+    import torch
+    fn = getattr(lib(), fn_name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != AB_OK:
+        raise AbError(status, fn_name)
+
+
+def _cuda_device(t):
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.device
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _tokens(t, shape, device, name):
+    """The strided tokens [(B,) T, H, d] as the library takes them."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.device != device or t.stride(-1) != 1:
+        raise ValueError(f"{name}: expected bf16 {list(shape)} with contiguous heads on {device}, got {t.dtype} "
+                         f"{list(t.shape)}, strides {t.stride()}, on {t.device}")
+    st = t.stride()
+    return ab_tokens(t.data_ptr(), st[0] if len(shape) == 4 else 0, st[-3], st[-2])
+
+
+def _dense_tokens(p: Params, nr: NormRope, q, k, v, pos_q, pos_k):
+    """Checked arguments of the calls from the projections' layout."""
+    import torch
+    given = [t for t in (q, k, v) if t is not None]
+    if not given:
+        raise ValueError("none of q, k, v is given")
+    dev = _cuda_device(given[0])
+    nr.check(p.H, p.H, p.d, dev)
+    tok = [None if t is None else _tokens(t, (p.B, n, p.H, p.d), dev, name)
+           for t, n, name in ((q, p.L, "q"), (k, p.Lk, "k"), (v, p.Lk, "v"))]
+    for pos, n, name in ((pos_q, p.L, "pos_q"), (pos_k, p.Lk, "pos_k")):
+        if pos is not None:
+            _check_tensor(pos, torch.int32, (p.B, n), dev, name)
+    return dev, tok
+
+
+def _span(t):
+    """First byte of a tensor and the one behind its last."""
+    n = 1 + sum((k - 1) * st for k, st in zip(t.shape, t.stride())) if t.numel() else 0
+    return t.data_ptr(), t.data_ptr() + n * t.element_size()
+
+
+def _apart(out, inputs):
+    """No output reaches into an input's span or another output's, except that the
+    inputs may share one."""
+    spans = [_span(t) for t in out if t is not None]
+    for k, (lo, hi) in enumerate(spans):
+        for lo2, hi2 in spans[:k] + [_span(t) for t in inputs if t is not None]:
+            if lo < hi2 and lo2 < hi:
+                raise ValueError("outputs must not overlap each other or the inputs")
+
+
+def ab_qk_norm_rope(p: Params, nr: NormRope, q, k=None, v=None, pos_q=None, pos_k=None, out=None):
+    """Norm and rotation from the projections' layout to the attention's: q
+    [B, L, H, d], k and v [B, Lk, H, d] bf16 (any strides that are multiples of
+    8, e.g. slices of a fused projection; each may be None); returns
+    (Q, K, V) [B, H, L or Lk, d] bf16 (None for what was not given), ready for
+    ``ab_forward``.  pos_q [B, L], pos_k [B, Lk] int32 are the tokens' rows in
+    the tables (None: 0, 1, 2, ...).  `out` = (Q, K, V) writes into caller-owned
+    tensors."""
+    import torch
+    dev, tok = _dense_tokens(p, nr, q, k, v, pos_q, pos_k)
+    shapes = [None if t is None else (p.B, p.H, n, p.d) for t, n in ((q, p.L), (k, p.Lk), (v, p.Lk))]
+    if out is None:
+        out = tuple(None if s is None else torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes)
+    else:
+        for t, s, name in zip(out, shapes, "QKV"):
+            if s is not None:
+                _check_tensor(t, torch.bfloat16, s, dev, name)
+        _apart([t for t, s in zip(out, shapes) if s is not None], (q, k, v))
+    _call("ab_qk_norm_rope", dev, p.c(), nr._c, *tok, _p(pos_q), _p(pos_k), *(_p(t) for t in out))
+    return tuple(t if s is not None else None for t, s in zip(out, shapes))
+
+
+def ab_forward_qkv(p: Params, nr: NormRope, q, k, v, pos_q=None, pos_k=None, bufs: Buffers | None = None) -> Buffers:
+    """``ab_qk_norm_rope`` then ``ab_forward``: the path from the projections q
+    [B, L, H, d], k and v [B, Lk, H, d].  The rotated tensors are the returned
+    buffers' Q, K and V (made on the first call if `bufs` has none)."""
+    import torch
+    dev, tok = _dense_tokens(p, nr, q, k, v, pos_q, pos_k)
+    if None in tok:
+        raise ValueError("q, k and v are all needed")
+    b = Buffers(p, dev) if bufs is None else bufs
+    for name, n in (("Q", p.L), ("K", p.Lk), ("V", p.Lk)):
+        if getattr(b, name, None) is None:
+            setattr(b, name, torch.empty(p.B, p.H, n, p.d, dtype=torch.bfloat16, device=dev))
+        _check_tensor(getattr(b, name), torch.bfloat16, (p.B, p.H, n, p.d), dev, name)
+    _apart((b.Q, b.K, b.V), (q, k, v))
+    for name, shape in (("P", (p.B, p.H, p.Nq, p.Nkv)), ("idx", (p.B, p.H, p.Nq, p.Nkv)),
+                        ("pi_q32", (p.B, p.H, p.Nq, p.Nkv)), ("count", (p.B, p.H, p.Nq)), ("O", (p.B, p.H, p.L, p.d))):
+        _check_tensor(getattr(b, name), getattr(b, name).dtype, shape, dev, name)
+    _call("ab_forward_qkv", dev, p.c(), nr._c, *tok, _p(pos_q), _p(pos_k), _p(b.Q), _p(b.K), _p(b.V), _p(b.P),
+          _p(b.idx), _p(b.pi_q32), _p(b.count), _p(b.O), _p(b.ws), b.ws.numel())
+    return b
+
+
+def paged_workspace_size(pp: PagedParams, select=True) -> int:
+    """Bytes of workspace for ab_attention_paged, and with `select` for
+    ab_paged_select and ab_paged_forward too."""
+    n = ctypes.c_size_t(0)
+    _check(lib().ab_paged_workspace_size(pp.c(), int(bool(select)), n), "ab_paged_workspace_size")
+    return int(n.value)
+
+
+def alloc_paged_workspace(pp: PagedParams, device, select=True):
+    import torch
+    return torch.empty(paged_workspace_size(pp, select), dtype=torch.uint8, device=device)
+
+
+class PagedCache:
+    """A cache's tensors: K, V [num_pages, Hkv, page, d] and ksum
+    [num_pages, Hkv, d] bf16, the block table [S, max_pages], the sequences'
+    lengths, the list of free pages with its count, and a workspace.  All
+    sequences are empty, all pages free."""
+
+    def __init__(self, pp: PagedParams, device, select=True):
+        import torch
+        kv = (pp.num_pages, pp.Hkv, pp.page, pp.d)
+        self.K, self.V = (torch.empty(kv, dtype=torch.bfloat16, device=device) for _ in range(2))
+        self.ksum = torch.empty(pp.num_pages, pp.Hkv, pp.d, dtype=torch.bfloat16, device=device)
+        self.table = torch.zeros(pp.S, pp.max_pages, dtype=torch.int32, device=device)
+        self.lens = torch.zeros(pp.S, dtype=torch.int32, device=device)
+        self.free_pages = torch.arange(pp.num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.free_count = torch.full((1,), pp.num_pages, dtype=torch.int32, device=device)
+        self.ws = alloc_paged_workspace(pp, device, select)
+
+
+def ab_paged_plan(pp: PagedParams, n_new, lens, table, free_pages, free_count, T=None, lens_out=None,
+                  free_count_out=None, out=None):
+    """Block tables and slot maps of one step: n_new [S] int32 new tokens per
+    sequence (-1: the sequence has ended), lens [S], table [S, max_pages],
+    free_pages [num_pages], free_count [1] int32.  Updates table and free_pages,
+    lens and free_count too (or writes lens_out, free_count_out instead);
+    returns (cu_new [S + 1], slots [T], positions [T]).  T: length of the slot
+    map (at least the number of new tokens; None with `out`: that of out's
+    slots).  `out` = (cu_new, slots, positions) writes into caller-owned
+    tensors."""
+    import torch
+    dev = _cuda_device(n_new)
+    i32 = torch.int32
+    if out is None:
+        if T is None:
+            raise ValueError("T or out is needed")
+        out = (torch.empty(pp.S + 1, dtype=i32, device=dev), torch.empty(T, dtype=i32, device=dev),
+               torch.empty(T, dtype=i32, device=dev))
+    elif T is None:
+        T = out[1].numel()
+    lens_out = lens if lens_out is None else lens_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    for t, shape, name in ((n_new, (pp.S,), "n_new"), (lens, (pp.S,), "lens"), (lens_out, (pp.S,), "lens_out"),
+                           (table, (pp.S, pp.max_pages), "table"), (free_pages, (pp.num_pages,), "free_pages"),
+                           (free_count, (1,), "free_count"), (free_count_out, (1,), "free_count_out"),
+                           (out[0], (pp.S + 1,), "cu_new"), (out[1], (T,), "slots"), (out[2], (T,), "positions")):
+        _check_tensor(t, i32, shape, dev, name)
+    _call("ab_paged_plan", dev, pp.c(), T, *(t.data_ptr() for t in (n_new, lens, lens_out, table, free_pages, free_count,
+                                                                  free_count_out, *out)))
+    return out
+
+
+def _paged_tokens(pp: PagedParams, nr: NormRope, q, k, v, slots, positions, K, V, ksum, Q):
+    """Checked arguments of the calls that write tokens into the cache."""
+    import torch
+    dev = _cuda_device(q)
+    T = q.shape[0]
+    nr.check(pp.Hq, pp.Hkv, pp.d, dev)
+    tok = (_tokens(q, (T, pp.Hq, pp.d), dev, "q"), _tokens(k, (T, pp.Hkv, pp.d), dev, "k"),
+           _tokens(v, (T, pp.Hkv, pp.d), dev, "v"))
+    _check_tensor(slots, torch.int32, (T,), dev, "slots")
+    _check_tensor(positions, torch.int32, (T,), dev, "positions")
+    kv = (pp.num_pages, pp.Hkv, pp.page, pp.d)
+    _check_tensor(K, torch.bfloat16, kv, dev, "K")
+    _check_tensor(V, torch.bfloat16, kv, dev, "V")
+    if ksum is not None:
+        _check_tensor(ksum, torch.bfloat16, (pp.num_pages, pp.Hkv, pp.d), dev, "ksum")
+    if Q is None:
+        Q = torch.empty(T, pp.Hq, pp.d, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_tensor(Q, torch.bfloat16, (T, pp.Hq, pp.d), dev, "Q")
+        _apart((Q,), (q, k, v))
+    return dev, T, tok, Q
+
+
+def ab_paged_append(pp: PagedParams, nr: NormRope, q, k, v, slots, positions, K, V, ksum=None, out=None):
+    """Norm and rotation of new tokens q [T, Hq, d], k and v [T, Hkv, d] bf16
+    (strides as for ab_qk_norm_rope), keys and values written to their slots of
+    the cache, the touched pages' means to ksum (None: not kept); returns the
+    queries Q [T, Hq, d] (`out` if given)."""
+    dev, T, tok, Q = _paged_tokens(pp, nr, q, k, v, slots, positions, K, V, ksum, out)
+    if T:
+        _call("ab_paged_append", dev, pp.c(), nr._c, T, *tok, _p(slots), _p(positions), _p(Q), _p(K), _p(V), _p(ksum))
+    return Q
+
+
+def _paged_rows(pp: PagedParams, Q, table, lens, cu_new):
+    import torch
+    dev = _cuda_device(Q)
+    T = Q.shape[0]
+    if cu_new is None and T != pp.S:
+        raise ValueError(f"Q has {T} rows, {pp.S} expected without cu_new")
+    _check_tensor(Q, torch.bfloat16, (T, pp.Hq, pp.d), dev, "Q")
+    _check_tensor(table, torch.int32, (pp.S, pp.max_pages), dev, "table")
+    _check_tensor(lens, torch.int32, (pp.S,), dev, "lens")
+    if cu_new is not None:
+        _check_tensor(cu_new, torch.int32, (pp.S + 1,), dev, "cu_new")
+    return dev, T
+
+
+def _paged_ws(pp: PagedParams, workspace, dev, select):
+    import torch
+    if workspace is None:
+        return alloc_paged_workspace(pp, dev, select)
+    _check_tensor(workspace, torch.uint8, (workspace.numel(),), dev, "workspace")
+    return workspace
+
+
+def ab_paged_select(pp: PagedParams, Q, ksum, table, lens, cu_new=None, workspace=None, out=None):
+    """Every page's estimated share P [S, Hkv, max_pages] fp32 of the attention
+    mass of each sequence's newest token (entries behind a sequence's last page
+    are left as they were, 0 in a new P).  Q [S, Hq, d], or [T, Hq, d] with
+    cu_new [S + 1] as ab_paged_plan returns it."""
+    import torch
+    dev, T = _paged_rows(pp, Q, table, lens, cu_new)
+    _check_tensor(ksum, torch.bfloat16, (pp.num_pages, pp.Hkv, pp.d), dev, "ksum")
+    shape = (pp.S, pp.Hkv, pp.max_pages)
+    P = torch.zeros(shape, dtype=torch.float32, device=dev) if out is None else out
+    _check_tensor(P, torch.float32, shape, dev, "P")
+    ws = _paged_ws(pp, workspace, dev, True)
+    _call("ab_paged_select", dev, pp.c(), T, _p(Q), _p(ksum), _p(table), _p(lens), _p(cu_new), _p(P), _p(ws), ws.numel())
+    return P
+
+
+def ab_paged_topk(pp: PagedParams, P, lens, out=None):
+    """The pages to attend to: (idx [S, Hkv, max_pages], count [S, Hkv]) int32,
+    the newest `recent` pages and those of largest P, keep_ratio of them in all."""
+    import torch
+    dev = _cuda_device(P)
+    shape = (pp.S, pp.Hkv, pp.max_pages)
+    _check_tensor(P, torch.float32, shape, dev, "P")
+    _check_tensor(lens, torch.int32, (pp.S,), dev, "lens")
+    if out is None:
+        out = (torch.zeros(shape, dtype=torch.int32, device=dev), torch.zeros(shape[:2], dtype=torch.int32, device=dev))
+    _check_tensor(out[0], torch.int32, shape, dev, "idx")
+    _check_tensor(out[1], torch.int32, shape[:2], dev, "count")
+    _call("ab_paged_topk", dev, pp.c(), _p(P), _p(lens), _p(out[0]), _p(out[1]))
+    return out
+
+
+def ab_attention_paged(pp: PagedParams, Q, K, V, table, lens, idx=None, count=None, cu_new=None, workspace=None,
+                       out=None):
+    """Attention of each sequence's newest token over the cache (all pages, or
+    the listed ones); Q as for ab_paged_select; returns O [S, Hq, d] bf16 (rows
+    of sequences without a new token are left as they were, 0 in a new O)."""
+    import torch
+    dev, T = _paged_rows(pp, Q, table, lens, cu_new)
+    kv = (pp.num_pages, pp.Hkv, pp.page, pp.d)
+    _check_tensor(K, torch.bfloat16, kv, dev, "K")
+    _check_tensor(V, torch.bfloat16, kv, dev, "V")
+    if (idx is None) != (count is None):
+        raise ValueError("idx and count come together")
+    if idx is not None:
+        _check_tensor(idx, torch.int32, (pp.S, pp.Hkv, pp.max_pages), dev, "idx")
+        _check_tensor(count, torch.int32, (pp.S, pp.Hkv), dev, "count")
+    shape = (pp.S, pp.Hq, pp.d)
+    O = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if out is None else out
+    _check_tensor(O, torch.bfloat16, shape, dev, "O")
+    ws = _paged_ws(pp, workspace, dev, False)
+    _call("ab_attention_paged", dev, pp.c(), T, _p(Q), _p(K), _p(V), _p(table), _p(lens), _p(cu_new), _p(idx), _p(count),
+          _p(O), _p(ws), ws.numel())
+    return O
+
+
+class PagedBuffers:
+    """Outputs of ab_paged_forward: Q [T, Hq, d], P, idx, count and O [S, Hq, d]."""
+
+    def __init__(self, pp: PagedParams, T: int, device):
+        import torch
+        shape = (pp.S, pp.Hkv, pp.max_pages)
+        self.Q = torch.zeros(T, pp.Hq, pp.d, dtype=torch.bfloat16, device=device)
+        self.P = torch.zeros(shape, dtype=torch.float32, device=device)
+        self.idx = torch.zeros(shape, dtype=torch.int32, device=device)
+        self.count = torch.zeros(shape[:2], dtype=torch.int32, device=device)
+        self.O = torch.zeros(pp.S, pp.Hq, pp.d, dtype=torch.bfloat16, device=device)
+
+
+def ab_paged_forward(pp: PagedParams, nr: NormRope, q, k, v, cache: PagedCache, cu_new, slots, positions,
+                     bufs: PagedBuffers | None = None) -> PagedBuffers:
+    """One step of sparse attention over the cache for new tokens q [T, Hq, d], k
+    and v [T, Hkv, d], after ab_paged_plan: append, select, top-k, attention of
+    each sequence's newest token."""
+    import torch
+    T = q.shape[0]
+    b = PagedBuffers(pp, T, _cuda_device(q)) if bufs is None else bufs
+    c = cache
+    dev, T, tok, Q = _paged_tokens(pp, nr, q, k, v, slots, positions, c.K, c.V, c.ksum, b.Q)
+    _paged_rows(pp, Q, c.table, c.lens, cu_new)
+    if cu_new is None:
+        raise ValueError("cu_new is needed")
+    shape = (pp.S, pp.Hkv, pp.max_pages)
+    for t, dtype, s, name in ((c.ksum, torch.bfloat16, (pp.num_pages, pp.Hkv, pp.d), "ksum"), (b.P, torch.float32, shape, "P"),
+                              (b.idx, torch.int32, shape, "idx"), (b.count, torch.int32, shape[:2], "count"),
+                              (b.O, torch.bfloat16, (pp.S, pp.Hq, pp.d), "O")):
+        _check_tensor(t, dtype, s, dev, name)
+    ws = _paged_ws(pp, c.ws, dev, True)
+    _call("ab_paged_forward", dev, pp.c(), nr._c, T, *tok, _p(slots), _p(positions), _p(c.table), _p(c.lens), _p(cu_new),
+          _p(Q), _p(c.K), _p(c.V), _p(c.ksum), _p(b.P), _p(b.idx), _p(b.count), _p(b.O), _p(ws), ws.numel())
+    return b
 
 
 def device_error(device=None) -> int:

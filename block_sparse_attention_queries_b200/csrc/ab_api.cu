@@ -1,7 +1,9 @@
 // C ABI of the AB-Attention hot path (declared in include/ab.h): argument
 // checks, workspace layout, TMA descriptors and kernel launches.  The library
 // allocates no memory; every buffer belongs to the caller.
+#include <climits>
 #include <cmath>
+#include <initializer_list>
 #include <vector>
 #include <cstdio>
 #include <cstring>
@@ -14,6 +16,8 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "ab_attention.cuh"
+#include "ab_norm_rope.cuh"
+#include "ab_paged_attention.cuh"
 #include "ab_sample.cuh"
 #include "ab_select.cuh"
 
@@ -789,3 +793,5 @@ const char* ab_status_string(ab_status s) {
 }
 
 }  // extern "C"
+
+#include "ab_paged_api.cuh"

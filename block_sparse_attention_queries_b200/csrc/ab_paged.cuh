@@ -1,0 +1,720 @@
+// A paged key-value cache: block tables and slot maps from the requests'
+// lengths, page summaries, and the selection of pages for one new token per
+// sequence.  The attention over the cache is in ab_paged_attention.cuh.
+//
+// The cache holds num_pages pages of `page` tokens; K and V are
+// [num_pages, Hkv, page, d], so that one page of one head is a contiguous run
+// of 2 to 16 KB.  Sequence s's j-th page is table[s][j]; slot = page id * page
+// + offset names a token's place.
+#pragma once
+
+#include <climits>
+
+#include "ab_ptx.cuh"
+
+namespace ab {
+
+constexpr int kMaxSeqs = 8192;   // sequences of a block table: their prefix sums fit in shared memory
+constexpr int kMaxGroup = 16;    // query heads per key/value head
+
+struct PagedView {
+  const int32_t* table;   // [S, max_pages]
+  const int32_t* lens;    // [S]
+  const int32_t* cu_new;  // [S + 1] or null: row of Q (null: row s)
+  int T;                  // rows of Q
+  int S, Hkv, G;
+  int page, page_shift, num_pages, max_pages;
+};
+
+// Tokens of sequence s, 0 if the length is out of range.
+__device__ __forceinline__ int seq_len(const PagedView& v, int s) {
+  const int n = __ldg(v.lens + s);
+  if (n < 0 || n > v.max_pages << v.page_shift) {
+    raise_error(AB_ERR_CAPACITY);
+    return 0;
+  }
+  return n;
+}
+__device__ __forceinline__ int pages_of(const PagedView& v, int tokens) {
+  return (tokens + v.page - 1) >> v.page_shift;
+}
+// Row of Q that holds sequence s's newest token, -1 if it has none.
+__device__ __forceinline__ int query_row(const PagedView& v, int s) {
+  if (!v.cu_new) return s;
+  const int lo = __ldg(v.cu_new + s), hi = __ldg(v.cu_new + s + 1);
+  if (hi <= lo) return -1;
+  if (hi > v.T || lo < 0) {
+    raise_error(AB_ERR_CAPACITY);
+    return -1;
+  }
+  return hi - 1;
+}
+
+// ------------------------------------------------------------------- plan
+// One cluster of 8 CTAs.  Each CTA computes the prefix sums of all sequences
+// in shared memory (the inputs are a few KB), then the CTAs share the list
+// entries, table entries and slots.  The cluster's barrier stands between the
+// last read of lens and free_count and their update, so both may be updated in
+// place.  Bound by latency: a step of 256 sequences moves a few KB.
+constexpr int kPlanCtas = 8;
+constexpr int kPlanThreads = 1024;
+
+struct PlanArgs {
+  int S, T, page, page_shift, num_pages, max_pages;
+  const int32_t *n_new, *lens;
+  int32_t* lens_out;
+  int32_t* table;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  int32_t *cu_new, *slots, *positions;
+};
+
+struct PlanScan {
+  int64_t rel, need, want;
+};
+__device__ __forceinline__ PlanScan operator+(const PlanScan& a, const PlanScan& b) {
+  return {a.rel + b.rel, a.need + b.need, a.want + b.want};
+}
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
+  extern __shared__ int32_t plan_smem[];
+  // prefix sums over the sequences ([0] = 0) and the lengths before the step
+  int32_t* cu_want = plan_smem;                 // [S + 1]
+  int32_t* cu_need = cu_want + a.S + 1;         // [S + 1]
+  int32_t* cu_rel = cu_need + a.S + 1;          // [S + 1]
+  int32_t* old_len = cu_rel + a.S + 1;          // [S]
+  __shared__ PlanScan warp_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  int F0 = *a.free_count;
+  if (F0 < 0 || F0 > a.num_pages) {
+    if (tid == 0) raise_error(AB_ERR_CAPACITY);
+    F0 = F0 < 0 ? 0 : a.num_pages;
+  }
+
+  // what sequence s gives back and asks for
+  auto ask = [&](int s) -> PlanScan {
+    PlanScan v{0, 0, 0};
+    if (s >= a.S) return v;
+    int len = a.lens[s];
+    const int n = a.n_new[s];
+    const int cap = a.max_pages << a.page_shift;
+    bool bad = n < -1;
+    if (len < 0 || len > cap) {
+      bad = true;
+      len = len < 0 ? 0 : cap;
+    }
+    old_len[s] = len;
+    const int old = (len + a.page - 1) >> a.page_shift;
+    if (!bad && n == -1) {
+      v.rel = old;
+    } else if (!bad && n > 0) {
+      if (n > cap - len) {
+        bad = true;  // longer than its row of the table: not served
+      } else {
+        v.need = ((len + n + a.page - 1) >> a.page_shift) - old;
+        v.want = n;
+      }
+    }
+    if (bad) raise_error(AB_ERR_CAPACITY);
+    return v;
+  };
+  auto block_scan = [&](PlanScan v, PlanScan& total) -> PlanScan {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const PlanScan y{__shfl_up_sync(0xffffffffu, v.rel, o), __shfl_up_sync(0xffffffffu, v.need, o),
+                       __shfl_up_sync(0xffffffffu, v.want, o)};
+      if (lane >= o) v = v + y;
+    }
+    __syncthreads();  // warp_sum is reused
+    if (lane == 31) warp_sum[warp] = v;
+    __syncthreads();
+    PlanScan w = warp_sum[lane];
+    const PlanScan mine = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const PlanScan y{__shfl_up_sync(0xffffffffu, w.rel, o), __shfl_up_sync(0xffffffffu, w.need, o),
+                       __shfl_up_sync(0xffffffffu, w.want, o)};
+      if (lane >= o) w = w + y;
+    }
+    total = {__shfl_sync(0xffffffffu, w.rel, 31), __shfl_sync(0xffffffffu, w.need, 31),
+             __shfl_sync(0xffffffffu, w.want, 31)};
+    const PlanScan before{w.rel - mine.rel, w.need - mine.need, w.want - mine.want};
+    return v + PlanScan{__shfl_sync(0xffffffffu, before.rel, warp), __shfl_sync(0xffffffffu, before.need, warp),
+                        __shfl_sync(0xffffffffu, before.want, warp)};
+  };
+
+  // all pages given back (they can be handed out again in this step)
+  PlanScan total{0, 0, 0}, t;
+  int64_t rel_all = 0;
+  const bool one_chunk = a.S <= kPlanThreads;
+  PlanScan v{0, 0, 0}, incl{0, 0, 0};
+  for (int s0 = 0; s0 < a.S; s0 += kPlanThreads) {
+    v = ask(s0 + tid);
+    incl = block_scan(v, t);
+    rel_all += t.rel;
+  }
+  if (F0 + rel_all > a.num_pages) {  // a page given back twice, or lists that do not belong together
+    if (tid == 0) raise_error(AB_ERR_CAPACITY);
+    rel_all = a.num_pages - F0;
+  }
+  const int F = F0 + int(rel_all);
+
+  // the sequences up to the first that no longer fits are served
+  for (int s0 = 0; s0 < a.S; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    if (!one_chunk) {
+      v = ask(s);
+      incl = block_scan(v, t);
+    }
+    const PlanScan c = total + incl;
+    if (s < a.S) {
+      // sums beyond the first that does not fit are mended below
+      cu_rel[s + 1] = int(c.rel < rel_all ? c.rel : rel_all);
+      cu_need[s + 1] = c.need <= F && c.want <= a.T ? int(c.need) : -1;
+      cu_want[s + 1] = int(c.want < a.T ? c.want : a.T);
+    }
+    total = total + t;
+  }
+  if (tid == 0) cu_want[0] = cu_need[0] = cu_rel[0] = 0;
+  __syncthreads();
+  if (total.need > F || total.want > a.T) {
+    // the served sequences are a prefix: find its end, repeat its sums behind it
+    if (tid == 0) raise_error(AB_ERR_CAPACITY);
+    int lo = 0, hi = a.S;  // cu_need[lo] >= 0, the answer is the last such index
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (cu_need[m] >= 0) lo = m;
+      else hi = m - 1;
+    }
+    const int need = cu_need[lo], want = cu_want[lo];
+    __syncthreads();
+    for (int s = lo + 1 + tid; s <= a.S; s += kPlanThreads) {
+      cu_need[s] = need;
+      cu_want[s] = want;
+    }
+    __syncthreads();
+  }
+  const int n_rel = cu_rel[a.S], n_need = cu_need[a.S], n_want = cu_want[a.S];
+
+  // the last sequence whose prefix sum is <= i
+  auto find = [&](const int32_t* cu, int i) -> int {
+    int lo = 0, hi = a.S - 1;
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (cu[m] <= i) lo = m;
+      else hi = m - 1;
+    }
+    return lo;
+  };
+  auto given_back = [&](int i) -> int {
+    const int s = find(cu_rel, i);
+    return a.table[int64_t(s) * a.max_pages + (i - cu_rel[s])];
+  };
+  // the i-th page handed out: from the top of the list, the pages given back in this step first
+  auto handed_out = [&](int i) -> int {
+    const int at = F - 1 - i;
+    return at >= F0 ? given_back(at - F0) : a.free_pages[at];
+  };
+  const int64_t gtid = int64_t(blockIdx.x) * kPlanThreads + tid, gstep = int64_t(kPlanCtas) * kPlanThreads;
+  for (int64_t t64 = gtid; t64 < a.T; t64 += gstep) {
+    const int tk = int(t64);
+    int slot = -1, pos = 0;
+    if (tk < n_want) {
+      const int s = find(cu_want, tk);
+      const int len = old_len[s], old = (len + a.page - 1) >> a.page_shift;
+      pos = len + tk - cu_want[s];
+      const int j = pos >> a.page_shift;
+      const int id = j < old ? a.table[int64_t(s) * a.max_pages + j] : handed_out(cu_need[s] + j - old);
+      if (id >= 0 && id < a.num_pages) {
+        slot = (id << a.page_shift) + (pos & (a.page - 1));
+      } else {
+        raise_error(AB_ERR_CAPACITY);
+      }
+    }
+    a.slots[tk] = slot;
+    a.positions[tk] = pos;
+  }
+  // The table rows written here (served sequences, entries from their old
+  // number of pages on) are never read above, the list entries written here
+  // (from F0 on) neither.
+  for (int64_t i = gtid; i < n_need; i += gstep) {
+    const int s = find(cu_need, int(i));
+    const int old = (old_len[s] + a.page - 1) >> a.page_shift;
+    a.table[int64_t(s) * a.max_pages + old + (int(i) - cu_need[s])] = handed_out(int(i));
+  }
+  for (int64_t i = gtid; i < n_rel; i += gstep) a.free_pages[F0 + i] = given_back(int(i));
+
+  // every CTA has read lens and free_count
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  for (int64_t s = gtid; s <= a.S; s += gstep) {
+    a.cu_new[s] = cu_want[s];
+    if (s < a.S) {
+      const int len = a.lens[s];
+      const bool ended = a.n_new[s] == -1 && len == old_len[s];  // a length out of range stays as it is
+      a.lens_out[s] = ended ? 0 : len + cu_want[s + 1] - cu_want[s];
+    }
+  }
+  if (gtid == 0) *a.free_count_out = F - n_need;
+}
+
+// -------------------------------------------------------------- summaries
+// Mean of a page's keys, for every page that a slot list touches: the last
+// slot of each run of slots in one page owns the page, and the mean is over
+// the page's keys up to that slot.  A warp takes one (page, head), a run of at
+// most 16 KB.  Bound by memory (the page's keys are read once).
+template <int D>
+__global__ void __launch_bounds__(256)
+    page_sum_kernel(const int32_t* slots, int T, int per_cta, const __nv_bfloat16* K, __nv_bfloat16* ksum, int Hkv,
+                    int page_shift, int num_pages) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t0 = blockIdx.x * per_cta;
+  int slot = -1;
+  if (lane < per_cta && t0 + lane < T) {
+    slot = __ldg(slots + t0 + lane);
+    if (slot >> page_shift >= num_pages) slot = -1;  // reported where the token is written
+    if (slot >= 0 && t0 + lane + 1 < T && __ldg(slots + t0 + lane + 1) >> page_shift == slot >> page_shift) slot = -1;
+  }
+  uint32_t owners = __ballot_sync(0xffffffffu, slot >= 0);
+  const int sub = lane % kLanes, row0 = lane / kLanes;
+  for (int item = warp; owners; owners &= owners - 1, item -= Hkv) {
+    const int sl = __shfl_sync(0xffffffffu, slot, __ffs(owners) - 1);
+    const int64_t id = sl >> page_shift;
+    const int n = (sl & ((1 << page_shift) - 1)) + 1;
+    for (; item < Hkv; item += 8) {
+      const __nv_bfloat16* src = K + (((id * Hkv + item) << page_shift) * D) + sub * 8;
+      float acc[8] = {};
+      for (int r0 = 0; r0 < n; r0 += 8 * kRows) {
+        uint4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = r0 + k * kRows + row0;
+          x[k] = r < n ? *reinterpret_cast<const uint4*>(src + int64_t(r) * D) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[2 * e] += __uint_as_float(u[e] << 16);
+            acc[2 * e + 1] += __uint_as_float(u[e] & 0xFFFF0000u);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+#pragma unroll
+        for (int o = kLanes; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
+        acc[e] /= float(n);
+      }
+      if (row0 == 0)
+        *reinterpret_cast<uint4*>(ksum + (id * Hkv + item) * D + sub * 8) =
+            make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+                       pack_bf16x2(acc[6], acc[7]));
+    }
+  }
+}
+
+// ------------------------------------------------- an even share of ragged work
+// The work is a list of units (sequences, or rows of lists) of tiles(u) equal
+// tiles.  CTA c of C takes the tiles [c total / C, (c + 1) total / C) of the
+// whole list, whatever the units' lengths, so the load is even without the
+// host knowing any length.  Every CTA sums the units' tiles itself.
+struct Share {
+  int unit;       // first unit with work
+  int off;        // first tile in it
+  int n;          // tiles of this CTA
+  int64_t begin;  // position of the first tile in the whole list
+  int64_t total;  // tiles of the whole list
+};
+
+constexpr int kShareMaxUnits = 65536;
+constexpr int kShareSums = kShareMaxUnits / 32;  // 64-bit sums of 32 units each
+
+template <typename F>
+__device__ __forceinline__ Share share_work(F tiles, int n_units, int c, int C, int64_t* sums, Share* out) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int chunks = (n_units + 31) / 32;
+  auto warp_incl = [&](int64_t v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    return v;
+  };
+  for (int k = warp; k < chunks; k += warps) {
+    const int u = k * 32 + lane;
+    const int64_t v = warp_incl(u < n_units ? int64_t(tiles(u)) : 0);
+    if (lane == 31) sums[k] = v;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int64_t total = 0;
+    for (int k = lane; k < chunks; k += 32) total += sums[k];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    // total < 2^41 (2^16 units of at most 2^25 tiles) and C < 2^10
+    const int64_t b = total * c / C, e = total * (c + 1) / C;
+    Share r{0, 0, int(e - b), b, total};
+    int64_t base = 0;
+    int chunk = 0;
+    for (int k0 = 0; k0 < chunks; k0 += 32) {
+      const int64_t w = k0 + lane < chunks ? sums[k0 + lane] : 0;
+      const int64_t incl = warp_incl(w);
+      const uint32_t past = __ballot_sync(0xffffffffu, base + incl > b);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        chunk = k0 + l;
+        base += __shfl_sync(0xffffffffu, incl - w, l);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const int u = chunk * 32 + lane;
+    const int64_t w = u < n_units ? int64_t(tiles(u)) : 0;
+    const int64_t incl = warp_incl(w);
+    const uint32_t past = __ballot_sync(0xffffffffu, base + incl > b);
+    if (past) {  // none: b == total, no work
+      const int l = __ffs(past) - 1;
+      r.unit = chunk * 32 + l;
+      r.off = int(b - (base + __shfl_sync(0xffffffffu, incl - w, l)));
+    }
+    if (lane == 0) *out = r;
+  }
+  __syncthreads();
+  return *out;
+}
+
+// First unit from u on with tiles, n_units if there is none; whole warps, 32
+// units at a time.
+template <typename F>
+__device__ __forceinline__ int next_unit(F tiles, int n_units, int u) {
+  const int lane = threadIdx.x & 31;
+  for (; u < n_units; u += 32) {
+    const uint32_t some = __ballot_sync(0xffffffffu, u + lane < n_units && tiles(u + lane) > 0);
+    if (some) return u + __ffs(some) - 1;
+  }
+  return n_units;
+}
+
+// m16n8k16 bf16 product with fp32 accumulation.  The single-token kernels use
+// it instead of tcgen05: a key meets at most 16 queries, so they are bound by
+// the bytes of the keys, and operands straight from registers need neither a
+// 128-row tile nor a trip through TMEM.
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// ----------------------------------------------------------------- select
+// P[s, g, j] = (1/G) sum_h softmax_j(q_h . kbar_j / sqrt(d) + ln n_j): the
+// block-mass estimate of the selector with the group's G query heads in the
+// place of the clusters.  Two kernels: the scores (and each chunk's maximum
+// and sum of exponentials per head) go to the workspace, then every chunk is
+// normalised with the row's sums.
+//
+// Scores: a warp takes 32 pages of one head, four products of 8 pages, with
+// the summaries loaded straight into the products' registers: the order of
+// the d products is free, so lane (g, t) takes 16-byte pieces t, t + 4, ... of
+// page g's summary, and the query's registers follow the same order.
+constexpr int kSelPages = 128;    // pages per CTA and step: 32 per warp
+constexpr int kSelThreads = 128;
+
+struct SelectArgs {
+  PagedView v;
+  const __nv_bfloat16* Q;     // [T, Hq, d]
+  const __nv_bfloat16* ksum;  // [num_pages, Hkv, d]
+  float* scores;              // [S, Hkv, G, max_pages], log2 domain
+  float2* part;               // [S, Hkv, G, chunks]: maximum, sum of exp2
+  float* P;                   // [S, Hkv, max_pages]
+  int chunks;                 // ceil(max_pages / 128)
+  float scale_log2;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kSelThreads, 4) page_score_kernel(const SelectArgs a) {
+  constexpr int kPieces = D / 32;  // 16-byte pieces of a summary per lane
+  __shared__ int64_t sums[kShareSums / 8];
+  __shared__ Share share_out;
+  __shared__ float2 wpart[4][kMaxGroup];
+  const PagedView& v = a.v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  auto chunks_of = [&](int s) { return (pages_of(v, seq_len(v, s)) + kSelPages - 1) / kSelPages; };
+  auto tiles = [&](int s) { return query_row(v, s) < 0 ? 0 : chunks_of(s) * v.Hkv; };
+  const Share sh = share_work(tiles, v.S, blockIdx.x, gridDim.x, sums, &share_out);
+  int s = sh.unit, off = sh.off;
+  for (int left = sh.n; left > 0; --left, ++off) {
+    if (off >= tiles(s)) {
+      s = next_unit(tiles, v.S, s + 1);
+      off = 0;
+      if (s >= v.S) return;
+    }
+    const int len = seq_len(v, s), pages = pages_of(v, len);
+    const int hk = off % v.Hkv, chunk = off / v.Hkv;
+    const int j0 = chunk * kSelPages + warp * 32;
+    // query: rows g and g + 8 of the 16 x d operand, pieces in the keys' order
+    const __nv_bfloat16* q = a.Q + (int64_t(query_row(v, s)) * v.Hkv + hk) * v.G * D + t * 8;
+    uint4 qa[kPieces], qb[kPieces];
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      qa[p] = g < v.G ? __ldg(reinterpret_cast<const uint4*>(q + g * D + p * 32)) : make_uint4(0u, 0u, 0u, 0u);
+      qb[p] = g + 8 < v.G ? __ldg(reinterpret_cast<const uint4*>(q + (g + 8) * D + p * 32)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    uint4 kx[4][kPieces];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int j = j0 + n * 8 + g;
+      int id = -1;
+      if (j < pages) {
+        id = __ldg(v.table + int64_t(s) * v.max_pages + j);
+        if (id < 0 || id >= v.num_pages) {
+          raise_error(AB_ERR_CAPACITY);
+          id = -1;
+        }
+      }
+      const uint4* src = reinterpret_cast<const uint4*>(a.ksum + (int64_t(id) * v.Hkv + hk) * D + t * 8);
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) kx[n][p] = id >= 0 ? __ldg(src + p * 4) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float m[2] = {-INFINITY, -INFINITY}, x[4][4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      float c0[4] = {}, c1[4] = {};
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        mma_16816(c0, qa[p].x, qb[p].x, qa[p].y, qb[p].y, kx[n][p].x, kx[n][p].y);
+        mma_16816(c1, qa[p].z, qb[p].z, qa[p].w, qb[p].w, kx[n][p].z, kx[n][p].w);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + n * 8 + t * 2 + (e & 1);
+        const int keys = min(v.page, len - (j << v.page_shift));
+        // log2 of the number of keys: whole pages take the exact integer
+        const float bias = keys == v.page ? float(v.page_shift) : log2f(float(max(keys, 1)));
+        x[n][e] = j < pages ? fmaf(c0[e] + c1[e], a.scale_log2, bias) : -INFINITY;
+        m[e >> 1] = fmaxf(m[e >> 1], x[n][e]);
+      }
+    }
+    float l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 1));
+      m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 2));
+      const float ref = m[k] == -INFINITY ? 0.f : m[k];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) l[k] += exp2f(x[n][2 * k] - ref) + exp2f(x[n][2 * k + 1] - ref);
+      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+      if (t == 0) wpart[warp][g + 8 * k] = make_float2(m[k], l[k]);
+    }
+    const int64_t row = int64_t(s) * v.Hkv + hk;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int h = g + 8 * k;
+      if (h < v.G) {
+        float* dst = a.scores + (row * v.G + h) * v.max_pages;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int j = j0 + n * 8 + t * 2;
+          if (j < pages) dst[j] = x[n][2 * k];
+          if (j + 1 < pages) dst[j + 1] = x[n][2 * k + 1];
+        }
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < v.G) {
+      float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mm = fmaxf(mm, wpart[w][threadIdx.x].x);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 z = wpart[w][threadIdx.x];
+        ll += z.x == -INFINITY ? 0.f : z.y * exp2f(z.x - mm);
+      }
+      a.part[(row * v.G + threadIdx.x) * a.chunks + chunk] = make_float2(mm, ll);
+    }
+    __syncthreads();  // wpart is reused
+  }
+}
+
+// Normalisation: every CTA joins the row's partial sums, then turns 1024
+// pages' scores into P, at most 8 steps apart along the row.
+constexpr int kNormThreads = 256;
+
+__global__ void __launch_bounds__(kNormThreads) page_mass_kernel(const SelectArgs a) {
+  __shared__ float2 ml[kMaxGroup];  // maximum, 1 / (G sum)
+  const PagedView& v = a.v;
+  const int s = blockIdx.z, hk = blockIdx.y;
+  if (query_row(v, s) < 0) return;
+  const int pages = pages_of(v, seq_len(v, s));
+  if (int(blockIdx.x) * 4 * kNormThreads >= pages) return;
+  const int chunks = (pages + kSelPages - 1) / kSelPages;
+  const int64_t row = int64_t(s) * v.Hkv + hk;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int h = warp; h < v.G; h += kNormThreads / 32) {
+    const float2* part = a.part + (row * v.G + h) * a.chunks;
+    float m = -INFINITY, l = 0.f;
+    for (int k = lane; k < chunks; k += 32) {
+      const float2 z = part[k];
+      if (z.x > m) {
+        l *= exp2f(m - z.x);
+        m = z.x;
+      }
+      if (z.x != -INFINITY) l += z.y * exp2f(z.x - m);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float om = __shfl_xor_sync(0xffffffffu, m, o), ol = __shfl_xor_sync(0xffffffffu, l, o);
+      const float mm = fmaxf(m, om);
+      if (mm != -INFINITY) l = l * exp2f(m - mm) + ol * exp2f(om - mm);
+      m = mm;
+    }
+    if (lane == 0) ml[h] = make_float2(m, 1.f / (l * float(v.G)));
+  }
+  __syncthreads();
+  for (int j0 = blockIdx.x * 4 * kNormThreads; j0 < pages; j0 += gridDim.x * 4 * kNormThreads) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = j0 + k * kNormThreads + threadIdx.x;
+      if (j < pages) {
+        const float* src = a.scores + row * v.G * v.max_pages + j;
+        float p = 0.f;
+        for (int h = 0; h < v.G; ++h) p += exp2f(src[int64_t(h) * v.max_pages] - ml[h].x) * ml[h].y;
+        a.P[row * v.max_pages + j] = p;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- top-k
+// The newest min(recent, Kb) pages and the Kb minus that many others of
+// largest P, in ascending order; ties go to the lower page.  Keys are P's bits
+// (P >= 0 orders as its bits; anything else counts as 0), the newest pages get
+// the largest key.  One CTA per row: a radix select over four digits of 8
+// bits, then one ordered pass.
+struct TopkArgs {
+  const float* P;
+  const int32_t* lens;
+  int32_t *idx, *count;
+  int Hkv, page, page_shift, max_pages, recent;
+  double keep;
+};
+constexpr int kTopkThreads = 256;
+
+__device__ __forceinline__ int page_budget(int n, double keep) {
+  const double kb = floor(keep * double(n) + 0.5);
+  return kb < 1.0 ? min(1, n) : kb > double(n) ? n : int(kb);
+}
+
+__global__ void __launch_bounds__(kTopkThreads) page_topk_kernel(const TopkArgs a) {
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t sel[2];
+  __shared__ uint32_t scan[8];
+  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int len = __ldg(a.lens + row / a.Hkv);
+  if (len < 0 || len > a.max_pages << a.page_shift) {
+    if (tid == 0) raise_error(AB_ERR_CAPACITY);
+    len = 0;
+  }
+  const int n = (len + a.page - 1) >> a.page_shift;
+  const int Kb = page_budget(n, a.keep);
+  if (tid == 0) a.count[row] = Kb;
+  if (n == 0) return;
+  const int newest = n - min(a.recent, Kb);  // pages from here on are kept
+  const float* P = a.P + int64_t(row) * a.max_pages;
+  auto key_of = [&](int j) -> uint32_t {
+    const float p = __ldg(P + j);
+    return j >= newest ? 0xFFFFFFFFu : p > 0.f ? __float_as_uint(p) : 0u;
+  };
+  uint32_t prefix = 0, pmask = 0, need = uint32_t(Kb);
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    hist[tid] = 0;
+    __syncthreads();
+    for (int j = tid; j < n; j += kTopkThreads) {
+      const uint32_t k = key_of(j);
+      if ((k & pmask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+    }
+    __syncthreads();
+    if (warp == 0) {  // lane l: bins 255 - 8 l down to 248 - 8 l
+      uint32_t c[8], tot = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        c[k] = hist[255 - 8 * lane - k];
+        tot += c[k];
+      }
+      uint32_t incl = tot;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      uint32_t above = incl - tot;
+      if (above < need && need <= incl) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (above < need && need <= above + c[k]) {
+            sel[0] = uint32_t(255 - 8 * lane - k);
+            sel[1] = need - above;
+          }
+          above += c[k];
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= sel[0] << shift;
+    pmask |= 0xFFu << shift;
+    need = sel[1];
+  }
+  // kept: keys above the threshold, and the lowest `need` pages of those equal to it
+  int32_t* out = a.idx + int64_t(row) * a.max_pages;
+  uint32_t base_gt = 0, base_eq = 0;
+  for (int c0 = 0; c0 < n; c0 += 4 * kTopkThreads) {
+    const int j0 = c0 + 4 * tid;
+    uint32_t gt = 0, eq = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (j0 + q < n) {
+        const uint32_t k = key_of(j0 + q);
+        gt |= (k > prefix ? 1u : 0u) << q;
+        eq |= (k == prefix ? 1u : 0u) << q;
+      }
+    }
+    const uint32_t mine = uint32_t(__popc(gt)) | (uint32_t(__popc(eq)) << 16);
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    __syncthreads();  // scan[] may still be read for the chunk before
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    uint32_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    const uint32_t excl = before + incl - mine;
+    uint32_t n_gt = base_gt + (excl & 0xFFFFu), n_eq = base_eq + (excl >> 16);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool is_gt = (gt >> q) & 1u, is_eq = (eq >> q) & 1u;
+      if (is_gt || (is_eq && n_eq < need)) out[n_gt + min(n_eq, need)] = j0 + q;
+      n_gt += is_gt ? 1u : 0u;
+      n_eq += is_eq ? 1u : 0u;
+    }
+    base_gt += total & 0xFFFFu;
+    base_eq += total >> 16;
+  }
+}
+
+}  // namespace ab

@@ -1,0 +1,454 @@
+// C ABI of the norm and rotation and of the paged cache (declared in
+// include/ab.h): argument checks, workspace layout, launches.  Included by
+// ab_api.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+int log2_of(int x) {
+  int k = 0;
+  while ((1 << k) < x) ++k;
+  return k;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    return 0;
+  return n;
+}
+
+// ------------------------------------------------------ norm and rotation
+ab_status check_norm_rope(const ab_norm_rope* nr) {
+  if (!nr) return AB_ERR_INVALID_ARG;
+  if (nr->norm < 0 || nr->norm > 2 || (nr->interleaved != 0 && nr->interleaved != 1)) return AB_ERR_INVALID_ARG;
+  if (!(nr->eps >= 0.f) || nr->n_pos < 0) return AB_ERR_INVALID_ARG;
+  if ((nr->cos_table == nullptr) != (nr->sin_table == nullptr)) return AB_ERR_INVALID_ARG;
+  const void* ptrs[] = {nr->wq, nr->wk, nr->cos_table, nr->sin_table};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return AB_ERR_INVALID_ARG;
+  return AB_OK;
+}
+
+// Strides keep every head row 16-byte aligned; a stride of a dimension of
+// size 1 is never used.
+ab_status check_tokens(const ab_tokens* x, int64_t nb, int64_t nt, int64_t nh) {
+  if (!x || !x->ptr || !aligned16(x->ptr)) return AB_ERR_INVALID_ARG;
+  if ((nb > 1 && x->batch % 8 != 0) || (nt > 1 && x->token % 8 != 0) || (nh > 1 && x->head % 8 != 0))
+    return AB_ERR_INVALID_ARG;
+  return AB_OK;
+}
+
+TokenView view_of(const ab_tokens* x) {
+  return TokenView{static_cast<const __nv_bfloat16*>(x->ptr), x->batch, x->token, x->head};
+}
+
+// Head rows that one CTA can hold: 16 warps of 32 / (d/8) rows, 8 rows a lane.
+int rope_max_heads(int d) { return 16 * (256 / d) * kRopeVecs; }
+
+ab_status launch_norm_rope(const NormRopeArgs& a, int d, const ab_norm_rope* nr, int64_t blocks, cudaStream_t st) {
+  int heads = 0;
+  for (int k = 0; k < 3; ++k)
+    if (a.in[k].ptr) heads = a.heads[k] > heads ? a.heads[k] : heads;
+  // four head rows a lane, as far as 16 warps reach
+  const int per_warp = 4 * (256 / d);
+  int warps = (heads + per_warp - 1) / per_warp;
+  warps = warps > 16 ? 16 : warps;
+  auto go = [&](auto kern) -> ab_status {
+    kern<<<unsigned(blocks), unsigned(32 * warps), 0, st>>>(a);
+    return launch_status();
+  };
+  auto by_norm = [&](auto dd, auto il) -> ab_status {
+    constexpr int D = decltype(dd)::value;
+    constexpr bool I = decltype(il)::value;
+    switch (nr->norm) {
+      case kNormNone: return go(norm_rope_kernel<D, kNormNone, I>);
+      case kNormHead: return go(norm_rope_kernel<D, kNormHead, I>);
+      default: return go(norm_rope_kernel<D, kNormToken, I>);
+    }
+  };
+  using T128 = std::integral_constant<int, 128>;
+  using T64 = std::integral_constant<int, 64>;
+  if (d == 128) return nr->interleaved ? by_norm(T128{}, std::true_type{}) : by_norm(T128{}, std::false_type{});
+  return nr->interleaved ? by_norm(T64{}, std::true_type{}) : by_norm(T64{}, std::false_type{});
+}
+
+void set_norm_rope(NormRopeArgs* a, const ab_norm_rope* nr) {
+  a->w[0] = nr->norm ? nr->wq : nullptr;
+  a->w[1] = nr->norm ? nr->wk : nullptr;
+  a->cos_t = nr->cos_table;
+  a->sin_t = nr->sin_table;
+  a->n_pos = nr->n_pos;
+  a->eps = nr->eps;
+}
+
+// Arguments of the dense call; the launch's blocks in *blocks.
+ab_status prepare_norm_rope(const Dims& d, const ab_norm_rope* nr, const ab_tokens* q, const ab_tokens* k,
+                            const ab_tokens* v, const int32_t* pos_q, const int32_t* pos_k, void* Q, void* K, void* V,
+                            NormRopeArgs* a, int64_t* blocks) {
+  const ab_status s = check_norm_rope(nr);
+  if (s != AB_OK) return s;
+  if (!q && !k && !v) return AB_ERR_INVALID_ARG;
+  const ab_tokens* in[3] = {q, k, v};
+  void* out[3] = {Q, K, V};
+  const int32_t* pos[2] = {pos_q, pos_k};
+  *a = NormRopeArgs{};
+  int64_t n = 0;
+  for (int x = 0; x < 3; ++x) {
+    const int len = x == 0 ? d.L : d.Lk;
+    a->first_block[x] = int(n);
+    a->heads[x] = d.H;
+    a->len[x] = len;
+    if (!in[x]) continue;
+    if (check_tokens(in[x], d.B, len, d.H) != AB_OK || !out[x] || !aligned16(out[x])) return AB_ERR_INVALID_ARG;
+    if (x < 2) {
+      if (pos[x] && !aligned16(pos[x])) return AB_ERR_INVALID_ARG;
+      if (nr->cos_table && !pos[x] && len > nr->n_pos) return AB_ERR_INVALID_ARG;
+      a->pos[x] = pos[x];
+    }
+    a->in[x] = view_of(in[x]);
+    a->out[x] = static_cast<__nv_bfloat16*>(out[x]);
+    n += int64_t(d.B) * len;
+    if (n > INT_MAX) return AB_ERR_UNSUPPORTED;
+  }
+  // a tensor that is left out has no CTAs: the next one begins where it would
+  if (d.H > rope_max_heads(d.d)) return AB_ERR_UNSUPPORTED;
+  set_norm_rope(a, nr);
+  *blocks = n;
+  return AB_OK;
+}
+
+// ---------------------------------------------------------- the paged cache
+ab_status check_paged(const ab_paged_params* p) {
+  if (!p) return AB_ERR_INVALID_ARG;
+  if (p->S < 1 || p->Hq < 1 || p->Hkv < 1 || p->num_pages < 1 || p->max_pages < 1 || p->recent < 0)
+    return AB_ERR_INVALID_ARG;
+  if (p->Hq % p->Hkv != 0) return AB_ERR_INVALID_ARG;
+  if (!(p->keep_ratio > 0.f) || !(p->keep_ratio <= 1.f)) return AB_ERR_INVALID_ARG;
+  if (p->d != 64 && p->d != 128) return p->d > 0 ? AB_ERR_UNSUPPORTED : AB_ERR_INVALID_ARG;
+  if (p->page != 16 && p->page != 32 && p->page != 64) return p->page > 0 ? AB_ERR_UNSUPPORTED : AB_ERR_INVALID_ARG;
+  if (int64_t(p->max_pages) * p->page > (int64_t(1) << 24)) return AB_ERR_INVALID_ARG;
+  if (int64_t(p->num_pages) * p->page > INT_MAX || int64_t(p->num_pages) * p->Hkv > INT_MAX) return AB_ERR_INVALID_ARG;
+  if (p->S > kMaxSeqs || p->Hq / p->Hkv > kMaxGroup || int64_t(p->S) * p->Hkv > kShareMaxUnits)
+    return AB_ERR_UNSUPPORTED;
+  return AB_OK;
+}
+
+bool any_bad(std::initializer_list<const void*> ptrs) {
+  for (const void* q : ptrs)
+    if (!q || !aligned16(q)) return true;
+  return false;
+}
+
+PagedView paged_view(const ab_paged_params* p, const int32_t* table, const int32_t* lens, const int32_t* cu_new, int T) {
+  PagedView v{};
+  v.table = table; v.lens = lens; v.cu_new = cu_new; v.T = T;
+  v.S = p->S; v.Hkv = p->Hkv; v.G = p->Hq / p->Hkv;
+  v.page = p->page; v.page_shift = log2_of(p->page); v.num_pages = p->num_pages; v.max_pages = p->max_pages;
+  return v;
+}
+
+struct PagedWorkspace {
+  size_t off_scores, off_part;                     // select
+  size_t off_meta, off_part_o, off_ml;  // attention (its first bytes: the number of tiles)
+  size_t select, attend;                // bytes of each
+};
+
+PagedWorkspace paged_workspace(const ab_paged_params* p) {
+  PagedWorkspace w{};
+  const size_t rows = size_t(p->S) * p->Hq;
+  const size_t chunks = (size_t(p->max_pages) + kSelPages - 1) / kSelPages;
+  w.off_part = align256(w.off_scores + rows * p->max_pages * 4);
+  w.select = align256(w.off_part + rows * chunks * 8);
+  const size_t heads = p->Hq / p->Hkv > 8 ? 16 : 8;
+  w.off_meta = 256;
+  w.off_part_o = align256(w.off_meta + kDecMaxParts * sizeof(DecMeta));
+  w.off_ml = align256(w.off_part_o + size_t(kDecMaxParts) * 2 * heads * p->d * 4);
+  w.attend = align256(w.off_ml + size_t(kDecMaxParts) * 2 * heads * 8);
+  return w;
+}
+
+// Rows of Q: with cu_new the tokens' rows, else one row per sequence.
+ab_status check_rows(const ab_paged_params* p, const int32_t* cu_new, int32_t T) {
+  if (cu_new ? (!aligned16(cu_new) || T < 1) : T != p->S) return AB_ERR_INVALID_ARG;
+  return AB_OK;
+}
+
+ab_status prepare_append(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T, const ab_tokens* q,
+                         const ab_tokens* k, const ab_tokens* v, const int32_t* slots, const int32_t* positions,
+                         void* Q, void* Kc, void* Vc, void* ksum, NormRopeArgs* a) {
+  ab_status s = check_norm_rope(nr);
+  if (s != AB_OK) return s;
+  if (T < 1) return AB_ERR_INVALID_ARG;
+  if (any_bad({slots, positions, Q, Kc, Vc}) || !aligned16(ksum)) return AB_ERR_INVALID_ARG;
+  if (T > INT_MAX / 3 || p->Hq > rope_max_heads(p->d)) return AB_ERR_UNSUPPORTED;
+  const ab_tokens* in[3] = {q, k, v};
+  void* out[3] = {Q, Kc, Vc};
+  *a = NormRopeArgs{};
+  for (int x = 0; x < 3; ++x) {
+    a->heads[x] = x == 0 ? p->Hq : p->Hkv;
+    if (check_tokens(in[x], 1, T, a->heads[x]) != AB_OK) return AB_ERR_INVALID_ARG;
+    a->len[x] = T;
+    a->first_block[x] = x * T;
+    a->in[x] = view_of(in[x]);
+    a->out[x] = static_cast<__nv_bfloat16*>(out[x]);
+  }
+  a->pos[0] = a->pos[1] = positions;
+  a->slots = slots;
+  a->page_shift = log2_of(p->page);
+  a->num_pages = p->num_pages;
+  set_norm_rope(a, nr);
+  return AB_OK;
+}
+
+ab_status run_append(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T, const NormRopeArgs& a, void* Kc,
+                     void* ksum, cudaStream_t st) {
+  ab_status s = launch_norm_rope(a, p->d, nr, int64_t(3) * T, st);
+  if (s != AB_OK || !ksum) return s;
+  // a CTA looks at 1 to 32 slots: few where there are few, so that pages spread over the SMs
+  int per_cta = (T + 1183) / 1184;
+  per_cta = per_cta > 32 ? 32 : per_cta;
+  const unsigned grid = unsigned((T + per_cta - 1) / per_cta);
+  const auto* kc = static_cast<const __nv_bfloat16*>(Kc);
+  auto* ks = static_cast<__nv_bfloat16*>(ksum);
+  if (p->d == 128)
+    page_sum_kernel<128><<<grid, 256, 0, st>>>(a.slots, T, per_cta, kc, ks, p->Hkv, a.page_shift, a.num_pages);
+  else
+    page_sum_kernel<64><<<grid, 256, 0, st>>>(a.slots, T, per_cta, kc, ks, p->Hkv, a.page_shift, a.num_pages);
+  return launch_status();
+}
+
+ab_status run_paged_select(const ab_paged_params* p, const PagedView& v, const void* Q, const void* ksum, float* P,
+                           uint8_t* ws, cudaStream_t st) {
+  const PagedWorkspace w = paged_workspace(p);
+  SelectArgs a{};
+  a.v = v;
+  a.Q = static_cast<const __nv_bfloat16*>(Q);
+  a.ksum = static_cast<const __nv_bfloat16*>(ksum);
+  a.scores = reinterpret_cast<float*>(ws + w.off_scores);
+  a.part = reinterpret_cast<float2*>(ws + w.off_part);
+  a.P = P;
+  a.chunks = (p->max_pages + kSelPages - 1) / kSelPages;
+  a.scale_log2 = float(1.4426950408889634 / std::sqrt(double(p->d)));
+  const int sms = sm_count();
+  if (!sms) return AB_ERR_CUDA;
+  const int64_t most = int64_t(p->S) * p->Hkv * a.chunks;
+  const unsigned grid = unsigned(most < sms * 4 ? most : sms * 4);
+  if (p->d == 128) page_score_kernel<128><<<grid, kSelThreads, 0, st>>>(a);
+  else page_score_kernel<64><<<grid, kSelThreads, 0, st>>>(a);
+  if (launch_status() != AB_OK) return AB_ERR_CUDA;
+  int steps = (p->max_pages + 4 * kNormThreads - 1) / (4 * kNormThreads);
+  steps = steps > 8 ? 8 : steps;
+  page_mass_kernel<<<dim3(unsigned(steps), unsigned(p->Hkv), unsigned(p->S)), kNormThreads, 0, st>>>(a);
+  return launch_status();
+}
+
+ab_status run_paged_topk(const ab_paged_params* p, const float* P, const int32_t* lens, int32_t* idx, int32_t* count,
+                         cudaStream_t st) {
+  TopkArgs a{};
+  a.P = P; a.lens = lens; a.idx = idx; a.count = count;
+  a.Hkv = p->Hkv; a.page = p->page; a.page_shift = log2_of(p->page); a.max_pages = p->max_pages;
+  a.recent = p->recent; a.keep = double(p->keep_ratio);
+  page_topk_kernel<<<unsigned(p->S * p->Hkv), kTopkThreads, 0, st>>>(a);
+  return launch_status();
+}
+
+template <int D, int RB, bool kLists>
+ab_status launch_paged_attention(const DecArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int grid,
+                                 cudaStream_t st) {
+  auto kern = paged_attention_kernel<D, RB, kLists>;
+  constexpr int smem = DecSmem<D, RB>::kAlloc;
+  if (set_smem(kern, smem) != cudaSuccess) return AB_ERR_CUDA;
+  kern<<<unsigned(grid), kDecThreads, smem, st>>>(tmK, tmV, a);
+  if (launch_status() != AB_OK) return AB_ERR_CUDA;
+  if (grid > 1) {
+    paged_join_kernel<D><<<dim3(unsigned(grid - 1), unsigned(a.v.G)), D * kJoinGroups, 0, st>>>(a, grid, RB * 8);
+    return launch_status();
+  }
+  return AB_OK;
+}
+
+ab_status run_paged_attention(const ab_paged_params* p, const PagedView& v, const void* Q, const void* Kc,
+                              const void* Vc, const int32_t* idx, const int32_t* count, void* O, uint8_t* ws,
+                              cudaStream_t st) {
+  const PagedWorkspace w = paged_workspace(p);
+  CUtensorMap tmK, tmV;
+  const uint64_t rows = uint64_t(p->num_pages) * p->Hkv;
+  if (!make_map_grouped(&tmK, Kc, uint64_t(p->d), uint64_t(p->page), rows, uint32_t(p->page / 8))) return AB_ERR_CUDA;
+  if (!make_map_grouped(&tmV, Vc, uint64_t(p->d), uint64_t(p->page), rows, uint32_t(p->page / 8))) return AB_ERR_CUDA;
+  const int sms = sm_count();
+  if (!sms) return AB_ERR_CUDA;
+  DecArgs a{};
+  a.v = v;
+  a.Q = static_cast<const __nv_bfloat16*>(Q);
+  a.idx = idx;
+  a.count = count;
+  a.O = static_cast<__nv_bfloat16*>(O);
+  a.scale_log2 = float(1.4426950408889634 / std::sqrt(double(p->d)));
+  a.total = reinterpret_cast<int64_t*>(ws);
+  a.meta = reinterpret_cast<DecMeta*>(ws + w.off_meta);
+  a.part_o = reinterpret_cast<float*>(ws + w.off_part_o);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.off_ml);
+  const int grid = sms < kDecMaxParts ? sms : kDecMaxParts;
+  auto by_lists = [&](auto dd, auto rb) -> ab_status {
+    constexpr int D = decltype(dd)::value, RB = decltype(rb)::value;
+    return idx ? launch_paged_attention<D, RB, true>(a, tmK, tmV, grid, st)
+               : launch_paged_attention<D, RB, false>(a, tmK, tmV, grid, st);
+  };
+  using T128 = std::integral_constant<int, 128>;
+  using T64 = std::integral_constant<int, 64>;
+  using R1 = std::integral_constant<int, 1>;
+  using R2 = std::integral_constant<int, 2>;
+  if (p->d == 128) return v.G <= 8 ? by_lists(T128{}, R1{}) : by_lists(T128{}, R2{});
+  return v.G <= 8 ? by_lists(T64{}, R1{}) : by_lists(T64{}, R2{});
+}
+
+}  // namespace
+
+extern "C" {
+
+ab_status ab_qk_norm_rope(const ab_params* p, const ab_norm_rope* nr, const ab_tokens* q, const ab_tokens* k,
+                          const ab_tokens* v, const int32_t* pos_q, const int32_t* pos_k, void* Q, void* K, void* V,
+                          void* stream) {
+  Dims d;
+  NvtxRange nvtx("ab_qk_norm_rope");
+  ab_status s = check_params(p, false, &d);
+  if (s != AB_OK) return s;
+  NormRopeArgs a;
+  int64_t blocks = 0;
+  s = prepare_norm_rope(d, nr, q, k, v, pos_q, pos_k, Q, K, V, &a, &blocks);
+  if (s != AB_OK) return s;
+  return launch_norm_rope(a, d.d, nr, blocks, static_cast<cudaStream_t>(stream));
+}
+
+ab_status ab_forward_qkv(const ab_params* p, const ab_norm_rope* nr, const ab_tokens* q, const ab_tokens* k,
+                         const ab_tokens* v, const int32_t* pos_q, const int32_t* pos_k, void* Q, void* K, void* V,
+                         float* P, int32_t* idx, uint32_t* pi_q32, int32_t* count, void* O, void* workspace,
+                         size_t ws_bytes, void* stream) {
+  Dims d;
+  NvtxRange nvtx("ab_forward_qkv");
+  ab_status s = check_params(p, true, &d);
+  if (s != AB_OK) return s;
+  if (!q || !k || !v) return AB_ERR_INVALID_ARG;
+  s = check_path_args(Q, K, V, P, idx, pi_q32, count, O, workspace, ws_bytes, workspace_layout(d).total);
+  if (s != AB_OK) return s;
+  NormRopeArgs a;
+  int64_t blocks = 0;
+  s = prepare_norm_rope(d, nr, q, k, v, pos_q, pos_k, Q, K, V, &a, &blocks);
+  if (s != AB_OK) return s;
+  s = launch_norm_rope(a, d.d, nr, blocks, static_cast<cudaStream_t>(stream));
+  if (s != AB_OK) return s;
+  return ab_forward(p, Q, K, V, P, idx, pi_q32, count, O, workspace, ws_bytes, stream);
+}
+
+ab_status ab_paged_workspace_size(const ab_paged_params* p, int32_t with_select, size_t* bytes) {
+  const ab_status s = check_paged(p);
+  if (s != AB_OK) return s;
+  if (!bytes) return AB_ERR_INVALID_ARG;
+  const PagedWorkspace w = paged_workspace(p);
+  *bytes = with_select && w.select > w.attend ? w.select : w.attend;
+  return AB_OK;
+}
+
+ab_status ab_paged_plan(const ab_paged_params* p, int32_t T, const int32_t* n_new, const int32_t* lens,
+                        int32_t* lens_out, int32_t* table, int32_t* free_pages, const int32_t* free_count,
+                        int32_t* free_count_out, int32_t* cu_new, int32_t* slots, int32_t* positions, void* stream) {
+  NvtxRange nvtx("ab_paged_plan");
+  const ab_status s = check_paged(p);
+  if (s != AB_OK) return s;
+  if (T < 0) return AB_ERR_INVALID_ARG;
+  if (any_bad({n_new, lens, lens_out, table, free_pages, free_count, free_count_out, cu_new})) return AB_ERR_INVALID_ARG;
+  if (T > 0 && any_bad({slots, positions})) return AB_ERR_INVALID_ARG;
+  PlanArgs a{};
+  a.S = p->S; a.T = T; a.page = p->page; a.page_shift = log2_of(p->page);
+  a.num_pages = p->num_pages; a.max_pages = p->max_pages;
+  a.n_new = n_new; a.lens = lens; a.lens_out = lens_out; a.table = table; a.free_pages = free_pages;
+  a.free_count = free_count; a.free_count_out = free_count_out;
+  a.cu_new = cu_new; a.slots = slots; a.positions = positions;
+  const int smem = (4 * p->S + 3) * 4;
+  if (smem > 40 * 1024 && set_smem(plan_kernel, smem) != cudaSuccess) return AB_ERR_CUDA;
+  plan_kernel<<<kPlanCtas, kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
+  return launch_status();
+}
+
+ab_status ab_paged_append(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T, const ab_tokens* q,
+                          const ab_tokens* k, const ab_tokens* v, const int32_t* slots, const int32_t* positions,
+                          void* Q, void* K, void* V, void* ksum, void* stream) {
+  NvtxRange nvtx("ab_paged_append");
+  ab_status s = check_paged(p);
+  if (s != AB_OK) return s;
+  if (T == 0) return check_norm_rope(nr);  // nothing to write
+  NormRopeArgs a;
+  s = prepare_append(p, nr, T, q, k, v, slots, positions, Q, K, V, ksum, &a);
+  if (s != AB_OK) return s;
+  return run_append(p, nr, T, a, K, ksum, static_cast<cudaStream_t>(stream));
+}
+
+ab_status ab_paged_select(const ab_paged_params* p, int32_t T, const void* Q, const void* ksum, const int32_t* table,
+                          const int32_t* lens, const int32_t* cu_new, float* P, void* workspace, size_t ws_bytes,
+                          void* stream) {
+  NvtxRange nvtx("ab_paged_select");
+  ab_status s = check_paged(p);
+  if (s != AB_OK) return s;
+  if (any_bad({Q, ksum, table, lens, P, workspace})) return AB_ERR_INVALID_ARG;
+  s = check_rows(p, cu_new, T);
+  if (s != AB_OK) return s;
+  if (ws_bytes < paged_workspace(p).select) return AB_ERR_WORKSPACE;
+  return run_paged_select(p, paged_view(p, table, lens, cu_new, T), Q, ksum, P, static_cast<uint8_t*>(workspace),
+                          static_cast<cudaStream_t>(stream));
+}
+
+ab_status ab_paged_topk(const ab_paged_params* p, const float* P, const int32_t* lens, int32_t* idx, int32_t* count,
+                        void* stream) {
+  NvtxRange nvtx("ab_paged_topk");
+  const ab_status s = check_paged(p);
+  if (s != AB_OK) return s;
+  if (any_bad({P, lens, idx, count})) return AB_ERR_INVALID_ARG;
+  return run_paged_topk(p, P, lens, idx, count, static_cast<cudaStream_t>(stream));
+}
+
+ab_status ab_attention_paged(const ab_paged_params* p, int32_t T, const void* Q, const void* K, const void* V,
+                             const int32_t* table, const int32_t* lens, const int32_t* cu_new, const int32_t* idx,
+                             const int32_t* count, void* O, void* workspace, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("ab_attention_paged");
+  ab_status s = check_paged(p);
+  if (s != AB_OK) return s;
+  if (any_bad({Q, K, V, table, lens, O, workspace})) return AB_ERR_INVALID_ARG;
+  if ((idx == nullptr) != (count == nullptr) || !aligned16(idx) || !aligned16(count)) return AB_ERR_INVALID_ARG;
+  s = check_rows(p, cu_new, T);
+  if (s != AB_OK) return s;
+  if (ws_bytes < paged_workspace(p).attend) return AB_ERR_WORKSPACE;
+  return run_paged_attention(p, paged_view(p, table, lens, cu_new, T), Q, K, V, idx, count, O,
+                             static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream));
+}
+
+ab_status ab_paged_forward(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T, const ab_tokens* q,
+                           const ab_tokens* k, const ab_tokens* v, const int32_t* slots, const int32_t* positions,
+                           const int32_t* table, const int32_t* lens, const int32_t* cu_new, void* Q, void* K, void* V,
+                           void* ksum, float* P, int32_t* idx, int32_t* count, void* O, void* workspace,
+                           size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("ab_paged_forward");
+  ab_status s = check_paged(p);
+  if (s != AB_OK) return s;
+  if (any_bad({table, lens, cu_new, ksum, P, idx, count, O, workspace})) return AB_ERR_INVALID_ARG;
+  NormRopeArgs a;
+  s = prepare_append(p, nr, T, q, k, v, slots, positions, Q, K, V, ksum, &a);
+  if (s != AB_OK) return s;
+  s = check_rows(p, cu_new, T);
+  if (s != AB_OK) return s;
+  const PagedWorkspace w = paged_workspace(p);
+  if (ws_bytes < w.select || ws_bytes < w.attend) return AB_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const PagedView view = paged_view(p, table, lens, cu_new, T);
+  s = run_append(p, nr, T, a, K, ksum, st);
+  if (s != AB_OK) return s;
+  s = run_paged_select(p, view, Q, ksum, P, ws, st);
+  if (s != AB_OK) return s;
+  s = run_paged_topk(p, P, lens, idx, count, st);
+  if (s != AB_OK) return s;
+  return run_paged_attention(p, view, Q, K, V, idx, count, O, ws, st);
+}
+
+}  // extern "C"

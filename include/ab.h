@@ -317,6 +317,204 @@ ab_status ab_forward_host(const ab_params* p, const void* Q_host, const void* K_
 ab_status ab_select_static(const ab_params* p, const void* Q, const void* K, float* P, float* centroids,
                            int32_t* counts, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Norm and rotation of queries and keys
+ * ------------------------------------------------------------------------
+ * The step between the projections and attention: an RMS norm of queries and
+ * keys and the position rotation, in one pass from the projections' layout
+ * (tokens outermost) to the one that attention reads.  For the values x of one
+ * head of one token, computed in fp32 and rounded to bfloat16 once:
+ *   norm 0: y = x
+ *   norm 1: y_i = x_i w_i / sqrt(mean over the head's d values of x^2 + eps)
+ *   norm 2: the mean runs over all heads of the token, w has a row per head
+ *   rotation by the token's position, table row pos, for the pairs
+ *   (a, b) = (y_2i, y_2i+1) (interleaved) or (y_i, y_i+d/2):
+ *     (a cos_i - b sin_i, a sin_i + b cos_i)
+ * Any mapping of positions to angles (one axis, or (t, y, x) of a video) is a
+ * choice of the tables' rows.
+ */
+typedef struct {
+  int32_t norm;           /* 0, 1 or 2 */
+  int32_t interleaved;    /* 0 or 1 */
+  float eps;              /* >= 0 */
+  int32_t n_pos;          /* rows of the tables */
+  const float* wq;        /* device, weights of the queries' norm: [d] (norm 1), [heads, d] (norm 2); NULL: ones */
+  const float* wk;        /* the keys' */
+  const float* cos_table; /* device, [n_pos, d/2]; both tables NULL: no rotation */
+  const float* sin_table;
+} ab_norm_rope;
+
+/* Tokens in the projections' layout: value i of head h of token t of batch
+ * element b is ptr[b * batch + t * token + h * head + i], bfloat16.  ptr is
+ * 16-byte aligned and the strides are multiples of 8 elements (those of
+ * dimensions of size 1 are not used). */
+typedef struct {
+  const void* ptr;
+  int64_t batch, token, head;
+} ab_tokens;
+
+/*
+ * Norm and rotation into the layout of ab_forward.  Uses B, H, L, L_kv and d
+ * of *p.  q has L tokens, k and v have Lk; v is only moved.  Each of q, k, v
+ * may be NULL, its output is then not used.
+ *   pos_q, pos_k  device, int32 [B, L], [B, Lk]; NULL: token t has position t
+ *                 (then n_pos >= L, Lk).  A position outside [0, n_pos) raises
+ *                 AB_ERR_CAPACITY on the device, and its token's row of Q or K
+ *                 is left as it was.
+ *   Q, K, V       device, out, [B, H, L, d], [B, H, Lk, d] bf16; they must not
+ *                 overlap the inputs.
+ * AB_ERR_UNSUPPORTED for more than 256 heads (d 128) or 512 (d 64).
+ */
+ab_status ab_qk_norm_rope(const ab_params* p, const ab_norm_rope* nr, const ab_tokens* q, const ab_tokens* k,
+                          const ab_tokens* v, const int32_t* pos_q, const int32_t* pos_k, void* Q, void* K, void* V,
+                          void* stream);
+
+/*
+ * ab_qk_norm_rope followed by ab_forward: the path from the projections.  Q,
+ * K, V are buffers that receive the rotated tensors; everything else as for
+ * those two calls, all arguments checked before the first step is enqueued.
+ */
+ab_status ab_forward_qkv(const ab_params* p, const ab_norm_rope* nr, const ab_tokens* q, const ab_tokens* k,
+                         const ab_tokens* v, const int32_t* pos_q, const int32_t* pos_k, void* Q, void* K, void* V,
+                         float* P, int32_t* idx, uint32_t* pi_q32, int32_t* count, void* O, void* workspace,
+                         size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A paged key-value cache
+ * ------------------------------------------------------------------------
+ * For models that produce their sequences step by step.  The cache holds
+ * num_pages pages of `page` tokens, shared by S sequences:
+ *   K, V    device, [num_pages, Hkv, page, d] bf16
+ *   ksum    device, [num_pages, Hkv, d] bf16: mean of each page's keys
+ *   table   device, int32 [S, max_pages]: page of the j-th `page` tokens of
+ *           sequence s, j < ceil(lens[s] / page); the rest is not read
+ *   lens    device, int32 [S]: tokens of each sequence in the cache
+ * Several sequences may share pages.  A slot is page id * page + offset.
+ * Sequence lengths live on the device: no call needs them on the host, and
+ * every call can be captured in a CUDA graph and replayed for other lengths.
+ * Where a call takes cu_new (device, int32 [S + 1], as ab_paged_plan writes
+ * it), sequence s's query is row cu_new[s + 1] - 1 of Q [T, Hq, d], its newest
+ * token, and a sequence without new tokens is skipped; with cu_new NULL its
+ * query is row s and T must be S.
+ * Entries out of range (a length, a table or list entry, a count, a slot, a
+ * position) raise AB_ERR_CAPACITY on the device and their work is skipped.
+ */
+typedef struct {
+  int32_t S;          /* sequences, 1..8192; S * Hkv <= 65536 */
+  int32_t Hq, Hkv, d; /* query heads, key/value heads (Hq = G Hkv, G <= 16), head dim 64 or 128 */
+  int32_t page;       /* tokens per page: 16, 32 or 64 */
+  int32_t num_pages;  /* num_pages * page and num_pages * Hkv < 2^31 */
+  int32_t max_pages;  /* pages a sequence can have; max_pages * page <= 2^24 */
+  int32_t recent;     /* newest pages that ab_paged_topk always keeps, >= 0 */
+  float keep_ratio;   /* fraction of a sequence's pages that it keeps, in (0, 1] */
+} ab_paged_params;
+
+/* Bytes of device workspace ab_attention_paged needs, or (with_select not 0)
+ * that also suffices for ab_paged_select and ab_paged_forward.  Contents need
+ * no initialisation.  Calls that overlap on the GPU need workspaces of their
+ * own. */
+ab_status ab_paged_workspace_size(const ab_paged_params* p, int32_t with_select, size_t* bytes);
+
+/*
+ * Block tables and slot maps of one step from the requests' lengths.
+ * Sequence s has lens[s] tokens and gets n_new[s] more; n_new[s] = -1 says that
+ * it has ended.  The pages of ended sequences (in order of s, then j) go on top
+ * of the list of free pages; then the sequences take the pages they need, in
+ * order of s, then j, from the top of the list.  A sequence that would exceed
+ * max_pages pages is not served.  Where the pages or the T slots do not
+ * suffice, the first sequence that does not fit and all after it are not
+ * served.  A sequence that is not served keeps its length (ended ones are
+ * still released) and AB_ERR_CAPACITY is raised on the device.
+ *   n_new           device, int32 [S], >= -1
+ *   lens, lens_out  device, int32 [S]: lengths before and after the step (may
+ *                   be one buffer)
+ *   table           device, in/out: entries of the new pages are written
+ *   free_pages      device, in/out, int32 [num_pages]: the list, its top at
+ *                   free_count - 1; entries up to the new count are valid
+ *   free_count, free_count_out  device, int32 [1] (may be one buffer)
+ *   cu_new          device, out, int32 [S + 1]: prefix sums of the tokens served
+ *   slots, positions  device, out, int32 [T]: slot and position of each new
+ *                   token, sequence after sequence; slot -1 and position 0
+ *                   behind the last.  T = 0: only pages are given back.
+ * With lens_out and free_count_out apart from lens and free_count the call can
+ * be repeated with the same result.
+ */
+ab_status ab_paged_plan(const ab_paged_params* p, int32_t T, const int32_t* n_new, const int32_t* lens,
+                        int32_t* lens_out, int32_t* table, int32_t* free_pages, const int32_t* free_count,
+                        int32_t* free_count_out, int32_t* cu_new, int32_t* slots, int32_t* positions, void* stream);
+
+/*
+ * Norm and rotation of T new tokens (T = 0: nothing is done), written into the cache: Q [T, Hq, d]
+ * receives the queries, the tokens' slots of K and V receive keys and values.
+ * q has Hq heads, k and v have Hkv (the batch strides are not used).  A token
+ * with a negative slot is skipped (its row of Q is left as it was).
+ *   slots, positions  device, int32 [T], as ab_paged_plan writes them.  Slots
+ *                     must be distinct: of two tokens with one slot either may
+ *                     remain, in parts.
+ *   ksum              device, in/out, or NULL: for every page that the slots
+ *                     touch, the mean of its keys up to the page's last slot
+ *                     in the list (slots of one page stand together, in
+ *                     ascending order, as ab_paged_plan writes them).
+ */
+ab_status ab_paged_append(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T, const ab_tokens* q,
+                          const ab_tokens* k, const ab_tokens* v, const int32_t* slots, const int32_t* positions,
+                          void* Q, void* K, void* V, void* ksum, void* stream);
+
+/*
+ * The selector for one new token per sequence: with n_j the number of keys in
+ * page j and h the G query heads of key/value head g,
+ *   P[s,g,j] = (1/G) sum_h softmax_j(q_h . ksum_j / sqrt(d) + ln n_j)
+ * over the sequence's pages (ab_select's P with the heads in the place of the
+ * clusters).
+ *   P  device, out, fp32 [S, Hkv, max_pages]; entries behind the sequence's
+ *      last page are left as they were.
+ */
+ab_status ab_paged_select(const ab_paged_params* p, int32_t T, const void* Q, const void* ksum, const int32_t* table,
+                          const int32_t* lens, const int32_t* cu_new, float* P, void* workspace, size_t ws_bytes,
+                          void* stream);
+
+/*
+ * The pages to attend to.  For a sequence of n pages Kb = clamp(floor(keep_ratio
+ * n + 1/2), 1, n) (0 for n = 0): its newest min(recent, Kb) pages, and those of
+ * the others with the largest P (ties to the lower page), in ascending order.
+ * P must be >= 0; negative values and NaN count as 0.
+ *   idx    device, out, int32 [S, Hkv, max_pages]: the first count entries of a
+ *          row are written
+ *   count  device, out, int32 [S, Hkv]
+ */
+ab_status ab_paged_topk(const ab_paged_params* p, const float* P, const int32_t* lens, int32_t* idx, int32_t* count,
+                        void* stream);
+
+/*
+ * Attention of one token per sequence over the cache,
+ *   O[s,h] = sum_k e^{x_k} v_k / sum_k e^{x_k},  x_k = q_h . k_k / sqrt(d),
+ * over the first lens[s] tokens of sequence s, or over those in the pages
+ * idx[s,g,0..count[s,g]) (positions in the sequence; in any order, a page that
+ * is listed twice counts twice).  O = 0 where there is no key.  What the cache
+ * holds behind a sequence's end does not matter (NaN included).
+ *   idx, count  device, as ab_paged_topk writes them; both NULL: all pages
+ *   O           device, out, [S, Hq, d] bf16 (row s; rows of skipped sequences
+ *               are left as they were)
+ * The work is divided evenly over the GPU whatever the lengths are, and the
+ * parts of a row are joined in a fixed order: results are the same each time.
+ */
+ab_status ab_attention_paged(const ab_paged_params* p, int32_t T, const void* Q, const void* K, const void* V,
+                             const int32_t* table, const int32_t* lens, const int32_t* cu_new, const int32_t* idx,
+                             const int32_t* count, void* O, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * A step of sparse attention over the cache: ab_paged_append, ab_paged_select,
+ * ab_paged_topk and ab_attention_paged with the lists, for the newest token of
+ * each sequence.  Arguments as for those calls (lens, cu_new, slots and
+ * positions as ab_paged_plan leaves them: the lengths after the step), all
+ * checked before the first is enqueued.
+ */
+ab_status ab_paged_forward(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T, const ab_tokens* q,
+                           const ab_tokens* k, const ab_tokens* v, const int32_t* slots, const int32_t* positions,
+                           const int32_t* table, const int32_t* lens, const int32_t* cu_new, void* Q, void* K, void* V,
+                           void* ksum, float* P, int32_t* idx, int32_t* count, void* O, void* workspace,
+                           size_t ws_bytes, void* stream);
+
 /*
  * Reads and clears the device error word of the current device, after
  * synchronising `stream`.  *code receives AB_OK or the first ab_status raised

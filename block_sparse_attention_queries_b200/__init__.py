@@ -541,22 +541,6 @@ def _dense_tokens(p: Params, nr: NormRope, q, k, v, pos_q, pos_k):
     return dev, tok
 
 
-def _span(t):
-    """First byte of a tensor and the one behind its last."""
-    n = 1 + sum((k - 1) * st for k, st in zip(t.shape, t.stride())) if t.numel() else 0
-    return t.data_ptr(), t.data_ptr() + n * t.element_size()
-
-
-def _apart(out, inputs):
-    """No output reaches into an input's span or another output's, except that the
-    inputs may share one."""
-    spans = [_span(t) for t in out if t is not None]
-    for k, (lo, hi) in enumerate(spans):
-        for lo2, hi2 in spans[:k] + [_span(t) for t in inputs if t is not None]:
-            if lo < hi2 and lo2 < hi:
-                raise ValueError("outputs must not overlap each other or the inputs")
-
-
 def ab_qk_norm_rope(p: Params, nr: NormRope, q, k=None, v=None, pos_q=None, pos_k=None, out=None):
     """Norm and rotation from the projections' layout to the attention's: q
     [B, L, H, d], k and v [B, Lk, H, d] bf16 (any strides that are multiples of
@@ -574,7 +558,6 @@ def ab_qk_norm_rope(p: Params, nr: NormRope, q, k=None, v=None, pos_q=None, pos_
         for t, s, name in zip(out, shapes, "QKV"):
             if s is not None:
                 _check_tensor(t, torch.bfloat16, s, dev, name)
-        _apart([t for t, s in zip(out, shapes) if s is not None], (q, k, v))
     _call("ab_qk_norm_rope", dev, p.c(), nr._c, *tok, _p(pos_q), _p(pos_k), *(_p(t) for t in out))
     return tuple(t if s is not None else None for t, s in zip(out, shapes))
 
@@ -592,7 +575,6 @@ def ab_forward_qkv(p: Params, nr: NormRope, q, k, v, pos_q=None, pos_k=None, buf
         if getattr(b, name, None) is None:
             setattr(b, name, torch.empty(p.B, p.H, n, p.d, dtype=torch.bfloat16, device=dev))
         _check_tensor(getattr(b, name), torch.bfloat16, (p.B, p.H, n, p.d), dev, name)
-    _apart((b.Q, b.K, b.V), (q, k, v))
     for name, shape in (("P", (p.B, p.H, p.Nq, p.Nkv)), ("idx", (p.B, p.H, p.Nq, p.Nkv)),
                         ("pi_q32", (p.B, p.H, p.Nq, p.Nkv)), ("count", (p.B, p.H, p.Nq)), ("O", (p.B, p.H, p.L, p.d))):
         _check_tensor(getattr(b, name), getattr(b, name).dtype, shape, dev, name)
@@ -683,7 +665,6 @@ def _paged_tokens(pp: PagedParams, nr: NormRope, q, k, v, slots, positions, K, V
         Q = torch.empty(T, pp.Hq, pp.d, dtype=torch.bfloat16, device=dev)
     else:
         _check_tensor(Q, torch.bfloat16, (T, pp.Hq, pp.d), dev, "Q")
-        _apart((Q,), (q, k, v))
     return dev, T, tok, Q
 
 

@@ -20,6 +20,8 @@ int sm_count() {
 }
 
 // ------------------------------------------------------ norm and rotation
+constexpr int64_t kRopeMaxUnits = int64_t(1) << 30;  // positions in the list of units stay in 32 bits
+
 ab_status check_norm_rope(const ab_norm_rope* nr) {
   if (!nr) return AB_ERR_INVALID_ARG;
   if (nr->norm < 0 || nr->norm > 2 || (nr->interleaved != 0 && nr->interleaved != 1)) return AB_ERR_INVALID_ARG;
@@ -44,34 +46,82 @@ TokenView view_of(const ab_tokens* x) {
   return TokenView{static_cast<const __nv_bfloat16*>(x->ptr), x->batch, x->token, x->head};
 }
 
-// Head rows that one CTA can hold: 16 warps of 32 / (d/8) rows, 8 rows a lane.
-int rope_max_heads(int d) { return 16 * (256 / d) * kRopeVecs; }
+// Heads that one CTA can take for norm 2: 16 warps of 32 / (d/8) rows, 8 rows a lane.
+int rope_max_heads(int d) { return 16 * (256 / d) * kRopeRowsMany; }
 
-ab_status launch_norm_rope(const NormRopeArgs& a, int d, const ab_norm_rope* nr, int64_t blocks, cudaStream_t st) {
+// tokens[k] = 0 where the k-th of q, k, v is not wanted.
+ab_status launch_norm_rope(NormRopeArgs a, int d, const ab_norm_rope* nr, cudaStream_t st) {
+  const int sms = sm_count();
+  if (!sms) return AB_ERR_CUDA;
   int heads = 0;
   for (int k = 0; k < 3; ++k)
-    if (a.in[k].ptr) heads = a.heads[k] > heads ? a.heads[k] : heads;
-  // four head rows a lane, as far as 16 warps reach
-  const int per_warp = 4 * (256 / d);
-  int warps = (heads + per_warp - 1) / per_warp;
-  warps = warps > 16 ? 16 : warps;
+    if (a.tokens[k]) heads = a.heads[k] > heads ? a.heads[k] : heads;
+  const int rows = 256 / d;  // head rows a warp covers at once
+  const bool team = nr->norm == kNormToken, many = team && heads > 16 * rows * kRopeRows;
+  const int nv = many ? kRopeRowsMany : kRopeRows, stages = many ? kRopeStagesMany : kRopeStages;
+  const int per_warp = rows * nv;
+  const int threads = team ? 32 * ((heads + per_warp - 1) / per_warp) : kRopeThreads;
+  const int smem = rope_smem_bytes(nv, stages, threads);
+  // resident CTAs: as many as shared memory and the registers (96 or 80 a thread) allow
+  int per_sm = (team ? 640 : 768) / threads;
+  if (per_sm > 220 * 1024 / smem) per_sm = 220 * 1024 / smem;
+  if (per_sm < 1) per_sm = 1;
+  int64_t all = 0;
+  int tokens = 0, units = 0;
+  a.merged = !team;
+  for (int k = 0; k < 3; ++k) {
+    a.groups[k] = team ? 1 : (a.heads[k] + per_warp - 1) / per_warp;
+    all += int64_t(a.tokens[k]) * a.groups[k];
+    if (all > kRopeMaxUnits) return AB_ERR_UNSUPPORTED;
+    a.units[k] = int(all);
+    if (!a.tokens[k]) continue;
+    if (tokens && a.tokens[k] != tokens) a.merged = false;
+    tokens = a.tokens[k];
+  }
+  if (a.merged)
+    for (int k = 0; k < 3; ++k) a.units[k] = units += a.tokens[k] ? a.groups[k] : 0;
+  a.n_units = int(all);
+  const int per_cta = team ? 1 : threads / 32;
+  const int64_t most = (all + per_cta - 1) / per_cta;
+  const int64_t blocks = most < int64_t(sms) * per_sm ? most : int64_t(sms) * per_sm;
   auto go = [&](auto kern) -> ab_status {
-    kern<<<unsigned(blocks), unsigned(32 * warps), 0, st>>>(a);
+    if (smem > 48 * 1024 && set_smem(kern, smem) != cudaSuccess) return AB_ERR_CUDA;
+    kern<<<unsigned(blocks), unsigned(threads), smem, st>>>(a);
     return launch_status();
   };
   auto by_norm = [&](auto dd, auto il) -> ab_status {
     constexpr int D = decltype(dd)::value;
     constexpr bool I = decltype(il)::value;
     switch (nr->norm) {
-      case kNormNone: return go(norm_rope_kernel<D, kNormNone, I>);
-      case kNormHead: return go(norm_rope_kernel<D, kNormHead, I>);
-      default: return go(norm_rope_kernel<D, kNormToken, I>);
+      case kNormNone: return go(norm_rope_kernel<D, kNormNone, I, kRopeRows, kRopeStages>);
+      case kNormHead: return go(norm_rope_kernel<D, kNormHead, I, kRopeRows, kRopeStages>);
+      default:
+        return many ? go(norm_rope_kernel<D, kNormToken, I, kRopeRowsMany, kRopeStagesMany>)
+                    : go(norm_rope_kernel<D, kNormToken, I, kRopeRows, kRopeStages>);
     }
   };
   using T128 = std::integral_constant<int, 128>;
   using T64 = std::integral_constant<int, 64>;
   if (d == 128) return nr->interleaved ? by_norm(T128{}, std::true_type{}) : by_norm(T128{}, std::false_type{});
   return nr->interleaved ? by_norm(T64{}, std::true_type{}) : by_norm(T64{}, std::false_type{});
+}
+
+// Bytes [first, last) that tokens reach over.
+struct Span {
+  uintptr_t lo, hi;
+};
+Span span_of(const ab_tokens* x, int64_t nb, int64_t nt, int64_t nh, int d) {
+  const int64_t n[3] = {nb, nt, nh}, s[3] = {x->batch, x->token, x->head};
+  int64_t lo = 0, hi = d;
+  for (int k = 0; k < 3; ++k)
+    if (n[k] > 1) (s[k] < 0 ? lo : hi) += (n[k] - 1) * s[k];
+  const uintptr_t p = reinterpret_cast<uintptr_t>(x->ptr);
+  return {p + uintptr_t(lo * 2), p + uintptr_t(hi * 2)};
+}
+bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+Span span_of(const void* p, int64_t elements) {
+  const uintptr_t q = reinterpret_cast<uintptr_t>(p);
+  return {q, q + uintptr_t(elements) * 2};
 }
 
 void set_norm_rope(NormRopeArgs* a, const ab_norm_rope* nr) {
@@ -83,10 +133,10 @@ void set_norm_rope(NormRopeArgs* a, const ab_norm_rope* nr) {
   a->eps = nr->eps;
 }
 
-// Arguments of the dense call; the launch's blocks in *blocks.
+// Arguments of the dense call.
 ab_status prepare_norm_rope(const Dims& d, const ab_norm_rope* nr, const ab_tokens* q, const ab_tokens* k,
                             const ab_tokens* v, const int32_t* pos_q, const int32_t* pos_k, void* Q, void* K, void* V,
-                            NormRopeArgs* a, int64_t* blocks) {
+                            NormRopeArgs* a) {
   const ab_status s = check_norm_rope(nr);
   if (s != AB_OK) return s;
   if (!q && !k && !v) return AB_ERR_INVALID_ARG;
@@ -94,12 +144,8 @@ ab_status prepare_norm_rope(const Dims& d, const ab_norm_rope* nr, const ab_toke
   void* out[3] = {Q, K, V};
   const int32_t* pos[2] = {pos_q, pos_k};
   *a = NormRopeArgs{};
-  int64_t n = 0;
   for (int x = 0; x < 3; ++x) {
     const int len = x == 0 ? d.L : d.Lk;
-    a->first_block[x] = int(n);
-    a->heads[x] = d.H;
-    a->len[x] = len;
     if (!in[x]) continue;
     if (check_tokens(in[x], d.B, len, d.H) != AB_OK || !out[x] || !aligned16(out[x])) return AB_ERR_INVALID_ARG;
     if (x < 2) {
@@ -107,15 +153,23 @@ ab_status prepare_norm_rope(const Dims& d, const ab_norm_rope* nr, const ab_toke
       if (nr->cos_table && !pos[x] && len > nr->n_pos) return AB_ERR_INVALID_ARG;
       a->pos[x] = pos[x];
     }
+    if (int64_t(d.B) * len > kRopeMaxUnits) return AB_ERR_UNSUPPORTED;
+    a->heads[x] = d.H;
+    a->len[x] = len;
+    a->tokens[x] = d.B * len;
     a->in[x] = view_of(in[x]);
     a->out[x] = static_cast<__nv_bfloat16*>(out[x]);
-    n += int64_t(d.B) * len;
-    if (n > INT_MAX) return AB_ERR_UNSUPPORTED;
   }
-  // a tensor that is left out has no CTAs: the next one begins where it would
   if (d.H > rope_max_heads(d.d)) return AB_ERR_UNSUPPORTED;
+  for (int x = 0; x < 3; ++x) {
+    if (!in[x]) continue;
+    const Span o = span_of(out[x], int64_t(a->tokens[x]) * d.H * d.d);
+    for (int y = 0; y < 3; ++y) {
+      if (in[y] && overlap(o, span_of(in[y], d.B, a->len[y], d.H, d.d))) return AB_ERR_INVALID_ARG;
+      if (in[y] && y < x && overlap(o, span_of(out[y], int64_t(a->tokens[y]) * d.H * d.d))) return AB_ERR_INVALID_ARG;
+    }
+  }
   set_norm_rope(a, nr);
-  *blocks = n;
   return AB_OK;
 }
 
@@ -182,18 +236,20 @@ ab_status prepare_append(const ab_paged_params* p, const ab_norm_rope* nr, int32
   if (s != AB_OK) return s;
   if (T < 1) return AB_ERR_INVALID_ARG;
   if (any_bad({slots, positions, Q, Kc, Vc}) || !aligned16(ksum)) return AB_ERR_INVALID_ARG;
-  if (T > INT_MAX / 3 || p->Hq > rope_max_heads(p->d)) return AB_ERR_UNSUPPORTED;
+  if (T > kRopeMaxUnits || p->Hq > rope_max_heads(p->d)) return AB_ERR_UNSUPPORTED;
   const ab_tokens* in[3] = {q, k, v};
   void* out[3] = {Q, Kc, Vc};
   *a = NormRopeArgs{};
   for (int x = 0; x < 3; ++x) {
     a->heads[x] = x == 0 ? p->Hq : p->Hkv;
     if (check_tokens(in[x], 1, T, a->heads[x]) != AB_OK) return AB_ERR_INVALID_ARG;
-    a->len[x] = T;
-    a->first_block[x] = x * T;
+    a->len[x] = a->tokens[x] = T;
     a->in[x] = view_of(in[x]);
     a->out[x] = static_cast<__nv_bfloat16*>(out[x]);
   }
+  const Span o = span_of(Q, int64_t(T) * p->Hq * p->d);
+  for (int x = 0; x < 3; ++x)
+    if (overlap(o, span_of(in[x], 1, T, a->heads[x], p->d))) return AB_ERR_INVALID_ARG;
   a->pos[0] = a->pos[1] = positions;
   a->slots = slots;
   a->page_shift = log2_of(p->page);
@@ -204,7 +260,7 @@ ab_status prepare_append(const ab_paged_params* p, const ab_norm_rope* nr, int32
 
 ab_status run_append(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T, const NormRopeArgs& a, void* Kc,
                      void* ksum, cudaStream_t st) {
-  ab_status s = launch_norm_rope(a, p->d, nr, int64_t(3) * T, st);
+  ab_status s = launch_norm_rope(a, p->d, nr, st);
   if (s != AB_OK || !ksum) return s;
   // a CTA looks at 1 to 32 slots: few where there are few, so that pages spread over the SMs
   int per_cta = (T + 1183) / 1184;
@@ -316,10 +372,9 @@ ab_status ab_qk_norm_rope(const ab_params* p, const ab_norm_rope* nr, const ab_t
   ab_status s = check_params(p, false, &d);
   if (s != AB_OK) return s;
   NormRopeArgs a;
-  int64_t blocks = 0;
-  s = prepare_norm_rope(d, nr, q, k, v, pos_q, pos_k, Q, K, V, &a, &blocks);
+  s = prepare_norm_rope(d, nr, q, k, v, pos_q, pos_k, Q, K, V, &a);
   if (s != AB_OK) return s;
-  return launch_norm_rope(a, d.d, nr, blocks, static_cast<cudaStream_t>(stream));
+  return launch_norm_rope(a, d.d, nr, static_cast<cudaStream_t>(stream));
 }
 
 ab_status ab_forward_qkv(const ab_params* p, const ab_norm_rope* nr, const ab_tokens* q, const ab_tokens* k,
@@ -334,10 +389,9 @@ ab_status ab_forward_qkv(const ab_params* p, const ab_norm_rope* nr, const ab_to
   s = check_path_args(Q, K, V, P, idx, pi_q32, count, O, workspace, ws_bytes, workspace_layout(d).total);
   if (s != AB_OK) return s;
   NormRopeArgs a;
-  int64_t blocks = 0;
-  s = prepare_norm_rope(d, nr, q, k, v, pos_q, pos_k, Q, K, V, &a, &blocks);
+  s = prepare_norm_rope(d, nr, q, k, v, pos_q, pos_k, Q, K, V, &a);
   if (s != AB_OK) return s;
-  s = launch_norm_rope(a, d.d, nr, blocks, static_cast<cudaStream_t>(stream));
+  s = launch_norm_rope(a, d.d, nr, static_cast<cudaStream_t>(stream));
   if (s != AB_OK) return s;
   return ab_forward(p, Q, K, V, P, idx, pi_q32, count, O, workspace, ws_bytes, stream);
 }

@@ -361,8 +361,8 @@ typedef struct {
  *                 (then n_pos >= L, Lk).  A position outside [0, n_pos) raises
  *                 AB_ERR_CAPACITY on the device, and its token's row of Q or K
  *                 is left as it was.
- *   Q, K, V       device, out, [B, H, L, d], [B, H, Lk, d] bf16; they must not
- *                 overlap the inputs.
+ *   Q, K, V       device, out, [B, H, L, d], [B, H, Lk, d] bf16; outputs that
+ *                 overlap the inputs or each other are refused.
  * AB_ERR_UNSUPPORTED for more than 256 heads (d 128) or 512 (d 64).
  */
 ab_status ab_qk_norm_rope(const ab_params* p, const ab_norm_rope* nr, const ab_tokens* q, const ab_tokens* k,
@@ -446,7 +446,8 @@ ab_status ab_paged_plan(const ab_paged_params* p, int32_t T, const int32_t* n_ne
 /*
  * Norm and rotation of T new tokens (T = 0: nothing is done), written into the cache: Q [T, Hq, d]
  * receives the queries, the tokens' slots of K and V receive keys and values.
- * q has Hq heads, k and v have Hkv (the batch strides are not used).  A token
+ * q has Hq heads, k and v have Hkv (the batch strides are not used); Q must not
+ * overlap them.  A token
  * with a negative slot is skipped (its row of Q is left as it was).
  *   slots, positions  device, int32 [T], as ab_paged_plan writes them.  Slots
  *                     must be distinct: of two tokens with one slot either may

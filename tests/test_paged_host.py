@@ -14,6 +14,8 @@ from block_sparse_attention_queries_b200 import build as abbuild
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 GOOD, BAD = 0x1000, 0x1008
+IN = 0x40000000                       # inputs, apart from the outputs
+OUT = (0x1000, 0x1000000, 0x2000000)
 BIG = 1 << 45
 
 
@@ -97,9 +99,9 @@ BAD_NR = [dict(norm=3), dict(norm=-1), dict(interleaved=2), dict(eps=-1.0), dict
 
 def test_norm_rope(lib):
     p = ab.Params(B=2, H=4, L=50, d=64).c()
-    t = ab.ab_tokens(GOOD, 50 * 256, 256, 64)
+    t = ab.ab_tokens(IN, 50 * 256, 256, 64)
 
-    def call(nr=None, tok=(t, t, t), pos=(None, None), out=(GOOD,) * 3, p=p):
+    def call(nr=None, tok=(t, t, t), pos=(None, None), out=OUT, p=p):
         return lib.ab_qk_norm_rope(p, nr or _nr(), *tok, *pos, *out, None)
 
     for kw in BAD_NR:
@@ -110,7 +112,7 @@ def test_norm_rope(lib):
                   ab.ab_tokens(GOOD, 8, 8, 1)):
         for k in range(3):
             assert call(tok=tuple(wrong if j == k else t for j in range(3))) == 1
-    for out in _each([GOOD] * 3):
+    for out in _each(list(OUT)):
         assert call(out=out) == 1
     assert call(pos=(BAD, None)) == 1 and call(pos=(None, BAD)) == 1
     assert call(_nr(n_pos=49)) == 1                              # no positions: every token needs its row
@@ -119,8 +121,24 @@ def test_norm_rope(lib):
     assert call(p=ab.Params(B=1 << 13, H=1, L=1 << 18, d=64).c(), nr=_nr(n_pos=1 << 18)) == 2  # more CTAs than a grid has
 
 
+def test_overlapping_outputs(lib):
+    # inputs of 50 tokens in a fused projection of 3 x 4 x 64; outputs of 50 x 256 values
+    p = ab.Params(B=1, H=4, L=50, d=64).c()
+    fused, n = 50 * 768 * 2, 50 * 256 * 2
+    t = [ab.ab_tokens(0x100000 + 512 * k, 0, 768, 64) for k in range(3)]
+    out = [0x200000 + n * k for k in range(3)]
+
+    for k in range(3):
+        for wrong in (0x100000 + 16, 0x100000 + fused - 16, 0x100000 - n + 16, out[k - 1] + 16):
+            a = [wrong if j == k else out[j] for j in range(3)]
+            assert lib.ab_qk_norm_rope(p, _nr(), *t, None, None, *a, None) == 1, (k, hex(wrong))
+    paged = [ab.ab_tokens(0x100000 + 2048 * k, 0, 1536, 128) for k in range(3)]
+    for wrong in (0x100000, 0x100000 + 16):
+        assert lib.ab_paged_append(PP.c(), _nr(), 5, *paged, GOOD, GOOD, wrong, GOOD, GOOD, None, None) == 1
+
+
 def test_append_and_forward(lib):
-    t = ab.ab_tokens(GOOD, 0, 8 * 128, 128)
+    t = ab.ab_tokens(IN, 0, 8 * 128, 128)
     nr = _nr()
 
     def append(T=5, tok=(t, t, t), ptr=(GOOD,) * 6, nr=nr, pp=PP):
@@ -149,9 +167,9 @@ def test_append_and_forward(lib):
 
 def test_forward_qkv(lib):
     p = ab.Params(B=1, H=2, L=256, d=64, q_block=64, kv_block=16, C=4).c()
-    t = ab.ab_tokens(GOOD, 0, 128, 64)
+    t = ab.ab_tokens(IN, 0, 128, 64)
     nr = _nr(n_pos=256)
-    ok = [GOOD] * 9                                              # Q, K, V, P, idx, pi_q32, count, O, workspace
+    ok = [*OUT] + [GOOD] * 6                                     # Q, K, V, P, idx, pi_q32, count, O, workspace
     for ptr in _each(ok):
         assert lib.ab_forward_qkv(p, nr, t, t, t, None, None, *ptr, BIG, None) == 1
     for k in range(3):
@@ -196,9 +214,3 @@ def test_binding_checks():
                dict(cos=torch.zeros(3, 64), sin=torch.zeros(3, 64))):
         with pytest.raises(ValueError):
             ab.NormRope(**kw)
-    a = torch.zeros(10, 16)
-    ab._apart((a[:4],), (a[4:], a[5:]))                          # inputs may share memory
-    ab._apart((a[0], None), (None, a[1]))
-    for out, inputs in (((a[:5],), (a[4:],)), ((a, a.clone()), (a[:, 3],)), ((a[:5], a[4:]), ())):
-        with pytest.raises(ValueError):
-            ab._apart(out, inputs)

@@ -14,6 +14,19 @@
 
 namespace ab {
 
+// A kernel that follows one of this library's in the same call is launched
+// while that one still runs, and waits here for its end and its results;
+// pdl_trigger lets the next one be launched.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Untiled copy into shared memory: 16-byte aligned, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 constexpr int kMaxSeqs = 8192;   // sequences of a block table: their prefix sums fit in shared memory
 constexpr int kMaxGroup = 16;    // query heads per key/value head
 
@@ -321,7 +334,8 @@ __global__ void __launch_bounds__(256)
 // The work is a list of units (sequences, or rows of lists) of tiles(u) equal
 // tiles.  CTA c of C takes the tiles [c total / C, (c + 1) total / C) of the
 // whole list, whatever the units' lengths, so the load is even without the
-// host knowing any length.  Every CTA sums the units' tiles itself.
+// host knowing any length (C is the number of tiles where that is less).  Every
+// CTA sums the units' tiles itself.
 struct Share {
   int unit;       // first unit with work
   int off;        // first tile in it
@@ -357,7 +371,8 @@ __device__ __forceinline__ Share share_work(F tiles, int n_units, int c, int C, 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     // total < 2^41 (2^16 units of at most 2^25 tiles) and C < 2^10
-    const int64_t b = total * c / C, e = total * (c + 1) / C;
+    const int64_t n = total < C ? total : C;
+    const int64_t b = c < n ? total * c / n : total, e = c < n ? total * (c + 1) / n : total;
     Share r{0, 0, int(e - b), b, total};
     int64_t base = 0;
     int chunk = 0;

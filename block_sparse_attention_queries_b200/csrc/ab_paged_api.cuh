@@ -19,6 +19,27 @@ int sm_count() {
   return n;
 }
 
+// Launch of a kernel that begins with pdl_wait, behind another kernel of the
+// same call.
+template <typename... Params, typename... Args>
+ab_status launch_after(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, Params(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return AB_ERR_CUDA;
+  }
+  return AB_OK;
+}
+
 // ------------------------------------------------------ norm and rotation
 constexpr int64_t kRopeMaxUnits = int64_t(1) << 30;  // positions in the list of units stay in 32 bits
 
@@ -205,7 +226,7 @@ PagedView paged_view(const ab_paged_params* p, const int32_t* table, const int32
 
 struct PagedWorkspace {
   size_t off_scores, off_part;                     // select
-  size_t off_meta, off_part_o, off_ml;  // attention (its first bytes: the number of tiles)
+  size_t off_part_o, off_ml;            // attention (its first bytes: DecMeta)
   size_t select, attend;                // bytes of each
 };
 
@@ -216,8 +237,7 @@ PagedWorkspace paged_workspace(const ab_paged_params* p) {
   w.off_part = align256(w.off_scores + rows * p->max_pages * 4);
   w.select = align256(w.off_part + rows * chunks * 8);
   const size_t heads = p->Hq / p->Hkv > 8 ? 16 : 8;
-  w.off_meta = 256;
-  w.off_part_o = align256(w.off_meta + kDecMaxParts * sizeof(DecMeta));
+  w.off_part_o = align256(kDecMaxParts * sizeof(DecMeta));
   w.off_ml = align256(w.off_part_o + size_t(kDecMaxParts) * 2 * heads * p->d * 4);
   w.attend = align256(w.off_ml + size_t(kDecMaxParts) * 2 * heads * 8);
   return w;
@@ -316,13 +336,10 @@ ab_status launch_paged_attention(const DecArgs& a, const CUtensorMap& tmK, const
   auto kern = paged_attention_kernel<D, RB, kLists>;
   constexpr int smem = DecSmem<D, RB>::kAlloc;
   if (set_smem(kern, smem) != cudaSuccess) return AB_ERR_CUDA;
-  kern<<<unsigned(grid), kDecThreads, smem, st>>>(tmK, tmV, a);
+  kern<<<unsigned(grid), dec_threads(RB), smem, st>>>(tmK, tmV, a);
   if (launch_status() != AB_OK) return AB_ERR_CUDA;
-  if (grid > 1) {
-    paged_join_kernel<D><<<dim3(unsigned(grid - 1), unsigned(a.v.G)), D * kJoinGroups, 0, st>>>(a, grid, RB * 8);
-    return launch_status();
-  }
-  return AB_OK;
+  if (grid == 1) return AB_OK;
+  return launch_after(paged_join_kernel<D>, dim3(unsigned(grid - 1), unsigned(a.v.G)), 32 * kJoinWarps, 0, st, a, RB * 8);
 }
 
 ab_status run_paged_attention(const ab_paged_params* p, const PagedView& v, const void* Q, const void* Kc,
@@ -342,8 +359,7 @@ ab_status run_paged_attention(const ab_paged_params* p, const PagedView& v, cons
   a.count = count;
   a.O = static_cast<__nv_bfloat16*>(O);
   a.scale_log2 = float(1.4426950408889634 / std::sqrt(double(p->d)));
-  a.total = reinterpret_cast<int64_t*>(ws);
-  a.meta = reinterpret_cast<DecMeta*>(ws + w.off_meta);
+  a.meta = reinterpret_cast<DecMeta*>(ws);
   a.part_o = reinterpret_cast<float*>(ws + w.off_part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + w.off_ml);
   const int grid = sms < kDecMaxParts ? sms : kDecMaxParts;

@@ -13,34 +13,52 @@
 //    whole list of tiles is divided evenly among persistent CTAs, whatever the
 //    lengths (share_work); a row that several CTAs share is joined from their
 //    partial results by a second kernel;
-//  - one warp brings the tiles into a ring of shared-memory stages by TMA (a
-//    page of a head is one box of 2 to 16 KB, found through the block table),
-//    running ahead across rows;
-//  - four warps take 16 keys of each tile each, with a softmax state of their
-//    own, joined once per row.
+//  - one warp plans 32 tiles at a time, a lane for each: the tile's row, its
+//    pages through the lists and the block table.  All lookups of 32 tiles run
+//    side by side, so that rows of a single tile cost no more than long ones;
+//  - one warp brings the planned tiles into a ring of shared-memory stages by
+//    TMA (a page of a head is one box of 2 to 16 KB), with the row's queries
+//    where a row begins;
+//  - groups of four warps take the rows in turn (two groups for G <= 8, so that
+//    one row's start and end, about 2500 cycles, overlap the next one's tiles);
+//    a group's warps take 16 keys of each tile each, with a softmax state of
+//    their own, joined once per row.
 //
 // The G heads are the rows of an m16n8k16 product.  P is used as the sum of two
 // bfloat16 numbers, so that its rounding (2^-17) does not show next to the
 // output's own: for G <= 8 the upper part fills rows 0-7 of the P V product
 // and the lower part rows 8-15, at no cost; for G up to 16 two products run
-// per half.  V rows that lie behind the sequence's end are set to zero in
-// shared memory, since 0 times what an unwritten page holds may be NaN.
+// per half.  V rows that lie behind the sequence's end are set to zero in the
+// operand, since 0 times what an unwritten page holds may be NaN.
 #pragma once
 
 #include "ab_paged.cuh"
 
 namespace ab {
 
-constexpr int kDecThreads = 160;   // four consumer warps, one producer warp
+// groups of four consumer warps, the TMA warp, the planning warp
+__host__ __device__ constexpr int dec_groups(int RB) { return RB == 1 ? 2 : 1; }
+__host__ __device__ constexpr int dec_threads(int RB) { return dec_groups(RB) * 128 + 64; }
 constexpr int kDecTile = 64;       // keys per tile
 constexpr int kDecMaxParts = 1024; // CTAs at most
 constexpr float kDecLazy = 8.f;    // log2 slack of the reference maximum
 
-// Where CTA c's share starts: the row that holds its first tile (-1: behind
-// the end), the tile's place in the row, and the row's tiles.
+// Where CTA c's share starts, for the joining kernel: the row whose parts the
+// CTAs c - 1 to `last` hold if c is the first share that begins inside of it,
+// else -1; `slot`: where CTA c - 1 has put its part.
 struct DecMeta {
-  int row, off, tiles, pad;
+  int row, last, slot, pad;
 };
+
+// A planned tile.
+struct DecTile {
+  int coord[4];  // page * Hkv + head of up to 4 pages, -1: none
+  int valid;     // valid keys of each, a byte each
+  int row;       // s * Hkv + key/value head
+  int qrow;      // row of Q
+  int flags;
+};
+enum : int { kTileFirst = 1, kTileLast = 2, kRowStart = 4, kRowEnd = 8, kTileRow = 4 /* shift: rows begun before */ };
 
 struct DecArgs {
   PagedView v;
@@ -49,8 +67,7 @@ struct DecArgs {
   const int32_t* count;      // [S, Hkv]
   __nv_bfloat16* O;          // [S, Hq, d]
   float scale_log2;
-  int64_t* total;            // workspace: tiles of all rows
-  DecMeta* meta;             // [grid + 1]
+  DecMeta* meta;             // workspace: [grid]
   float* part_o;             // [grid, 2, 8 RB, d] unnormalised
   float2* part_ml;           // [grid, 2, 8 RB]
 };
@@ -59,40 +76,50 @@ template <int D, int RB>
 struct DecSmem {
   static constexpr int kRow = D * 2;
   static constexpr int kTileBytes = kDecTile * kRow;  // one of K, V
-  static constexpr int kStages = D == 128 ? (RB == 1 ? 6 : 5) : (RB == 1 ? 12 : 10);
+  static constexpr int kGroups = dec_groups(RB);
+  static constexpr int kStages = D == 128 ? 5 : (RB == 1 ? 10 : 9);
   static constexpr int kPitch = D + 8;                // floats; rows of a quad's lanes in different banks
-  static constexpr int kOffMerge = kStages * 2 * kTileBytes;
+  static constexpr int kQPitch = kRow + 16;           // bytes, for the same reason
+  static constexpr int kQBytes = RB * 8 * kQPitch;
+  static constexpr int kOffQ = kStages * 2 * kTileBytes;
+  static constexpr int kOffMerge = kOffQ + kStages * kQBytes;
   static constexpr int kMergeBytes = 4 * RB * 8 * kPitch * 4;
-  static constexpr int kOffMl = kOffMerge + kMergeBytes;  // 4 warps x 8 RB float2
-  static constexpr int kOffMeta = kOffMl + 4 * RB * 8 * 8;  // per stage: valid keys of up to 4 pages
+  static constexpr int kOffMl = kOffMerge + kGroups * kMergeBytes;  // per group: 4 warps x 8 RB float2
+  static constexpr int kMlBytes = 4 * RB * 8 * 8;
+  static constexpr int kOffPlan = kOffMl + kGroups * kMlBytes;      // 2 x 32 planned tiles
+  static constexpr int kOffMeta = kOffPlan + 2 * 32 * int(sizeof(DecTile));  // per stage: valid, row, flags
   static constexpr int kOffBar = kOffMeta + kStages * 16;
-  static constexpr int kOffMisc = kOffBar + kStages * 16;
+  static constexpr int kNumBars = 2 * kStages + 4;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 64;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 232448, "more shared memory than a CTA may have");
-  static_assert(kOffMerge >= kShareSums * 8, "share_work's sums lie in the stages");
+  static_assert(kOffQ >= kShareSums * 8, "share_work's sums lie in the stages");
 };
 
 template <bool kLists>
 struct DecRows {
-  // tiles of unit u (a sequence, or a row of the lists), all of its heads
-  static __device__ __forceinline__ int row_tiles(const DecArgs& a, int s, int hk) {
+  // list entries (pages) of a row
+  static __device__ __forceinline__ int row_entries(const DecArgs& a, int s, int hk) {
     const PagedView& v = a.v;
     if (query_row(v, s) < 0) return 0;
-    const int pages = pages_of(v, seq_len(v, s));
-    int entries = pages;
     if constexpr (kLists) {
-      entries = __ldg(a.count + int64_t(s) * v.Hkv + hk);
-      if (entries < 0 || entries > v.max_pages) {
+      const int n = __ldg(a.count + int64_t(s) * v.Hkv + hk);
+      if (n < 0 || n > v.max_pages) {
         raise_error(AB_ERR_CAPACITY);
-        entries = entries < 0 ? 0 : v.max_pages;
+        return n < 0 ? 0 : v.max_pages;
       }
+      return n;
     }
-    return (entries * v.page + kDecTile - 1) / kDecTile;
+    return pages_of(v, seq_len(v, s));
   }
+  static __device__ __forceinline__ int tiles_of(const DecArgs& a, int entries) {
+    return ((entries << a.v.page_shift) + kDecTile - 1) / kDecTile;
+  }
+  // tiles of unit u: a row of the lists, or a sequence with all of its heads
   static __device__ __forceinline__ int unit_tiles(const DecArgs& a, int u) {
-    if constexpr (kLists) return row_tiles(a, u / a.v.Hkv, u % a.v.Hkv);
-    return row_tiles(a, u, 0) * a.v.Hkv;
+    if constexpr (kLists) return tiles_of(a, row_entries(a, u / a.v.Hkv, u % a.v.Hkv));
+    return tiles_of(a, row_entries(a, u, 0)) * a.v.Hkv;
   }
 };
 
@@ -124,19 +151,24 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool p) {
 // D: head dim.  RB: blocks of 8 query heads per key/value head (1: G <= 8,
 // 2: G <= 16).  kLists: the pages of a list instead of all.
 template <int D, int RB, bool kLists>
-__global__ void __launch_bounds__(kDecThreads, 1)
+__global__ void __launch_bounds__(dec_threads(RB), 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                           const DecArgs a) {
+                           const __grid_constant__ DecArgs a) {
   using SM = DecSmem<D, RB>;
+  using Rows = DecRows<kLists>;
   constexpr int kStages = SM::kStages;
   constexpr int kHalves = D / 64;
+  constexpr int kGroups = dec_groups(RB), kTmaWarp = 4 * kGroups, kPlanWarp = kTmaWarp + 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   auto full = [&](int k) { return sbase + SM::kOffBar + 16u * uint32_t(k); };
   auto empty = [&](int k) { return sbase + SM::kOffBar + 16u * uint32_t(k) + 8u; };
+  auto plan_full = [&](int k) { return full(kStages + k); };
+  auto plan_empty = [&](int k) { return empty(kStages + k); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::kOffMisc);
   Share* share_out = reinterpret_cast<Share*>(smem + SM::kOffMisc + 16);
+  DecTile* plan = reinterpret_cast<DecTile*>(smem + SM::kOffPlan);
   // the prefix sums' scratch: stage memory that no copy has been issued into yet
   int64_t* sums = reinterpret_cast<int64_t*>(smem);
   const PagedView& v = a.v;
@@ -145,112 +177,153 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages; ++k) {
       mbar_init(full(k), 1);
-      mbar_init(empty(k), 4);
+      mbar_init(empty(k), 4 * kGroups);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(plan_full(k), 1);
+      mbar_init(plan_empty(k), 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == kTmaWarp && lane == 0) {
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
+  pdl_wait();
+  pdl_trigger();
   const int n_units = kLists ? v.S * v.Hkv : v.S;
-  const Share sh = share_work([&](int u) { return DecRows<kLists>::unit_tiles(a, u); }, n_units, blockIdx.x, gridDim.x,
-                              sums, share_out);
+  const Share sh =
+      share_work([&](int u) { return Rows::unit_tiles(a, u); }, n_units, blockIdx.x, gridDim.x, sums, share_out);
   fence_proxy_async_smem();  // the scratch's generic accesses come before the copies into it
   __syncthreads();
 
-  // start of the share, for the joining kernel
-  int s = kLists ? sh.unit / v.Hkv : sh.unit, hk = kLists ? sh.unit % v.Hkv : 0, off = sh.off;
-  if (sh.begin < sh.total) {
-    const int T = DecRows<kLists>::row_tiles(a, s, hk);
-    if (!kLists) {
-      hk = off / T;
-      off -= hk * T;
+  if (warp == kPlanWarp) {
+    // ------------------------------------------------------------ planner
+    const int per_tile = kDecTile >> v.page_shift;  // pages of a tile
+    int unit = sh.unit, pos = sh.off;  // tile `base` of the share is tile `pos` from the start of unit `unit` on
+    int rows = 0;  // rows begun
+    bool ok = true;
+    for (int base = 0, batch = 0; base < sh.n && ok; base += 32, ++batch) {
+      // find this lane's tile: the unit, and the tile's place in it
+      int x = pos + lane, mine = -1;
+      bool open = base + lane < sh.n;
+      for (int u0 = unit; __any_sync(0xffffffffu, open) && u0 < n_units; u0 += 32) {
+        const int t = u0 + lane < n_units ? Rows::unit_tiles(a, u0 + lane) : 0;
+        int64_t incl = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
+        int l = 0;  // first unit of these 32 whose sum passes x
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const int64_t y = __shfl_sync(0xffffffffu, incl, l + o - 1);
+          if (y <= x) l += o;
+        }
+        const int64_t before = __shfl_sync(0xffffffffu, incl - t, l & 31);
+        if (open) {
+          if (x < all) {
+            mine = u0 + l;
+            x -= int(before);
+            open = false;
+          } else {
+            x -= int(all);
+          }
+        }
+      }
+      DecTile d{{-1, -1, -1, -1}, 0, 0, 0, 0};
+      if (mine >= 0) {
+        int s = mine, hk = 0, off = x;
+        if constexpr (kLists) {
+          s = mine / v.Hkv;
+          hk = mine - s * v.Hkv;
+        }
+        const int entries = Rows::row_entries(a, s, hk), T = Rows::tiles_of(a, entries);
+        if constexpr (!kLists) {
+          hk = off / T;
+          off -= hk * T;
+        }
+        const int64_t row = int64_t(s) * v.Hkv + hk;
+        const int len = seq_len(v, s), pages = pages_of(v, len);
+        d.row = int(row);
+        d.qrow = query_row(v, s);
+        d.flags = (off == 0 || base + lane == 0 ? kTileFirst : 0) | (off == T - 1 || base + lane == sh.n - 1 ? kTileLast : 0) |
+                  (off == 0 ? kRowStart : 0) | (off == T - 1 ? kRowEnd : 0);
+        int j[4], id[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int e = off * per_tile + k;
+          j[k] = -1;
+          if (k < per_tile && e < entries) j[k] = kLists ? __ldg(a.idx + row * v.max_pages + e) : e;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          id[k] = -1;
+          if (j[k] >= 0 && j[k] < pages) id[k] = __ldg(v.table + int64_t(s) * v.max_pages + j[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k < per_tile && off * per_tile + k < entries) {
+            if (id[k] < 0 || id[k] >= v.num_pages) {
+              raise_error(AB_ERR_CAPACITY);
+            } else {
+              d.coord[k] = id[k] * v.Hkv + hk;
+              d.valid |= min(v.page, len - (j[k] << v.page_shift)) << (8 * k);
+            }
+          }
+        }
+      }
+      const uint32_t firsts = __ballot_sync(0xffffffffu, d.flags & kTileFirst);
+      d.flags |= (rows + __popc(firsts & (0xffffffffu >> (31 - lane))) - 1) << kTileRow;
+      rows += __popc(firsts);
+      ok = lane0_wait(plan_empty(batch & 1), ((batch >> 1) & 1) ^ 1, abort_flag);
+      if (!ok) break;
+      plan[(batch & 1) * 32 + lane] = d;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(plan_full(batch & 1));
+      // the next batch begins behind lane 31's tile
+      unit = __shfl_sync(0xffffffffu, mine, 31);
+      pos = __shfl_sync(0xffffffffu, x, 31) + 1;
+      if (unit < 0) break;  // the share's last batch
     }
-    if (threadIdx.x == 0) a.meta[blockIdx.x] = DecMeta{s * v.Hkv + hk, off, T, 0};
-  } else if (threadIdx.x == 0) {
-    a.meta[blockIdx.x] = DecMeta{-1, 0, 0, 0};
-  }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.total = sh.total;
-
-  // rows without keys: O = 0
-  for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
-    if (DecRows<kLists>::unit_tiles(a, u) == 0 && query_row(v, kLists ? u / v.Hkv : u) >= 0) {
-      const int n = v.G * D * (kLists ? 1 : v.Hkv);
-      uint32_t* o = reinterpret_cast<uint32_t*>(a.O + int64_t(u) * n);
-      for (int k = threadIdx.x; k < n / 2; k += kDecThreads) o[k] = 0u;
-    }
-  }
-
-  // next row with tiles (called by whole warps)
-  auto next_row = [&]() -> bool {
-    if (!kLists && ++hk < v.Hkv) return true;
-    const int u = next_unit([&](int k) { return DecRows<kLists>::unit_tiles(a, k); }, n_units,
-                            kLists ? s * v.Hkv + hk + 1 : s + 1);
-    s = kLists ? u / v.Hkv : u;
-    hk = kLists ? u % v.Hkv : 0;
-    return u < n_units;
-  };
-
-  int left = sh.n;
-  if (warp == 4) {
-    // ------------------------------------------------------------ producer
-    const int per_tile = kDecTile >> v.page_shift;  // list entries of a tile
+  } else if (warp == kTmaWarp) {
+    // ----------------------------------------------------------------- TMA
     const uint32_t page_bytes = uint32_t(SM::kRow) << v.page_shift;
     uint32_t use = 0;  // tiles issued
     bool ok = true;
-    while (left > 0 && ok) {
-      const int T = DecRows<kLists>::row_tiles(a, s, hk);
-      const int n = min(left, T - off);
-      const int len = seq_len(v, s), pages = pages_of(v, len);
-      const int64_t row = int64_t(s) * v.Hkv + hk;
-      const int e_end = kLists ? min(__ldg(a.count + row), v.max_pages) : pages;
-      // entries in groups of 32, each lane one: page id (-1: none) and valid keys
-      auto fetch = [&](int e, int& id, int& valid) {
-        id = -1;
-        valid = 0;
-        if (e < e_end) {
-          const int j = kLists ? __ldg(a.idx + row * v.max_pages + e) : e;
-          if (j >= 0 && j < pages) id = __ldg(v.table + int64_t(s) * v.max_pages + j);
-          if (id < 0 || id >= v.num_pages) {
-            raise_error(AB_ERR_CAPACITY);
-            id = -1;
-          } else {
-            valid = min(v.page, len - (j << v.page_shift));
-          }
+    for (int base = 0, batch = 0; base < sh.n && ok; base += 32, ++batch) {
+      ok = lane0_wait(plan_full(batch & 1), (batch >> 1) & 1, abort_flag);
+      const int n = min(32, sh.n - base);
+      for (int k = 0; k < n && ok; ++k, ++use) {
+        const DecTile* d = plan + (batch & 1) * 32 + k;
+        const int coord = lane < 4 ? d->coord[lane] : -1;
+        const int flags = d->flags;
+        const int st = int(use % kStages);
+        ok = lane0_wait(empty(st), ((use / kStages) & 1) ^ 1, abort_flag);
+        if (!ok) break;
+        const uint32_t there = __ballot_sync(0xffffffffu, coord >= 0);
+        if (lane == 0) {
+          *reinterpret_cast<int4*>(smem + SM::kOffMeta + st * 16) = make_int4(d->valid, d->row, flags, 0);
+          mbar_arrive_expect_tx(full(st), 2u * page_bytes * uint32_t(__popc(there)) +
+                                              ((flags & kTileFirst) ? uint32_t(v.G * SM::kRow) : 0u));
         }
-      };
-      const int e0 = off * per_tile, tiles_per_group = 32 / per_tile;
-      int id, valid, id_next, valid_next;
-      fetch(e0 + lane, id, valid);
-      for (int k0 = 0; k0 < n && ok; k0 += tiles_per_group) {
-        fetch(e0 + (k0 + tiles_per_group) * per_tile + lane, id_next, valid_next);
-        const int kn = min(tiles_per_group, n - k0);
-        for (int k = 0; k < kn; ++k, ++use) {
-          const int st = int(use % kStages);
-          bool got = true;
-          if (lane == 0) got = mbar_wait(empty(st), ((use / kStages) & 1) ^ 1, abort_flag);
-          if (!__shfl_sync(0xffffffffu, got ? 1 : 0, 0)) { ok = false; break; }
-          const int slot = lane - k * per_tile;  // this lane's entry of the tile
-          const bool mine = slot >= 0 && slot < per_tile;
-          const uint32_t there = __ballot_sync(0xffffffffu, mine && id >= 0);
-          if (mine) reinterpret_cast<int*>(smem + SM::kOffMeta + st * 16)[slot] = id >= 0 ? valid : 0;
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(full(st), 2u * page_bytes * uint32_t(__popc(there)));
-          __syncwarp();
-          if (mine && id >= 0) {
-            const uint32_t dst = sbase + uint32_t(st) * 2u * SM::kTileBytes + uint32_t(slot) * page_bytes;
-            tma_load_5d(dst, &tmK, full(st), 0, 0, 0, 0, id * v.Hkv + hk);
-            tma_load_5d(dst + SM::kTileBytes, &tmV, full(st), 0, 0, 0, 0, id * v.Hkv + hk);
-          }
+        __syncwarp();
+        if (coord >= 0) {
+          const uint32_t dst = sbase + uint32_t(st) * 2u * SM::kTileBytes + uint32_t(lane) * page_bytes;
+          tma_load_5d(dst, &tmK, full(st), 0, 0, 0, 0, coord);
+          tma_load_5d(dst + SM::kTileBytes, &tmV, full(st), 0, 0, 0, 0, coord);
         }
-        id = id_next;
-        valid = valid_next;
+        if ((flags & kTileFirst) && lane < v.G) {
+          const int hk = d->row % v.Hkv;
+          bulk_load(sbase + SM::kOffQ + uint32_t(st * SM::kQBytes + lane * SM::kQPitch),
+                    a.Q + ((int64_t(d->qrow) * v.Hkv + hk) * v.G + lane) * D, SM::kRow, full(st));
+        }
       }
-      left -= n;
-      off = 0;
-      if (left > 0 && ok) ok = next_row();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(plan_empty(batch & 1));
     }
     if (lane == 0) {
       // copies in flight land before shared memory is released, also if the
@@ -262,150 +335,188 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
   } else {
     // ----------------------------------------------------------- consumers
+    if (threadIdx.x == 0) {
+      // for the joining kernel
+      DecMeta mt{-1, 0, 0, 0};
+      if (sh.begin < sh.total && blockIdx.x > 0) {
+        int off = sh.off, s = sh.unit, hk = 0;
+        if constexpr (kLists) {
+          s = sh.unit / v.Hkv;
+          hk = sh.unit % v.Hkv;
+        }
+        const int T = Rows::tiles_of(a, Rows::row_entries(a, s, hk));
+        if constexpr (!kLists) {
+          hk = off / T;
+          off -= hk * T;
+        }
+        const int64_t C = sh.total < gridDim.x ? sh.total : int64_t(gridDim.x);
+        const int64_t start = sh.begin - off, prev = sh.total * (int(blockIdx.x) - 1) / C;
+        if (off > 0 && prev <= start) {
+          mt.row = s * v.Hkv + hk;
+          mt.last = int(((start + T) * C + sh.total - 1) / sh.total) - 1;  // the last whose begin is below the row's end
+          mt.slot = prev == start ? 0 : 1;
+        }
+      }
+      a.meta[blockIdx.x] = mt;
+    }
+    // units without keys: O = 0 (a lane looks at one, the warp writes)
+    for (int64_t k0 = int64_t(warp) * 32; blockIdx.x + k0 * gridDim.x < n_units; k0 += 128 * kGroups) {
+      const int64_t u = blockIdx.x + (k0 + lane) * gridDim.x;
+      const bool none = u < n_units && Rows::unit_tiles(a, int(u)) == 0 && query_row(v, kLists ? int(u) / v.Hkv : int(u)) >= 0;
+      for (uint32_t some = __ballot_sync(0xffffffffu, none); some; some &= some - 1) {
+        const int n = v.G * D * (kLists ? 1 : v.Hkv);
+        uint32_t* z = reinterpret_cast<uint32_t*>(a.O + (blockIdx.x + (k0 + __ffs(some) - 1) * gridDim.x) * n);
+        for (int k = lane; k < n / 2; k += 32) z[k] = 0u;
+      }
+    }
     const int g = lane >> 2, t = lane & 3;
-    const int key0 = warp * 16;  // this warp's keys of a tile
+    const int group = warp >> 2, gwarp = warp & 3, gthread = threadIdx.x & 127;
+    const int key0 = gwarp * 16;  // this warp's keys of a tile
     // row addresses of the operand loads within a tile (128-byte swizzle, 8-row
     // groups of kHalves KB): K as stored, V transposed
     const int krow = key0 + ((lane >> 4) << 3) + (lane & 7), kch = (lane >> 3) & 1;
     const int vrow = key0 + (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;
     const uint32_t kbase = uint32_t(krow >> 3) * (kHalves * 1024u) + uint32_t(krow & 7) * 128u;
     const uint32_t vbase = uint32_t(vrow >> 3) * (kHalves * 1024u) + uint32_t(vrow & 7) * 128u;
-    float* mrg = reinterpret_cast<float*>(smem + SM::kOffMerge);
-    float2* ml = reinterpret_cast<float2*>(smem + SM::kOffMl);
-    uint32_t use = 0;
-    int seg = 0;
-    bool ok = true;
-    while (left > 0 && ok) {
-      const int T = DecRows<kLists>::row_tiles(a, s, hk);
-      const int n = min(left, T - off);
-      const bool whole = n == T;
-      // queries: rows g and g + 8 of the 16 x d operand
-      uint32_t q0[D / 16][2], q1[D / 16][2];
-      {
-        const __nv_bfloat16* q = a.Q + (int64_t(query_row(v, s)) * v.Hkv + hk) * v.G * D + 2 * t;
+    float* mrg = reinterpret_cast<float*>(smem + SM::kOffMerge + group * SM::kMergeBytes);
+    float2* ml = reinterpret_cast<float2*>(smem + SM::kOffMl + group * SM::kMlBytes);
+    const int vshift = 8 * (key0 >> v.page_shift), vsub = key0 & (v.page - 1);
+    bool started = false;  // the current row's first tile is this CTA's
+    uint32_t q0[D / 16][2], q1[D / 16][2];  // queries: rows g and g + 8 of the 16 x d operand
+    float o[RB][D / 8][4], m[RB], l[RB];
+    for (uint32_t use = 0; use < uint32_t(sh.n); ++use) {
+      const int st = int(use % kStages);
+      const bool got = mbar_wait(full(st), (use / kStages) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, got)) {
+        bar_any(1 + group, 128, true);  // the group's other warps learn of it at their next barrier
+        break;
+      }
+      const int4 mt = *reinterpret_cast<const int4*>(smem + SM::kOffMeta + st * 16);
+      const int flags = mt.z;
+      if (kGroups > 1 && ((flags >> kTileRow) & (kGroups - 1)) != group) {  // another group's row
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(st));
+        continue;
+      }
+      if (flags & kTileFirst) {
+        const uint8_t* q = smem + SM::kOffQ + st * SM::kQBytes + g * SM::kQPitch + 4 * t;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            q0[k][z] = g < v.G ? __ldg(reinterpret_cast<const uint32_t*>(q + g * D + 16 * k + 8 * z)) : 0u;
+            q0[k][z] = g < v.G ? *reinterpret_cast<const uint32_t*>(q + 32 * k + 16 * z) : 0u;
             q1[k][z] = RB == 2 && g + 8 < v.G
-                           ? __ldg(reinterpret_cast<const uint32_t*>(q + (g + 8) * D + 16 * k + 8 * z))
+                           ? *reinterpret_cast<const uint32_t*>(q + 8 * SM::kQPitch + 32 * k + 16 * z)
                            : 0u;
           }
         }
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          m[r] = -INFINITY;
+          l[r] = 0.f;
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[r][k][e] = 0.f;
+        }
+        started = flags & kRowStart;
       }
-      float o[RB][D / 8][4];
+      const int valid = min(16, int((uint32_t(mt.x) >> vshift) & 255u) - vsub);
+      const uint32_t kt = sbase + uint32_t(st) * 2u * SM::kTileBytes, vt = kt + SM::kTileBytes;
+      if (valid > 0) {
+        // S = Q K^T for 16 keys: two n-tiles, each in two accumulators
+        float c[2][2][4] = {};
 #pragma unroll
-      for (int r = 0; r < RB; ++r)
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t b[4];
+          const int ch = 2 * kk + kch;
+          ldmatrix_x4(kt + kbase + uint32_t(ch >> 3) * 1024u + uint32_t(((ch & 7) ^ (krow & 7)) << 4), b);
+          mma_16816(c[0][kk & 1], q0[kk][0], q1[kk][0], q0[kk][1], q1[kk][1], b[0], b[1]);
+          mma_16816(c[1][kk & 1], q0[kk][0], q1[kk][0], q0[kk][1], q1[kk][1], b[2], b[3]);
+        }
+        uint32_t hi[RB][2], lo[RB][2];  // P of keys (0-7: 2t, 2t+1), (8-15: 2t, 2t+1) as A operands
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k)
+        for (int r = 0; r < RB; ++r) {
+          float x[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[r][k][e] = 0.f;
-      float m[RB], l[RB];
-#pragma unroll
-      for (int r = 0; r < RB; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-      }
-      for (int k = 0; k < n; ++k, ++use) {
-        const int st = int(use % kStages);
-        const bool got = mbar_wait(full(st), (use / kStages) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-        const int* mt = reinterpret_cast<const int*>(smem + SM::kOffMeta + st * 16);
-        const int valid = min(16, mt[key0 >> v.page_shift] - (key0 & (v.page - 1)));
-        const uint32_t kt = sbase + uint32_t(st) * 2u * SM::kTileBytes, vt = kt + SM::kTileBytes;
-        if (valid > 0) {
-          if (valid < 16) {
-            // zero the V rows behind the end
-            for (int r = key0 + valid; r < key0 + 16; ++r)
-              for (int h = 0; h < kHalves; ++h)
-                *reinterpret_cast<uint32_t*>(smem + size_t(st) * 2 * SM::kTileBytes + SM::kTileBytes +
-                                             (r >> 3) * (kHalves * 1024) + h * 1024 + (r & 7) * 128 + lane * 4) = 0u;
-            fence_proxy_async_smem();
-            __syncwarp();
+          for (int e = 0; e < 4; ++e) {
+            const int key = (e >> 1) * 8 + 2 * t + (e & 1);
+            x[e] = c[e >> 1][0][2 * r + (e & 1)] + c[e >> 1][1][2 * r + (e & 1)];
+            if (key >= valid) x[e] = -INFINITY;
           }
-          // S = Q K^T for 16 keys: two n-tiles, each in two accumulators
-          float c[2][2][4] = {};
+          float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.scale_log2;
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          if (__any_sync(0xffffffffu, mx > m[r] + kDecLazy)) {
+            const float mn = fmaxf(m[r], mx);
+            const float al = mn == -INFINITY ? 1.f : ex2_approx(m[r] - mn);
+            m[r] = mn;
+            l[r] *= al;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t b[4];
-            const int ch = 2 * kk + kch;
-            ldmatrix_x4(kt + kbase + uint32_t(ch >> 3) * 1024u + uint32_t(((ch & 7) ^ (krow & 7)) << 4), b);
-            mma_16816(c[0][kk & 1], q0[kk][0], q1[kk][0], q0[kk][1], q1[kk][1], b[0], b[1]);
-            mma_16816(c[1][kk & 1], q0[kk][0], q1[kk][0], q0[kk][1], q1[kk][1], b[2], b[3]);
+            for (int k8 = 0; k8 < D / 8; ++k8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[r][k8][e] *= al;
           }
-          uint32_t hi[RB][4], lo[RB][4];  // P of keys (0-7: 2t, 2t+1), (8-15: 2t, 2t+1) as A operands
+          const float ref = m[r] == -INFINITY ? 0.f : m[r];
+          float p[4];
 #pragma unroll
-          for (int r = 0; r < RB; ++r) {
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = (e >> 1) * 8 + 2 * t + (e & 1);
-              x[e] = c[e >> 1][0][2 * r + (e & 1)] + c[e >> 1][1][2 * r + (e & 1)];
-              if (key >= valid) x[e] = -INFINITY;
-            }
-            float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.scale_log2;
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            if (__any_sync(0xffffffffu, mx > m[r] + kDecLazy)) {
-              const float mn = fmaxf(m[r], mx);
-              const float al = mn == -INFINITY ? 1.f : ex2_approx(m[r] - mn);
-              m[r] = mn;
-              l[r] *= al;
-#pragma unroll
-              for (int k8 = 0; k8 < D / 8; ++k8)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[r][k8][e] *= al;
-            }
-            const float ref = m[r] == -INFINITY ? 0.f : m[r];
-            float p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              p[e] = ex2_approx(fmaf(x[e], a.scale_log2, -ref));
-              l[r] += p[e];
-            }
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              hi[r][z] = pack_bf16x2(p[2 * z], p[2 * z + 1]);
-              lo[r][z] = pack_bf16x2(p[2 * z] - __uint_as_float(hi[r][z] << 16),
-                                     p[2 * z + 1] - __uint_as_float(hi[r][z] & 0xFFFF0000u));
-            }
+          for (int e = 0; e < 4; ++e) {
+            p[e] = ex2_approx(fmaf(x[e], a.scale_log2, -ref));
+            l[r] += p[e];
           }
-          // O += P V: rows 0-7 the upper part of P, rows 8-15 the lower
 #pragma unroll
-          for (int np = 0; np < D / 16; ++np) {
-            uint32_t b[4];
-            const int ch = 2 * np + vch;
-            ldmatrix_x4_trans(vt + vbase + uint32_t(ch >> 3) * 1024u + uint32_t(((ch & 7) ^ (vrow & 7)) << 4), b);
-#pragma unroll
-            for (int r = 0; r < RB; ++r) {
-              mma_16816(o[r][2 * np], hi[r][0], lo[r][0], hi[r][1], lo[r][1], b[0], b[1]);
-              mma_16816(o[r][2 * np + 1], hi[r][0], lo[r][0], hi[r][1], lo[r][1], b[2], b[3]);
-            }
+          for (int z = 0; z < 2; ++z) {
+            hi[r][z] = pack_bf16x2(p[2 * z], p[2 * z + 1]);
+            lo[r][z] = pack_bf16x2(p[2 * z] - __uint_as_float(hi[r][z] << 16),
+                                   p[2 * z + 1] - __uint_as_float(hi[r][z] & 0xFFFF0000u));
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty(st));
+        // O += P V: rows 0-7 the upper part of P, rows 8-15 the lower; V rows
+        // behind the end count as zero
+        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (valid < 16) {
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            keep[z] = (z * 8 + 2 * t < valid ? 0xFFFFu : 0u) | (z * 8 + 2 * t + 1 < valid ? 0xFFFF0000u : 0u);
+        }
+#pragma unroll
+        for (int np = 0; np < D / 16; ++np) {
+          uint32_t b[4];
+          const int ch = 2 * np + vch;
+          ldmatrix_x4_trans(vt + vbase + uint32_t(ch >> 3) * 1024u + uint32_t(((ch & 7) ^ (vrow & 7)) << 4), b);
+          b[0] &= keep[0];
+          b[1] &= keep[1];
+          b[2] &= keep[0];
+          b[3] &= keep[1];
+#pragma unroll
+          for (int r = 0; r < RB; ++r) {
+            mma_16816(o[r][2 * np], hi[r][0], lo[r][0], hi[r][1], lo[r][1], b[0], b[1]);
+            mma_16816(o[r][2 * np + 1], hi[r][0], lo[r][0], hi[r][1], lo[r][1], b[2], b[3]);
+          }
+        }
       }
-      // join the four warps' results of this row (a warp that gave up comes too,
-      // and all of them learn of it)
-      asm volatile("bar.sync 1, 128;" ::: "memory");  // the buffer's last readers are done
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(st));
+      if (!(flags & kTileLast)) continue;
+
+      // join the four warps' results of this row
+      if (bar_any(1 + group, 128, false)) break;  // the buffer's last readers are done
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
         const int head = r * 8 + g;
-        if (t == 0) ml[warp * RB * 8 + head] = make_float2(m[r], l[r]);
-        float* dst = mrg + (warp * RB * 8 + head) * SM::kPitch + 2 * t;
+        if (t == 0) ml[gwarp * RB * 8 + head] = make_float2(m[r], l[r]);
+        float* dst = mrg + (gwarp * RB * 8 + head) * SM::kPitch + 2 * t;
 #pragma unroll
         for (int k = 0; k < D / 8; ++k)
           *reinterpret_cast<float2*>(dst + 8 * k) = make_float2(o[r][k][0] + o[r][k][2], o[r][k][1] + o[r][k][3]);
       }
-      ok = !bar_any(1, 128, !ok);
-      if (!ok) break;
-      const int64_t row = int64_t(s) * v.Hkv + hk;
-      const int slot = seg == 0 ? 0 : 1;  // a partial row is this CTA's first or its last
-      for (int e = threadIdx.x * 2; e < v.G * D; e += 256) {
+      if (bar_any(1 + group, 128, false)) break;
+      const bool whole = started && (flags & kRowEnd);
+      const int64_t row = mt.y;
+      const int slot = flags >> kTileRow == 0 ? 0 : 1;  // a partial row is this CTA's first or its last
+      for (int e = gthread * 2; e < v.G * D; e += 256) {
         const int head = e / D, i = e % D;
         float2 z[4];
         float mm = -INFINITY;
@@ -433,71 +544,64 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           if (i == 0) a.part_ml[at] = make_float2(mm, ll);
         }
       }
-      ++seg;
-      left -= n;
-      off = 0;
-      if (left > 0) ok = next_row();
     }
   }
 }
 
 // Joins the partial results of the rows that several CTAs share.  Block
-// (c, h) takes the row that CTA c's share starts inside of, if CTA c - 1's
-// share holds the row's first tile; one thread per output value and group of
-// parts.
-constexpr int kJoinGroups = 4;
+// (c - 1, h) takes head h of the row that CTA c's share begins inside of, if c
+// is the first such share; eight warps take every eighth part, four values a
+// lane.
+constexpr int kJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(D * kJoinGroups)
-    paged_join_kernel(const DecArgs a, int C, int heads_pad) {
-  __shared__ float so[kJoinGroups][D], sl[kJoinGroups], sm[kJoinGroups];
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ DecArgs a, int heads_pad) {
+  constexpr int kVec = D / 32;
+  __shared__ float so[kJoinWarps][D];
+  __shared__ float2 sml[kJoinWarps];
+  pdl_wait();
   const int c = blockIdx.x + 1, h = blockIdx.y;
   const DecMeta mt = a.meta[c];
-  if (mt.row < 0 || mt.off == 0) return;
-  const int64_t total = *a.total;
-  auto begin = [&](int k) { return total * k / C; };
-  const int64_t start = begin(c) - mt.off, end = start + mt.tiles;  // the row's tiles
-  if (begin(c - 1) > start) return;
-  int last = c;  // last CTA with a tile of the row
-  while (last + 1 < C && begin(last + 1) < end) ++last;
-  const int grp = threadIdx.x / D, i = threadIdx.x % D;
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int k = c - 1 + grp; k <= last; k += kJoinGroups) {
-    if (begin(k + 1) == begin(k)) continue;  // a CTA without work
-    const int slot = k == c - 1 && begin(k) != start ? 1 : 0;
-    const int64_t at = (int64_t(k) * 2 + slot) * heads_pad + h;
+  if (mt.row < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.f, o[kVec] = {};
+  for (int k = c - 1 + warp; k <= mt.last; k += kJoinWarps) {
+    const int64_t at = (int64_t(k) * 2 + (k == c - 1 ? mt.slot : 0)) * heads_pad + h;
     const float2 z = a.part_ml[at];
-    const float x = a.part_o[at * D + i];
+    float x[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2) {
+      const float2 y = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * kVec + i);
+      x[i] = y.x;
+      x[i + 1] = y.y;
+    }
     const float mm = fmaxf(m, z.x);
     if (mm != -INFINITY) {
       const float fa = ex2_approx(m - mm), fb = ex2_approx(z.x - mm);
       l = l * fa + z.y * fb;
-      o = o * fa + x * fb;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) o[i] = o[i] * fa + x[i] * fb;
       m = mm;
     }
   }
-  so[grp][i] = o;
-  if (i == 0) {
-    sl[grp] = l;
-    sm[grp] = m;
-  }
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) so[warp][lane * kVec + i] = o[i];
+  if (lane == 0) sml[warp] = make_float2(m, l);
   __syncthreads();
-  if (grp == 0) {
-    float mm = -INFINITY;
+  if (threadIdx.x >= D) return;
+  float mm = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < kJoinGroups; ++k) mm = fmaxf(mm, sm[k]);
-    float ll = 0.f, oo = 0.f;
-    if (mm != -INFINITY) {
+  for (int k = 0; k < kJoinWarps; ++k) mm = fmaxf(mm, sml[k].x);
+  float ll = 0.f, oo = 0.f;
+  if (mm != -INFINITY) {
 #pragma unroll
-      for (int k = 0; k < kJoinGroups; ++k) {
-        const float f = ex2_approx(sm[k] - mm);
-        ll += sl[k] * f;
-        oo += so[k][i] * f;
-      }
+    for (int k = 0; k < kJoinWarps; ++k) {
+      const float f = ex2_approx(sml[k].x - mm);
+      ll += sml[k].y * f;
+      oo += so[k][threadIdx.x] * f;
     }
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
-    a.O[(int64_t(mt.row) * a.v.G + h) * D + i] = __float2bfloat16(oo * inv);
   }
+  a.O[(int64_t(mt.row) * a.v.G + h) * D + threadIdx.x] = __float2bfloat16(ll > 0.f ? oo / ll : 0.f);
 }
 
 }  // namespace ab

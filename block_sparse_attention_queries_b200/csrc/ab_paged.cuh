@@ -337,70 +337,76 @@ __global__ void __launch_bounds__(256)
 // host knowing any length (C is the number of tiles where that is less).  Every
 // CTA sums the units' tiles itself.
 struct Share {
-  int unit;       // first unit with work
-  int off;        // first tile in it
-  int n;          // tiles of this CTA
-  int64_t begin;  // position of the first tile in the whole list
-  int64_t total;  // tiles of the whole list
+  int unit;   // first unit with work
+  int off;    // first tile in it
+  int n;      // tiles of this CTA
+  int begin;  // position of the first tile in the whole list
+  int total;  // tiles of the whole list (< 2^31: checked on the host)
 };
 
+// First tile of CTA c's share, of C CTAs with work.
+__device__ __forceinline__ int share_begin(int total, int C, int c) {
+  const int q = total / C, r = total - q * C;
+  return c * q + min(c, r);
+}
+// The CTA whose share holds tile x.
+__device__ __forceinline__ int share_of(int total, int C, int x) {
+  const int q = total / C, r = total - q * C;
+  return x < r * (q + 1) ? x / (q + 1) : r + (x - r * (q + 1)) / q;
+}
+
+__device__ __forceinline__ int warp_inclusive(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
 constexpr int kShareMaxUnits = 65536;
-constexpr int kShareSums = kShareMaxUnits / 32;  // 64-bit sums of 32 units each
+constexpr int kShareSums = kShareMaxUnits / 32;  // sums of 32 units each
 
 template <typename F>
-__device__ __forceinline__ Share share_work(F tiles, int n_units, int c, int C, int64_t* sums, Share* out) {
+__device__ __forceinline__ Share share_work(F tiles, int n_units, int c, int C, int* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int chunks = (n_units + 31) / 32;
-  auto warp_incl = [&](int64_t v) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
-    }
-    return v;
-  };
   for (int k = warp; k < chunks; k += warps) {
     const int u = k * 32 + lane;
-    const int64_t v = warp_incl(u < n_units ? int64_t(tiles(u)) : 0);
-    if (lane == 31) sums[k] = v;
+    const int v = __reduce_add_sync(0xffffffffu, u < n_units ? tiles(u) : 0);
+    if (lane == 0) sums[k] = v;
   }
   __syncthreads();
-  if (warp == 0) {
-    int64_t total = 0;
-    for (int k = lane; k < chunks; k += 32) total += sums[k];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    // total < 2^41 (2^16 units of at most 2^25 tiles) and C < 2^10
-    const int64_t n = total < C ? total : C;
-    const int64_t b = c < n ? total * c / n : total, e = c < n ? total * (c + 1) / n : total;
-    Share r{0, 0, int(e - b), b, total};
-    int64_t base = 0;
-    int chunk = 0;
-    for (int k0 = 0; k0 < chunks; k0 += 32) {
-      const int64_t w = k0 + lane < chunks ? sums[k0 + lane] : 0;
-      const int64_t incl = warp_incl(w);
-      const uint32_t past = __ballot_sync(0xffffffffu, base + incl > b);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        chunk = k0 + l;
-        base += __shfl_sync(0xffffffffu, incl - w, l);
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    const int u = chunk * 32 + lane;
-    const int64_t w = u < n_units ? int64_t(tiles(u)) : 0;
-    const int64_t incl = warp_incl(w);
-    const uint32_t past = __ballot_sync(0xffffffffu, base + incl > b);
-    if (past) {  // none: b == total, no work
+  // every warp works its CTA's share out by itself
+  int total = 0;
+  for (int k = lane; k < chunks; k += 32) total += sums[k];
+  total = __reduce_add_sync(0xffffffffu, total);
+  const int n = min(total, C);
+  Share r{0, 0, 0, total, total};
+  if (c >= n) return r;
+  r.begin = share_begin(total, n, c);
+  r.n = share_begin(total, n, c + 1) - r.begin;
+  int base = 0, chunk = 0;
+  for (int k0 = 0; k0 < chunks; k0 += 32) {
+    const int w = k0 + lane < chunks ? sums[k0 + lane] : 0;
+    const int incl = warp_inclusive(w);
+    const uint32_t past = __ballot_sync(0xffffffffu, base + incl > r.begin);
+    if (past) {
       const int l = __ffs(past) - 1;
-      r.unit = chunk * 32 + l;
-      r.off = int(b - (base + __shfl_sync(0xffffffffu, incl - w, l)));
+      chunk = k0 + l;
+      base += __shfl_sync(0xffffffffu, incl - w, l);
+      break;
     }
-    if (lane == 0) *out = r;
+    base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  __syncthreads();
-  return *out;
+  const int u = chunk * 32 + lane;
+  const int w = u < n_units ? tiles(u) : 0;
+  const int incl = warp_inclusive(w);
+  const int l = __ffs(__ballot_sync(0xffffffffu, base + incl > r.begin)) - 1;
+  r.unit = chunk * 32 + max(l, 0);
+  r.off = r.begin - (base + __shfl_sync(0xffffffffu, incl - w, max(l, 0)));
+  return r;
 }
 
 // First unit from u on with tiles, n_units if there is none; whole warps, 32
@@ -456,15 +462,14 @@ struct SelectArgs {
 template <int D>
 __global__ void __launch_bounds__(kSelThreads, 4) page_score_kernel(const SelectArgs a) {
   constexpr int kPieces = D / 32;  // 16-byte pieces of a summary per lane
-  __shared__ int64_t sums[kShareSums / 8];
-  __shared__ Share share_out;
+  __shared__ int sums[kMaxSeqs / 32];
   __shared__ float2 wpart[4][kMaxGroup];
   const PagedView& v = a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   auto chunks_of = [&](int s) { return (pages_of(v, seq_len(v, s)) + kSelPages - 1) / kSelPages; };
   auto tiles = [&](int s) { return query_row(v, s) < 0 ? 0 : chunks_of(s) * v.Hkv; };
-  const Share sh = share_work(tiles, v.S, blockIdx.x, gridDim.x, sums, &share_out);
+  const Share sh = share_work(tiles, v.S, blockIdx.x, gridDim.x, sums);
   int s = sh.unit, off = sh.off;
   for (int left = sh.n; left > 0; --left, ++off) {
     if (off >= tiles(s)) {

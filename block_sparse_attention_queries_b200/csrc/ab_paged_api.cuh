@@ -207,6 +207,9 @@ ab_status check_paged(const ab_paged_params* p) {
   if (int64_t(p->num_pages) * p->page > INT_MAX || int64_t(p->num_pages) * p->Hkv > INT_MAX) return AB_ERR_INVALID_ARG;
   if (p->S > kMaxSeqs || p->Hq / p->Hkv > kMaxGroup || int64_t(p->S) * p->Hkv > kShareMaxUnits)
     return AB_ERR_UNSUPPORTED;
+  // positions in the list of all tiles of 64 keys stay in 32 bits
+  if (int64_t(p->S) * p->Hkv * ((int64_t(p->max_pages) * p->page + kDecTile - 1) / kDecTile) > INT_MAX)
+    return AB_ERR_UNSUPPORTED;
   return AB_OK;
 }
 

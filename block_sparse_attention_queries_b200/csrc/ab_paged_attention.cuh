@@ -16,9 +16,10 @@
 //  - one warp plans 32 tiles at a time, a lane for each: the tile's row, its
 //    pages through the lists and the block table.  All lookups of 32 tiles run
 //    side by side, so that rows of a single tile cost no more than long ones;
-//  - one warp brings the planned tiles into a ring of shared-memory stages by
-//    TMA (a page of a head is one box of 2 to 16 KB), with the row's queries
-//    where a row begins;
+//  - three warps bring the planned tiles into a ring of shared-memory stages:
+//    keys and values by TMA (a page of a head is one box of 2 to 16 KB), and the
+//    row's queries where a row begins.  One warp for all three took 1300 cycles
+//    to issue a tile of 16-token pages, longer than its bytes take;
 //  - groups of four warps take the rows in turn (two groups for G <= 8, so that
 //    one row's start and end, about 2500 cycles, overlap the next one's tiles);
 //    a group's warps take 16 keys of each tile each, with a softmax state of
@@ -36,9 +37,10 @@
 
 namespace ab {
 
-// groups of four consumer warps, the TMA warp, the planning warp
+// groups of four consumer warps; warps that copy keys, values and queries; the
+// planning warp
 __host__ __device__ constexpr int dec_groups(int RB) { return RB == 1 ? 2 : 1; }
-__host__ __device__ constexpr int dec_threads(int RB) { return dec_groups(RB) * 128 + 64; }
+__host__ __device__ constexpr int dec_threads(int RB) { return dec_groups(RB) * 128 + 128; }
 constexpr int kDecTile = 64;       // keys per tile
 constexpr int kDecMaxParts = 1024; // CTAs at most
 constexpr float kDecLazy = 8.f;    // log2 slack of the reference maximum
@@ -94,7 +96,7 @@ struct DecSmem {
   static constexpr int kBytes = kOffMisc + 64;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 232448, "more shared memory than a CTA may have");
-  static_assert(kOffQ >= kShareSums * 8, "share_work's sums lie in the stages");
+  static_assert(kOffQ >= kShareSums * 4, "share_work's sums lie in the stages");
 };
 
 template <bool kLists>
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
   using Rows = DecRows<kLists>;
   constexpr int kStages = SM::kStages;
   constexpr int kHalves = D / 64;
-  constexpr int kGroups = dec_groups(RB), kTmaWarp = 4 * kGroups, kPlanWarp = kTmaWarp + 1;
+  constexpr int kGroups = dec_groups(RB), kCopyWarp = 4 * kGroups, kPlanWarp = kCopyWarp + 3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -167,34 +169,30 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
   auto plan_full = [&](int k) { return full(kStages + k); };
   auto plan_empty = [&](int k) { return empty(kStages + k); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::kOffMisc);
-  Share* share_out = reinterpret_cast<Share*>(smem + SM::kOffMisc + 16);
   DecTile* plan = reinterpret_cast<DecTile*>(smem + SM::kOffPlan);
   // the prefix sums' scratch: stage memory that no copy has been issued into yet
-  int64_t* sums = reinterpret_cast<int64_t*>(smem);
+  int* sums = reinterpret_cast<int*>(smem);
   const PagedView& v = a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages; ++k) {
-      mbar_init(full(k), 1);
+      mbar_init(full(k), 3);
       mbar_init(empty(k), 4 * kGroups);
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(plan_full(k), 1);
-      mbar_init(plan_empty(k), 1);
+      mbar_init(plan_empty(k), 3);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kTmaWarp && lane == 0) {
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
-  }
+  if (warp == kCopyWarp && lane == 0) prefetch_tmap(&tmK);
+  if (warp == kCopyWarp + 1 && lane == 0) prefetch_tmap(&tmV);
   pdl_wait();
   pdl_trigger();
   const int n_units = kLists ? v.S * v.Hkv : v.S;
-  const Share sh =
-      share_work([&](int u) { return Rows::unit_tiles(a, u); }, n_units, blockIdx.x, gridDim.x, sums, share_out);
+  const Share sh = share_work([&](int u) { return Rows::unit_tiles(a, u); }, n_units, blockIdx.x, gridDim.x, sums);
   fence_proxy_async_smem();  // the scratch's generic accesses come before the copies into it
   __syncthreads();
 
@@ -210,27 +208,19 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
       bool open = base + lane < sh.n;
       for (int u0 = unit; __any_sync(0xffffffffu, open) && u0 < n_units; u0 += 32) {
         const int t = u0 + lane < n_units ? Rows::unit_tiles(a, u0 + lane) : 0;
-        int64_t incl = t;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
+        const int incl = warp_inclusive(t), all = __shfl_sync(0xffffffffu, incl, 31);
         int l = 0;  // first unit of these 32 whose sum passes x
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const int64_t y = __shfl_sync(0xffffffffu, incl, l + o - 1);
-          if (y <= x) l += o;
-        }
-        const int64_t before = __shfl_sync(0xffffffffu, incl - t, l & 31);
+        for (int o = 16; o > 0; o >>= 1)
+          if (__shfl_sync(0xffffffffu, incl, l + o - 1) <= x) l += o;
+        const int before = __shfl_sync(0xffffffffu, incl - t, l);
         if (open) {
           if (x < all) {
             mine = u0 + l;
-            x -= int(before);
+            x -= before;
             open = false;
           } else {
-            x -= int(all);
+            x -= all;
           }
         }
       }
@@ -289,9 +279,12 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
       pos = __shfl_sync(0xffffffffu, x, 31) + 1;
       if (unit < 0) break;  // the share's last batch
     }
-  } else if (warp == kTmaWarp) {
-    // ----------------------------------------------------------------- TMA
+  } else if (warp >= kCopyWarp) {
+    // ------------------------------------------------- copies: K, V, queries
+    const int what = warp - kCopyWarp;
+    const int per_tile = kDecTile >> v.page_shift;
     const uint32_t page_bytes = uint32_t(SM::kRow) << v.page_shift;
+    const CUtensorMap* tm = what == 0 ? &tmK : &tmV;
     uint32_t use = 0;  // tiles issued
     bool ok = true;
     for (int base = 0, batch = 0; base < sh.n && ok; base += 32, ++batch) {
@@ -299,28 +292,33 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
       const int n = min(32, sh.n - base);
       for (int k = 0; k < n && ok; ++k, ++use) {
         const DecTile* d = plan + (batch & 1) * 32 + k;
-        const int coord = lane < 4 ? d->coord[lane] : -1;
-        const int flags = d->flags;
         const int st = int(use % kStages);
         ok = lane0_wait(empty(st), ((use / kStages) & 1) ^ 1, abort_flag);
         if (!ok) break;
-        const uint32_t there = __ballot_sync(0xffffffffu, coord >= 0);
         if (lane == 0) {
-          *reinterpret_cast<int4*>(smem + SM::kOffMeta + st * 16) = make_int4(d->valid, d->row, flags, 0);
-          mbar_arrive_expect_tx(full(st), 2u * page_bytes * uint32_t(__popc(there)) +
-                                              ((flags & kTileFirst) ? uint32_t(v.G * SM::kRow) : 0u));
+          const int flags = d->flags;
+          if (what < 2) {
+            const int4 at = *reinterpret_cast<const int4*>(d->coord);
+            const int coord[4] = {at.x, at.y, at.z, at.w};
+            int n_pages = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) n_pages += coord[e] >= 0 ? 1 : 0;
+            if (what == 0) *reinterpret_cast<int4*>(smem + SM::kOffMeta + st * 16) = make_int4(d->valid, d->row, flags, 0);
+            mbar_arrive_expect_tx(full(st), page_bytes * uint32_t(n_pages));
+            const uint32_t dst = sbase + uint32_t(st) * 2u * SM::kTileBytes + uint32_t(what) * SM::kTileBytes;
+            for (int e = 0; e < per_tile; ++e)
+              if (coord[e] >= 0) tma_load_5d(dst + uint32_t(e) * page_bytes, tm, full(st), 0, 0, 0, 0, coord[e]);
+          } else if (flags & kTileFirst) {
+            const int hk = d->row % v.Hkv;
+            const __nv_bfloat16* q = a.Q + (int64_t(d->qrow) * v.Hkv + hk) * v.G * D;
+            mbar_arrive_expect_tx(full(st), uint32_t(v.G * SM::kRow));
+            for (int h = 0; h < v.G; ++h)
+              bulk_load(sbase + SM::kOffQ + uint32_t(st * SM::kQBytes + h * SM::kQPitch), q + h * D, SM::kRow, full(st));
+          } else {
+            mbar_arrive(full(st));
+          }
         }
         __syncwarp();
-        if (coord >= 0) {
-          const uint32_t dst = sbase + uint32_t(st) * 2u * SM::kTileBytes + uint32_t(lane) * page_bytes;
-          tma_load_5d(dst, &tmK, full(st), 0, 0, 0, 0, coord);
-          tma_load_5d(dst + SM::kTileBytes, &tmV, full(st), 0, 0, 0, 0, coord);
-        }
-        if ((flags & kTileFirst) && lane < v.G) {
-          const int hk = d->row % v.Hkv;
-          bulk_load(sbase + SM::kOffQ + uint32_t(st * SM::kQBytes + lane * SM::kQPitch),
-                    a.Q + ((int64_t(d->qrow) * v.Hkv + hk) * v.G + lane) * D, SM::kRow, full(st));
-        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(plan_empty(batch & 1));
@@ -349,11 +347,11 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
           hk = off / T;
           off -= hk * T;
         }
-        const int64_t C = sh.total < gridDim.x ? sh.total : int64_t(gridDim.x);
-        const int64_t start = sh.begin - off, prev = sh.total * (int(blockIdx.x) - 1) / C;
+        const int C = min(sh.total, int(gridDim.x));
+        const int start = sh.begin - off, prev = share_begin(sh.total, C, blockIdx.x - 1);
         if (off > 0 && prev <= start) {
           mt.row = s * v.Hkv + hk;
-          mt.last = int(((start + T) * C + sh.total - 1) / sh.total) - 1;  // the last whose begin is below the row's end
+          mt.last = share_of(sh.total, C, start + T - 1);
           mt.slot = prev == start ? 0 : 1;
         }
       }
@@ -516,7 +514,7 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
       const bool whole = started && (flags & kRowEnd);
       const int64_t row = mt.y;
       const int slot = flags >> kTileRow == 0 ? 0 : 1;  // a partial row is this CTA's first or its last
-      for (int e = gthread * 2; e < v.G * D; e += 256) {
+      for (int e = gthread * 4; e < v.G * D; e += 512) {
         const int head = e / D, i = e % D;
         float2 z[4];
         float mm = -INFINITY;
@@ -526,21 +524,25 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
           mm = fmaxf(mm, z[w].x);
         }
         const float ref = mm == -INFINITY ? 0.f : mm;
-        float ll = 0.f, o0 = 0.f, o1 = 0.f;
+        float ll = 0.f;
+        float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const float f = ex2_approx(z[w].x - ref);
-          const float2 ow = *reinterpret_cast<const float2*>(mrg + (w * RB * 8 + head) * SM::kPitch + i);
+          const float4 ow = *reinterpret_cast<const float4*>(mrg + (w * RB * 8 + head) * SM::kPitch + i);
           ll += z[w].y * f;
-          o0 += ow.x * f;
-          o1 += ow.y * f;
+          s4.x += ow.x * f;
+          s4.y += ow.y * f;
+          s4.z += ow.z * f;
+          s4.w += ow.w * f;
         }
         if (whole) {
           const float inv = ll > 0.f ? 1.f / ll : 0.f;
-          *reinterpret_cast<uint32_t*>(a.O + (row * v.G + head) * D + i) = pack_bf16x2(o0 * inv, o1 * inv);
+          *reinterpret_cast<uint2*>(a.O + (row * v.G + head) * D + i) =
+              make_uint2(pack_bf16x2(s4.x * inv, s4.y * inv), pack_bf16x2(s4.z * inv, s4.w * inv));
         } else {
           const int64_t at = (int64_t(blockIdx.x) * 2 + slot) * (RB * 8) + head;
-          *reinterpret_cast<float2*>(a.part_o + at * D + i) = make_float2(o0, o1);
+          *reinterpret_cast<float4*>(a.part_o + at * D + i) = s4;
           if (i == 0) a.part_ml[at] = make_float2(mm, ll);
         }
       }

@@ -331,29 +331,20 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------- an even share of ragged work
-// The work is a list of units (sequences, or rows of lists) of tiles(u) equal
-// tiles.  CTA c of C takes the tiles [c total / C, (c + 1) total / C) of the
-// whole list, whatever the units' lengths, so the load is even without the
-// host knowing any length (C is the number of tiles where that is less).  Every
-// CTA sums the units' tiles itself.
+// The work is a list of units, each of `rows` rows of `tiles` equal tiles.  A
+// row costs two for each tile and `row_cost` besides; CTA c of C takes the tiles
+// between c / C and (c + 1) / C of the whole cost, whatever the units' lengths,
+// so the load is even without the host knowing any length.  Every CTA sums the
+// units itself.
+struct UnitWork {
+  int rows, tiles;  // tiles of each row
+};
 struct Share {
   int unit;   // first unit with work
-  int off;    // first tile in it
+  int off;    // first tile in it (may be one past its last: the next unit then)
   int n;      // tiles of this CTA
   int begin;  // position of the first tile in the whole list
-  int total;  // tiles of the whole list (< 2^31: checked on the host)
 };
-
-// First tile of CTA c's share, of C CTAs with work.
-__device__ __forceinline__ int share_begin(int total, int C, int c) {
-  const int q = total / C, r = total - q * C;
-  return c * q + min(c, r);
-}
-// The CTA whose share holds tile x.
-__device__ __forceinline__ int share_of(int total, int C, int x) {
-  const int q = total / C, r = total - q * C;
-  return x < r * (q + 1) ? x / (q + 1) : r + (x - r * (q + 1)) / q;
-}
 
 __device__ __forceinline__ int warp_inclusive(int v) {
   const int lane = threadIdx.x & 31;
@@ -366,47 +357,67 @@ __device__ __forceinline__ int warp_inclusive(int v) {
 }
 
 constexpr int kShareMaxUnits = 65536;
-constexpr int kShareSums = kShareMaxUnits / 32;  // sums of 32 units each
+constexpr int kShareSums = kShareMaxUnits / 32;  // pairs of sums over 32 units each
 
+// Sums stay below 2^31: the host limits the tiles of a full table to 2^29.
 template <typename F>
-__device__ __forceinline__ Share share_work(F tiles, int n_units, int c, int C, int* sums) {
+__device__ __forceinline__ Share share_work(F work, int row_cost, int n_units, int c, int C, int2* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int chunks = (n_units + 31) / 32;
+  auto cost_of = [&](const UnitWork& w) { return w.tiles > 0 ? w.rows * (2 * w.tiles + row_cost) : 0; };
   for (int k = warp; k < chunks; k += warps) {
     const int u = k * 32 + lane;
-    const int v = __reduce_add_sync(0xffffffffu, u < n_units ? tiles(u) : 0);
-    if (lane == 0) sums[k] = v;
+    const UnitWork w = u < n_units ? work(u) : UnitWork{0, 0};
+    const int cost = __reduce_add_sync(0xffffffffu, cost_of(w));
+    const int tiles = __reduce_add_sync(0xffffffffu, w.rows * w.tiles);
+    if (lane == 0) sums[k] = make_int2(cost, tiles);
   }
   __syncthreads();
   // every warp works its CTA's share out by itself
-  int total = 0;
-  for (int k = lane; k < chunks; k += 32) total += sums[k];
-  total = __reduce_add_sync(0xffffffffu, total);
-  const int n = min(total, C);
-  Share r{0, 0, 0, total, total};
-  if (c >= n) return r;
-  r.begin = share_begin(total, n, c);
-  r.n = share_begin(total, n, c + 1) - r.begin;
-  int base = 0, chunk = 0;
-  for (int k0 = 0; k0 < chunks; k0 += 32) {
-    const int w = k0 + lane < chunks ? sums[k0 + lane] : 0;
-    const int incl = warp_inclusive(w);
-    const uint32_t past = __ballot_sync(0xffffffffu, base + incl > r.begin);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      chunk = k0 + l;
-      base += __shfl_sync(0xffffffffu, incl - w, l);
-      break;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+  int total = 0, total_tiles = 0;
+  for (int k = lane; k < chunks; k += 32) {
+    total += sums[k].x;
+    total_tiles += sums[k].y;
   }
-  const int u = chunk * 32 + lane;
-  const int w = u < n_units ? tiles(u) : 0;
-  const int incl = warp_inclusive(w);
-  const int l = __ffs(__ballot_sync(0xffffffffu, base + incl > r.begin)) - 1;
-  r.unit = chunk * 32 + max(l, 0);
-  r.off = r.begin - (base + __shfl_sync(0xffffffffu, incl - w, max(l, 0)));
-  return r;
+  total = __reduce_add_sync(0xffffffffu, total);
+  total_tiles = __reduce_add_sync(0xffffffffu, total_tiles);
+  // the first tile at or behind cost p: its unit, place in the unit, place in the list
+  auto locate = [&](int p, int& unit, int& off) -> int {
+    unit = n_units;
+    off = 0;
+    if (p >= total) return total_tiles;
+    int base = 0, before = 0, chunk = 0;
+    for (int k0 = 0; k0 < chunks; k0 += 32) {
+      const int2 w = k0 + lane < chunks ? sums[k0 + lane] : make_int2(0, 0);
+      const int incl = warp_inclusive(w.x), tiles = warp_inclusive(w.y);
+      const uint32_t past = __ballot_sync(0xffffffffu, base + incl > p);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        chunk = k0 + l;
+        base += __shfl_sync(0xffffffffu, incl - w.x, l);
+        before += __shfl_sync(0xffffffffu, tiles - w.y, l);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+      before += __shfl_sync(0xffffffffu, tiles, 31);
+    }
+    const int u = chunk * 32 + lane;
+    const UnitWork w = u < n_units ? work(u) : UnitWork{0, 0};
+    const int cost = cost_of(w), incl = warp_inclusive(cost), tiles = warp_inclusive(w.rows * w.tiles);
+    const int l = __ffs(__ballot_sync(0xffffffffu, base + incl > p) | 0x80000000u) - 1;
+    const int rest = p - base - __shfl_sync(0xffffffffu, incl - cost, l);
+    const int T = __shfl_sync(0xffffffffu, w.tiles, l);
+    const int row = rest / (2 * T + row_cost), x = rest - row * (2 * T + row_cost);
+    unit = chunk * 32 + l;
+    off = row * T + min((x + 1) / 2, T);
+    return before + __shfl_sync(0xffffffffu, tiles - w.rows * w.tiles, l) + off;
+  };
+  const int q = total / C, r = total - q * C;
+  Share s;
+  int unit, off;
+  s.begin = locate(c * q + min(c, r), s.unit, s.off);
+  s.n = locate((c + 1) * q + min(c + 1, r), unit, off) - s.begin;
+  return s;
 }
 
 // First unit from u on with tiles, n_units if there is none; whole warps, 32
@@ -462,14 +473,15 @@ struct SelectArgs {
 template <int D>
 __global__ void __launch_bounds__(kSelThreads, 4) page_score_kernel(const SelectArgs a) {
   constexpr int kPieces = D / 32;  // 16-byte pieces of a summary per lane
-  __shared__ int sums[kMaxSeqs / 32];
+  __shared__ int2 sums[kMaxSeqs / 32];
   __shared__ float2 wpart[4][kMaxGroup];
   const PagedView& v = a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   auto chunks_of = [&](int s) { return (pages_of(v, seq_len(v, s)) + kSelPages - 1) / kSelPages; };
   auto tiles = [&](int s) { return query_row(v, s) < 0 ? 0 : chunks_of(s) * v.Hkv; };
-  const Share sh = share_work(tiles, v.S, blockIdx.x, gridDim.x, sums);
+  const Share sh =
+      share_work([&](int s) { return UnitWork{1, tiles(s)}; }, 0, v.S, blockIdx.x, gridDim.x, sums);
   int s = sh.unit, off = sh.off;
   for (int left = sh.n; left > 0; --left, ++off) {
     if (off >= tiles(s)) {

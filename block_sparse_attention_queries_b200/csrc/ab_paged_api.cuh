@@ -207,8 +207,8 @@ ab_status check_paged(const ab_paged_params* p) {
   if (int64_t(p->num_pages) * p->page > INT_MAX || int64_t(p->num_pages) * p->Hkv > INT_MAX) return AB_ERR_INVALID_ARG;
   if (p->S > kMaxSeqs || p->Hq / p->Hkv > kMaxGroup || int64_t(p->S) * p->Hkv > kShareMaxUnits)
     return AB_ERR_UNSUPPORTED;
-  // positions in the list of all tiles of 64 keys stay in 32 bits
-  if (int64_t(p->S) * p->Hkv * ((int64_t(p->max_pages) * p->page + kDecTile - 1) / kDecTile) > INT_MAX)
+  // positions in the list of all tiles of 64 keys, and their cost, stay in 32 bits
+  if (int64_t(p->S) * p->Hkv * ((int64_t(p->max_pages) * p->page + 63) / 64) > INT_MAX / 4)
     return AB_ERR_UNSUPPORTED;
   return AB_OK;
 }
@@ -334,30 +334,28 @@ ab_status run_paged_topk(const ab_paged_params* p, const float* P, const int32_t
 }
 
 template <int D, int RB, bool kLists>
-ab_status launch_paged_attention(const DecArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int grid,
-                                 cudaStream_t st) {
+ab_status launch_paged_attention(const DecArgs& a, int grid, cudaStream_t st) {
   auto kern = paged_attention_kernel<D, RB, kLists>;
   constexpr int smem = DecSmem<D, RB>::kAlloc;
   if (set_smem(kern, smem) != cudaSuccess) return AB_ERR_CUDA;
-  kern<<<unsigned(grid), dec_threads(RB), smem, st>>>(tmK, tmV, a);
+  kern<<<unsigned(grid), dec_threads(RB), smem, st>>>(a);
   if (launch_status() != AB_OK) return AB_ERR_CUDA;
   if (grid == 1) return AB_OK;
-  return launch_after(paged_join_kernel<D>, dim3(unsigned(grid - 1), unsigned(a.v.G)), 32 * kJoinWarps, 0, st, a, RB * 8);
+  return launch_after(paged_join_kernel<D>, dim3(unsigned(grid - 1), unsigned(a.v.G)), 32 * kJoinWarps, 0, st, a, grid,
+                      RB * 8);
 }
 
 ab_status run_paged_attention(const ab_paged_params* p, const PagedView& v, const void* Q, const void* Kc,
                               const void* Vc, const int32_t* idx, const int32_t* count, void* O, uint8_t* ws,
                               cudaStream_t st) {
   const PagedWorkspace w = paged_workspace(p);
-  CUtensorMap tmK, tmV;
-  const uint64_t rows = uint64_t(p->num_pages) * p->Hkv;
-  if (!make_map_grouped(&tmK, Kc, uint64_t(p->d), uint64_t(p->page), rows, uint32_t(p->page / 8))) return AB_ERR_CUDA;
-  if (!make_map_grouped(&tmV, Vc, uint64_t(p->d), uint64_t(p->page), rows, uint32_t(p->page / 8))) return AB_ERR_CUDA;
   const int sms = sm_count();
   if (!sms) return AB_ERR_CUDA;
   DecArgs a{};
   a.v = v;
   a.Q = static_cast<const __nv_bfloat16*>(Q);
+  a.K = static_cast<const __nv_bfloat16*>(Kc);
+  a.V = static_cast<const __nv_bfloat16*>(Vc);
   a.idx = idx;
   a.count = count;
   a.O = static_cast<__nv_bfloat16*>(O);
@@ -368,8 +366,8 @@ ab_status run_paged_attention(const ab_paged_params* p, const PagedView& v, cons
   const int grid = sms < kDecMaxParts ? sms : kDecMaxParts;
   auto by_lists = [&](auto dd, auto rb) -> ab_status {
     constexpr int D = decltype(dd)::value, RB = decltype(rb)::value;
-    return idx ? launch_paged_attention<D, RB, true>(a, tmK, tmV, grid, st)
-               : launch_paged_attention<D, RB, false>(a, tmK, tmV, grid, st);
+    return idx ? launch_paged_attention<D, RB, true>(a, grid, st)
+               : launch_paged_attention<D, RB, false>(a, grid, st);
   };
   using T128 = std::integral_constant<int, 128>;
   using T64 = std::integral_constant<int, 64>;

@@ -9,21 +9,23 @@
 // Each key and value is read once for the G query heads that share it: 2 G
 // products per 2-byte element, far below what the tensor cores need per byte,
 // so the bound is memory bandwidth and the design keeps bytes in flight:
-//  - the (sequence, key/value head) rows are cut into tiles of 64 keys and the
-//    whole list of tiles is divided evenly among persistent CTAs, whatever the
-//    lengths (share_work); a row that several CTAs share is joined from their
-//    partial results by a second kernel;
+//  - the (sequence, key/value head) rows are cut into tiles of 64 keys (128 for
+//    d = 64) and the whole list of tiles is divided evenly among persistent
+//    CTAs, whatever the lengths (share_work; a row's start and end count as half
+//    a tile); a row that several CTAs share is joined from their partial results
+//    by a second kernel;
 //  - one warp plans 32 tiles at a time, a lane for each: the tile's row, its
 //    pages through the lists and the block table.  All lookups of 32 tiles run
 //    side by side, so that rows of a single tile cost no more than long ones;
-//  - three warps bring the planned tiles into a ring of shared-memory stages:
-//    keys and values by TMA (a page of a head is one box of 2 to 16 KB), and the
-//    row's queries where a row begins.  One warp for all three took 1300 cycles
-//    to issue a tile of 16-token pages, longer than its bytes take;
+//  - three warps bring the planned tiles into a ring of shared-memory stages, 16
+//    bytes a lane and copy, only the rows that hold keys, and the row's queries
+//    where a row begins.  (By TMA a tile of four 4 KB boxes each of K and V took
+//    1000 cycles, one of 2 KB boxes about as long: at most 32 bytes a cycle and
+//    about 100 cycles a box, where HBM needs 23 bytes a cycle.);
 //  - groups of four warps take the rows in turn (two groups for G <= 8, so that
 //    one row's start and end, about 2500 cycles, overlap the next one's tiles);
-//    a group's warps take 16 keys of each tile each, with a softmax state of
-//    their own, joined once per row.
+//    a group's warps take 16 (32) keys of each tile each, with a softmax state
+//    of their own, joined once per row.
 //
 // The G heads are the rows of an m16n8k16 product.  P is used as the sum of two
 // bfloat16 numbers, so that its rounding (2^-17) does not show next to the
@@ -33,6 +35,7 @@
 // operand, since 0 times what an unwritten page holds may be NaN.
 #pragma once
 
+#include "ab_norm_rope.cuh"
 #include "ab_paged.cuh"
 
 namespace ab {
@@ -41,30 +44,33 @@ namespace ab {
 // planning warp
 __host__ __device__ constexpr int dec_groups(int RB) { return RB == 1 ? 2 : 1; }
 __host__ __device__ constexpr int dec_threads(int RB) { return dec_groups(RB) * 128 + 128; }
-constexpr int kDecTile = 64;       // keys per tile
+// keys per tile: 32 KB of keys and values
+__host__ __device__ constexpr int dec_tile(int D) { return D == 128 ? 64 : 128; }
+constexpr int kDecRowCost = 1;     // a row's start and end, in halves of a tile
 constexpr int kDecMaxParts = 1024; // CTAs at most
 constexpr float kDecLazy = 8.f;    // log2 slack of the reference maximum
 
-// Where CTA c's share starts, for the joining kernel: the row whose parts the
-// CTAs c - 1 to `last` hold if c is the first share that begins inside of it,
-// else -1; `slot`: where CTA c - 1 has put its part.
+// A CTA's share, for the joining kernel: its tiles [begin, begin + n) of the
+// list, and the row that begins in it and ends behind it (-1: none), that row's
+// end in the list, and which of the CTA's two parts it is.
 struct DecMeta {
-  int row, last, slot, pad;
+  int begin, n, row, end, slot, pad[3];
 };
 
 // A planned tile.
 struct DecTile {
-  int coord[4];  // page * Hkv + head of up to 4 pages, -1: none
-  int valid;     // valid keys of each, a byte each
+  int coord[8];  // page * Hkv + head of up to 8 pages, -1: none
+  int valid[2];  // valid keys of each, a byte each
   int row;       // s * Hkv + key/value head
   int qrow;      // row of Q
   int flags;
+  int pad[3];
 };
 enum : int { kTileFirst = 1, kTileLast = 2, kRowStart = 4, kRowEnd = 8, kTileRow = 4 /* shift: rows begun before */ };
 
 struct DecArgs {
   PagedView v;
-  const __nv_bfloat16* Q;    // [T, Hq, d]
+  const __nv_bfloat16 *Q, *K, *V;  // [T, Hq, d], [num_pages, Hkv, page, d]
   const int32_t* idx;        // [S, Hkv, max_pages] or null
   const int32_t* count;      // [S, Hkv]
   __nv_bfloat16* O;          // [S, Hq, d]
@@ -77,9 +83,10 @@ struct DecArgs {
 template <int D, int RB>
 struct DecSmem {
   static constexpr int kRow = D * 2;
-  static constexpr int kTileBytes = kDecTile * kRow;  // one of K, V
+  static constexpr int kTile = dec_tile(D);
+  static constexpr int kTileBytes = kTile * kRow;     // one of K, V
   static constexpr int kGroups = dec_groups(RB);
-  static constexpr int kStages = D == 128 ? 5 : (RB == 1 ? 10 : 9);
+  static constexpr int kStages = 5;
   static constexpr int kPitch = D + 8;                // floats; rows of a quad's lanes in different banks
   static constexpr int kQPitch = kRow + 16;           // bytes, for the same reason
   static constexpr int kQBytes = RB * 8 * kQPitch;
@@ -96,10 +103,10 @@ struct DecSmem {
   static constexpr int kBytes = kOffMisc + 64;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kAlloc <= 232448, "more shared memory than a CTA may have");
-  static_assert(kOffQ >= kShareSums * 4, "share_work's sums lie in the stages");
+  static_assert(kOffQ >= kShareSums * 8, "share_work's sums lie in the stages");
 };
 
-template <bool kLists>
+template <int D, bool kLists>
 struct DecRows {
   // list entries (pages) of a row
   static __device__ __forceinline__ int row_entries(const DecArgs& a, int s, int hk) {
@@ -116,12 +123,12 @@ struct DecRows {
     return pages_of(v, seq_len(v, s));
   }
   static __device__ __forceinline__ int tiles_of(const DecArgs& a, int entries) {
-    return ((entries << a.v.page_shift) + kDecTile - 1) / kDecTile;
+    return ((entries << a.v.page_shift) + dec_tile(D) - 1) / dec_tile(D);
   }
-  // tiles of unit u: a row of the lists, or a sequence with all of its heads
-  static __device__ __forceinline__ int unit_tiles(const DecArgs& a, int u) {
-    if constexpr (kLists) return tiles_of(a, row_entries(a, u / a.v.Hkv, u % a.v.Hkv));
-    return tiles_of(a, row_entries(a, u, 0)) * a.v.Hkv;
+  // unit u: a row of the lists, or a sequence with all of its heads
+  static __device__ __forceinline__ UnitWork work(const DecArgs& a, int u) {
+    if constexpr (kLists) return {1, tiles_of(a, row_entries(a, u / a.v.Hkv, u % a.v.Hkv))};
+    return {a.v.Hkv, tiles_of(a, row_entries(a, u, 0))};
   }
 };
 
@@ -150,14 +157,18 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool p) {
   return r != 0;
 }
 
+// Arrive on `bar` when all of this thread's cp.async copies so far have landed
+// (counted among the barrier's arrivals).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // D: head dim.  RB: blocks of 8 query heads per key/value head (1: G <= 8,
 // 2: G <= 16).  kLists: the pages of a list instead of all.
 template <int D, int RB, bool kLists>
-__global__ void __launch_bounds__(dec_threads(RB), 1)
-    paged_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                           const __grid_constant__ DecArgs a) {
+__global__ void __launch_bounds__(dec_threads(RB), 1) paged_attention_kernel(const __grid_constant__ DecArgs a) {
   using SM = DecSmem<D, RB>;
-  using Rows = DecRows<kLists>;
+  using Rows = DecRows<D, kLists>;
   constexpr int kStages = SM::kStages;
   constexpr int kHalves = D / 64;
   constexpr int kGroups = dec_groups(RB), kCopyWarp = 4 * kGroups, kPlanWarp = kCopyWarp + 3;
@@ -171,13 +182,13 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::kOffMisc);
   DecTile* plan = reinterpret_cast<DecTile*>(smem + SM::kOffPlan);
   // the prefix sums' scratch: stage memory that no copy has been issued into yet
-  int* sums = reinterpret_cast<int*>(smem);
+  int2* sums = reinterpret_cast<int2*>(smem);
   const PagedView& v = a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages; ++k) {
-      mbar_init(full(k), 3);
+      mbar_init(full(k), 96);
       mbar_init(empty(k), 4 * kGroups);
     }
     for (int k = 0; k < 2; ++k) {
@@ -187,18 +198,19 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kCopyWarp && lane == 0) prefetch_tmap(&tmK);
-  if (warp == kCopyWarp + 1 && lane == 0) prefetch_tmap(&tmV);
   pdl_wait();
   pdl_trigger();
   const int n_units = kLists ? v.S * v.Hkv : v.S;
-  const Share sh = share_work([&](int u) { return Rows::unit_tiles(a, u); }, n_units, blockIdx.x, gridDim.x, sums);
-  fence_proxy_async_smem();  // the scratch's generic accesses come before the copies into it
-  __syncthreads();
+  const Share sh =
+      share_work([&](int u) { return Rows::work(a, u); }, kDecRowCost, n_units, blockIdx.x, gridDim.x, sums);
+  __syncthreads();  // the scratch has been read
 
   if (warp == kPlanWarp) {
     // ------------------------------------------------------------ planner
-    const int per_tile = kDecTile >> v.page_shift;  // pages of a tile
+    constexpr int kMaxPages = SM::kTile / 16;
+    const int per_tile = SM::kTile >> v.page_shift;  // pages of a tile
+    DecMeta meta{sh.begin, sh.n, -1, 0, 0, {0, 0, 0}};
+    if (sh.n == 0 && lane == 0) a.meta[blockIdx.x] = meta;
     int unit = sh.unit, pos = sh.off;  // tile `base` of the share is tile `pos` from the start of unit `unit` on
     int rows = 0;  // rows begun
     bool ok = true;
@@ -207,7 +219,8 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
       int x = pos + lane, mine = -1;
       bool open = base + lane < sh.n;
       for (int u0 = unit; __any_sync(0xffffffffu, open) && u0 < n_units; u0 += 32) {
-        const int t = u0 + lane < n_units ? Rows::unit_tiles(a, u0 + lane) : 0;
+        const UnitWork w = u0 + lane < n_units ? Rows::work(a, u0 + lane) : UnitWork{0, 0};
+        const int t = w.rows * w.tiles;
         const int incl = warp_inclusive(t), all = __shfl_sync(0xffffffffu, incl, 31);
         int l = 0;  // first unit of these 32 whose sum passes x
 #pragma unroll
@@ -224,7 +237,9 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
           }
         }
       }
-      DecTile d{{-1, -1, -1, -1}, 0, 0, 0, 0};
+      DecTile d{};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) d.coord[k] = -1;
       if (mine >= 0) {
         int s = mine, hk = 0, off = x;
         if constexpr (kLists) {
@@ -237,31 +252,39 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
           off -= hk * T;
         }
         const int64_t row = int64_t(s) * v.Hkv + hk;
-        const int len = seq_len(v, s), pages = pages_of(v, len);
+        const int len = seq_len(v, s), pages = pages_of(v, len), at = base + lane;
         d.row = int(row);
         d.qrow = query_row(v, s);
-        d.flags = (off == 0 || base + lane == 0 ? kTileFirst : 0) | (off == T - 1 || base + lane == sh.n - 1 ? kTileLast : 0) |
+        d.flags = (off == 0 || at == 0 ? kTileFirst : 0) | (off == T - 1 || at == sh.n - 1 ? kTileLast : 0) |
                   (off == 0 ? kRowStart : 0) | (off == T - 1 ? kRowEnd : 0);
-        int j[4], id[4];
+        if (at == sh.n - 1) {
+          if (off < T - 1 && off <= at) {  // the row begins here and goes on behind the share
+            meta.row = d.row;
+            meta.end = sh.begin + at - off + T;
+            meta.slot = off == at ? 0 : 1;
+          }
+          a.meta[blockIdx.x] = meta;
+        }
+        int j[kMaxPages], id[kMaxPages];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kMaxPages; ++k) {
           const int e = off * per_tile + k;
           j[k] = -1;
           if (k < per_tile && e < entries) j[k] = kLists ? __ldg(a.idx + row * v.max_pages + e) : e;
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kMaxPages; ++k) {
           id[k] = -1;
           if (j[k] >= 0 && j[k] < pages) id[k] = __ldg(v.table + int64_t(s) * v.max_pages + j[k]);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kMaxPages; ++k) {
           if (k < per_tile && off * per_tile + k < entries) {
             if (id[k] < 0 || id[k] >= v.num_pages) {
               raise_error(AB_ERR_CAPACITY);
             } else {
               d.coord[k] = id[k] * v.Hkv + hk;
-              d.valid |= min(v.page, len - (j[k] << v.page_shift)) << (8 * k);
+              d.valid[k >> 2] |= min(v.page, len - (j[k] << v.page_shift)) << (8 * (k & 3));
             }
           }
         }
@@ -280,11 +303,13 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
       if (unit < 0) break;  // the share's last batch
     }
   } else if (warp >= kCopyWarp) {
-    // ------------------------------------------------- copies: K, V, queries
-    const int what = warp - kCopyWarp;
-    const int per_tile = kDecTile >> v.page_shift;
-    const uint32_t page_bytes = uint32_t(SM::kRow) << v.page_shift;
-    const CUtensorMap* tm = what == 0 ? &tmK : &tmV;
+    // -------------------------------------------------------------- copies
+    // The 16-key pieces of a tile's K and V are dealt out to the three warps;
+    // a lane copies 16 bytes at a time into their place in the 128-byte swizzle.
+    constexpr int kCols = D / 8;          // 16-byte columns of a row
+    constexpr int kStep = 32 / kCols;     // rows that a warp copies at once
+    const int mine = warp - kCopyWarp;
+    const int col = lane % kCols, row0 = lane / kCols;
     uint32_t use = 0;  // tiles issued
     bool ok = true;
     for (int base = 0, batch = 0; base < sh.n && ok; base += 32, ++batch) {
@@ -295,72 +320,51 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
         const int st = int(use % kStages);
         ok = lane0_wait(empty(st), ((use / kStages) & 1) ^ 1, abort_flag);
         if (!ok) break;
-        if (lane == 0) {
-          const int flags = d->flags;
-          if (what < 2) {
-            const int4 at = *reinterpret_cast<const int4*>(d->coord);
-            const int coord[4] = {at.x, at.y, at.z, at.w};
-            int n_pages = 0;
+        const int flags = d->flags;
+        const uint64_t valid = uint64_t(uint32_t(d->valid[0])) | uint64_t(uint32_t(d->valid[1])) << 32;
+        constexpr int kPieces = SM::kTile / 16;  // of K, and as many of V
 #pragma unroll
-            for (int e = 0; e < 4; ++e) n_pages += coord[e] >= 0 ? 1 : 0;
-            if (what == 0) *reinterpret_cast<int4*>(smem + SM::kOffMeta + st * 16) = make_int4(d->valid, d->row, flags, 0);
-            mbar_arrive_expect_tx(full(st), page_bytes * uint32_t(n_pages));
-            const uint32_t dst = sbase + uint32_t(st) * 2u * SM::kTileBytes + uint32_t(what) * SM::kTileBytes;
-            for (int e = 0; e < per_tile; ++e)
-              if (coord[e] >= 0) tma_load_5d(dst + uint32_t(e) * page_bytes, tm, full(st), 0, 0, 0, 0, coord[e]);
-          } else if (flags & kTileFirst) {
-            const int hk = d->row % v.Hkv;
-            const __nv_bfloat16* q = a.Q + (int64_t(d->qrow) * v.Hkv + hk) * v.G * D;
-            mbar_arrive_expect_tx(full(st), uint32_t(v.G * SM::kRow));
-            for (int h = 0; h < v.G; ++h)
-              bulk_load(sbase + SM::kOffQ + uint32_t(st * SM::kQBytes + h * SM::kQPitch), q + h * D, SM::kRow, full(st));
-          } else {
-            mbar_arrive(full(st));
+        for (int x = 0; x < (2 * kPieces + 2) / 3; ++x) {
+          const int piece = mine + 3 * x;
+          const bool of_k = piece < kPieces;
+          const int key0 = (piece & (kPieces - 1)) * 16, entry = key0 >> v.page_shift, in_page = key0 & (v.page - 1);
+          const int rows = min(16, int(uint32_t(valid >> (8 * entry)) & 255u) - in_page);
+          if (piece < 2 * kPieces && rows > 0) {
+            const __nv_bfloat16* src =
+                (of_k ? a.K : a.V) + (int64_t(d->coord[entry]) * v.page + in_page + row0) * D + col * 8;
+            const uint32_t dst = sbase + uint32_t(st) * 2u * SM::kTileBytes + (of_k ? 0u : uint32_t(SM::kTileBytes)) +
+                                 uint32_t(key0 >> 3) * (kHalves * 1024u) + uint32_t(col >> 3) * 1024u;
+#pragma unroll
+            for (int r = 0; r < 16; r += kStep) {
+              const int row = r + row0;
+              if (row < rows)
+                cp_async16(dst + uint32_t(row >> 3) * (kHalves * 1024u) + uint32_t(row & 7) * 128u +
+                               (uint32_t((col & 7) ^ (row & 7)) << 4),
+                           src + r * D);
+            }
           }
         }
-        __syncwarp();
+        if (mine == 2 && (flags & kTileFirst)) {
+          const int hk = d->row % v.Hkv;
+          const __nv_bfloat16* q = a.Q + ((int64_t(d->qrow) * v.Hkv + hk) * v.G + row0) * D + col * 8;
+          const uint32_t dst = sbase + SM::kOffQ + uint32_t(st * SM::kQBytes + row0 * SM::kQPitch + col * 16);
+          for (int h = row0; h < v.G; h += kStep, q += kStep * D)
+            cp_async16(dst + uint32_t((h - row0) * SM::kQPitch), q);
+        }
+        if (mine == 0 && lane == 0)
+          *reinterpret_cast<int4*>(smem + SM::kOffMeta + st * 16) = make_int4(d->valid[0], d->valid[1], d->row, flags);
+        cp_async_arrive(full(st));  // arrives when this lane's copies have landed
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(plan_empty(batch & 1));
     }
-    if (lane == 0) {
-      // copies in flight land before shared memory is released, also if the
-      // consumers gave up: the last use of each stage
-      for (uint32_t k = 0; k < uint32_t(kStages) && k < use; ++k) {
-        const uint32_t last = use - 1 - ((use - 1 - k) % kStages);
-        mbar_wait_drain(full(int(k)), (last / kStages) & 1);
-      }
-    }
+    cp_async_wait<0>();
   } else {
     // ----------------------------------------------------------- consumers
-    if (threadIdx.x == 0) {
-      // for the joining kernel
-      DecMeta mt{-1, 0, 0, 0};
-      if (sh.begin < sh.total && blockIdx.x > 0) {
-        int off = sh.off, s = sh.unit, hk = 0;
-        if constexpr (kLists) {
-          s = sh.unit / v.Hkv;
-          hk = sh.unit % v.Hkv;
-        }
-        const int T = Rows::tiles_of(a, Rows::row_entries(a, s, hk));
-        if constexpr (!kLists) {
-          hk = off / T;
-          off -= hk * T;
-        }
-        const int C = min(sh.total, int(gridDim.x));
-        const int start = sh.begin - off, prev = share_begin(sh.total, C, blockIdx.x - 1);
-        if (off > 0 && prev <= start) {
-          mt.row = s * v.Hkv + hk;
-          mt.last = share_of(sh.total, C, start + T - 1);
-          mt.slot = prev == start ? 0 : 1;
-        }
-      }
-      a.meta[blockIdx.x] = mt;
-    }
     // units without keys: O = 0 (a lane looks at one, the warp writes)
     for (int64_t k0 = int64_t(warp) * 32; blockIdx.x + k0 * gridDim.x < n_units; k0 += 128 * kGroups) {
       const int64_t u = blockIdx.x + (k0 + lane) * gridDim.x;
-      const bool none = u < n_units && Rows::unit_tiles(a, int(u)) == 0 && query_row(v, kLists ? int(u) / v.Hkv : int(u)) >= 0;
+      const bool none = u < n_units && Rows::work(a, int(u)).tiles == 0 && query_row(v, kLists ? int(u) / v.Hkv : int(u)) >= 0;
       for (uint32_t some = __ballot_sync(0xffffffffu, none); some; some &= some - 1) {
         const int n = v.G * D * (kLists ? 1 : v.Hkv);
         uint32_t* z = reinterpret_cast<uint32_t*>(a.O + (blockIdx.x + (k0 + __ffs(some) - 1) * gridDim.x) * n);
@@ -369,16 +373,17 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
     }
     const int g = lane >> 2, t = lane & 3;
     const int group = warp >> 2, gwarp = warp & 3, gthread = threadIdx.x & 127;
-    const int key0 = gwarp * 16;  // this warp's keys of a tile
-    // row addresses of the operand loads within a tile (128-byte swizzle, 8-row
-    // groups of kHalves KB): K as stored, V transposed
-    const int krow = key0 + ((lane >> 4) << 3) + (lane & 7), kch = (lane >> 3) & 1;
-    const int vrow = key0 + (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;
+    // this warp's keys of a tile: 16 of every 64.  Row addresses of the operand
+    // loads (128-byte swizzle, 8-row groups of kHalves KB): K as stored, V
+    // transposed
+    constexpr int NB = SM::kTile / 64;
+    constexpr uint32_t kBlock = 8 * kHalves * 1024;  // 64 keys
+    const int krow = gwarp * 16 + ((lane >> 4) << 3) + (lane & 7), kch = (lane >> 3) & 1;
+    const int vrow = gwarp * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;
     const uint32_t kbase = uint32_t(krow >> 3) * (kHalves * 1024u) + uint32_t(krow & 7) * 128u;
     const uint32_t vbase = uint32_t(vrow >> 3) * (kHalves * 1024u) + uint32_t(vrow & 7) * 128u;
     float* mrg = reinterpret_cast<float*>(smem + SM::kOffMerge + group * SM::kMergeBytes);
     float2* ml = reinterpret_cast<float2*>(smem + SM::kOffMl + group * SM::kMlBytes);
-    const int vshift = 8 * (key0 >> v.page_shift), vsub = key0 & (v.page - 1);
     bool started = false;  // the current row's first tile is this CTA's
     uint32_t q0[D / 16][2], q1[D / 16][2];  // queries: rows g and g + 8 of the 16 x d operand
     float o[RB][D / 8][4], m[RB], l[RB];
@@ -390,7 +395,7 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
         break;
       }
       const int4 mt = *reinterpret_cast<const int4*>(smem + SM::kOffMeta + st * 16);
-      const int flags = mt.z;
+      const int flags = mt.w;
       if (kGroups > 1 && ((flags >> kTileRow) & (kGroups - 1)) != group) {  // another group's row
         __syncwarp();
         if (lane == 0) mbar_arrive(empty(st));
@@ -419,30 +424,46 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
         }
         started = flags & kRowStart;
       }
-      const int valid = min(16, int((uint32_t(mt.x) >> vshift) & 255u) - vsub);
+      const uint64_t valid8 = uint64_t(uint32_t(mt.x)) | uint64_t(uint32_t(mt.y)) << 32;
+      int valid[NB];  // keys of each 16
+      bool some = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int key = nb * 64 + gwarp * 16;
+        valid[nb] = int(uint32_t(valid8 >> (8 * (key >> v.page_shift))) & 255u) - (key & (v.page - 1));
+        some = some || valid[nb] > 0;
+      }
       const uint32_t kt = sbase + uint32_t(st) * 2u * SM::kTileBytes, vt = kt + SM::kTileBytes;
-      if (valid > 0) {
-        // S = Q K^T for 16 keys: two n-tiles, each in two accumulators
-        float c[2][2][4] = {};
+      if (some) {
+        // S = Q K^T, 8 keys by 8 keys, each in two accumulators
+        float c[2 * NB][2][4] = {};
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t b[4];
-          const int ch = 2 * kk + kch;
-          ldmatrix_x4(kt + kbase + uint32_t(ch >> 3) * 1024u + uint32_t(((ch & 7) ^ (krow & 7)) << 4), b);
-          mma_16816(c[0][kk & 1], q0[kk][0], q1[kk][0], q0[kk][1], q1[kk][1], b[0], b[1]);
-          mma_16816(c[1][kk & 1], q0[kk][0], q1[kk][0], q0[kk][1], q1[kk][1], b[2], b[3]);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            uint32_t b[4];
+            const int ch = 2 * kk + kch;
+            ldmatrix_x4(kt + nb * kBlock + kbase + uint32_t(ch >> 3) * 1024u + uint32_t(((ch & 7) ^ (krow & 7)) << 4), b);
+            mma_16816(c[2 * nb][kk & 1], q0[kk][0], q1[kk][0], q0[kk][1], q1[kk][1], b[0], b[1]);
+            mma_16816(c[2 * nb + 1][kk & 1], q0[kk][0], q1[kk][0], q0[kk][1], q1[kk][1], b[2], b[3]);
+          }
         }
-        uint32_t hi[RB][2], lo[RB][2];  // P of keys (0-7: 2t, 2t+1), (8-15: 2t, 2t+1) as A operands
+        uint32_t hi[RB][NB][2], lo[RB][NB][2];  // P of keys (0-7: 2t, 2t+1), (8-15: 2t, 2t+1) as A operands
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
-          float x[4];
+          float x[NB][4];
+          float mx = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = (e >> 1) * 8 + 2 * t + (e & 1);
-            x[e] = c[e >> 1][0][2 * r + (e & 1)] + c[e >> 1][1][2 * r + (e & 1)];
-            if (key >= valid) x[e] = -INFINITY;
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = (e >> 1) * 8 + 2 * t + (e & 1), n8 = 2 * nb + (e >> 1);
+              x[nb][e] = c[n8][0][2 * r + (e & 1)] + c[n8][1][2 * r + (e & 1)];
+              if (key >= valid[nb]) x[nb][e] = -INFINITY;
+            }
+            mx = fmaxf(fmaxf(mx, fmaxf(x[nb][0], x[nb][1])), fmaxf(x[nb][2], x[nb][3]));
           }
-          float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.scale_log2;
+          mx *= a.scale_log2;
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           if (__any_sync(0xffffffffu, mx > m[r] + kDecLazy)) {
@@ -456,40 +477,47 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
               for (int e = 0; e < 4; ++e) o[r][k8][e] *= al;
           }
           const float ref = m[r] == -INFINITY ? 0.f : m[r];
-          float p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = ex2_approx(fmaf(x[e], a.scale_log2, -ref));
-            l[r] += p[e];
-          }
+          for (int nb = 0; nb < NB; ++nb) {
+            float p[4];
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            hi[r][z] = pack_bf16x2(p[2 * z], p[2 * z + 1]);
-            lo[r][z] = pack_bf16x2(p[2 * z] - __uint_as_float(hi[r][z] << 16),
-                                   p[2 * z + 1] - __uint_as_float(hi[r][z] & 0xFFFF0000u));
+            for (int e = 0; e < 4; ++e) {
+              p[e] = ex2_approx(fmaf(x[nb][e], a.scale_log2, -ref));
+              l[r] += p[e];
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              hi[r][nb][z] = pack_bf16x2(p[2 * z], p[2 * z + 1]);
+              lo[r][nb][z] = pack_bf16x2(p[2 * z] - __uint_as_float(hi[r][nb][z] << 16),
+                                         p[2 * z + 1] - __uint_as_float(hi[r][nb][z] & 0xFFFF0000u));
+            }
           }
         }
         // O += P V: rows 0-7 the upper part of P, rows 8-15 the lower; V rows
         // behind the end count as zero
-        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (valid < 16) {
 #pragma unroll
-          for (int z = 0; z < 2; ++z)
-            keep[z] = (z * 8 + 2 * t < valid ? 0xFFFFu : 0u) | (z * 8 + 2 * t + 1 < valid ? 0xFFFF0000u : 0u);
-        }
+        for (int nb = 0; nb < NB; ++nb) {
+          uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+          if (valid[nb] < 16) {
 #pragma unroll
-        for (int np = 0; np < D / 16; ++np) {
-          uint32_t b[4];
-          const int ch = 2 * np + vch;
-          ldmatrix_x4_trans(vt + vbase + uint32_t(ch >> 3) * 1024u + uint32_t(((ch & 7) ^ (vrow & 7)) << 4), b);
-          b[0] &= keep[0];
-          b[1] &= keep[1];
-          b[2] &= keep[0];
-          b[3] &= keep[1];
+            for (int z = 0; z < 2; ++z)
+              keep[z] = (z * 8 + 2 * t < valid[nb] ? 0xFFFFu : 0u) | (z * 8 + 2 * t + 1 < valid[nb] ? 0xFFFF0000u : 0u);
+          }
 #pragma unroll
-          for (int r = 0; r < RB; ++r) {
-            mma_16816(o[r][2 * np], hi[r][0], lo[r][0], hi[r][1], lo[r][1], b[0], b[1]);
-            mma_16816(o[r][2 * np + 1], hi[r][0], lo[r][0], hi[r][1], lo[r][1], b[2], b[3]);
+          for (int np = 0; np < D / 16; ++np) {
+            uint32_t b[4];
+            const int ch = 2 * np + vch;
+            ldmatrix_x4_trans(vt + nb * kBlock + vbase + uint32_t(ch >> 3) * 1024u + uint32_t(((ch & 7) ^ (vrow & 7)) << 4),
+                              b);
+            b[0] &= keep[0];
+            b[1] &= keep[1];
+            b[2] &= keep[0];
+            b[3] &= keep[1];
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+              mma_16816(o[r][2 * np], hi[r][nb][0], lo[r][nb][0], hi[r][nb][1], lo[r][nb][1], b[0], b[1]);
+              mma_16816(o[r][2 * np + 1], hi[r][nb][0], lo[r][nb][0], hi[r][nb][1], lo[r][nb][1], b[2], b[3]);
+            }
           }
         }
       }
@@ -512,7 +540,7 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
       }
       if (bar_any(1 + group, 128, false)) break;
       const bool whole = started && (flags & kRowEnd);
-      const int64_t row = mt.y;
+      const int64_t row = mt.z;
       const int slot = flags >> kTileRow == 0 ? 0 : 1;  // a partial row is this CTA's first or its last
       for (int e = gthread * 4; e < v.G * D; e += 512) {
         const int head = e / D, i = e % D;
@@ -550,25 +578,27 @@ __global__ void __launch_bounds__(dec_threads(RB), 1)
   }
 }
 
-// Joins the partial results of the rows that several CTAs share.  Block
-// (c - 1, h) takes head h of the row that CTA c's share begins inside of, if c
-// is the first such share; eight warps take every eighth part, four values a
-// lane.
+// Joins the partial results of the rows that several CTAs share.  Block (c, h)
+// takes head h of the row that begins in CTA c's share and ends behind it; eight
+// warps take every eighth part, four values a lane.
 constexpr int kJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ DecArgs a, int heads_pad) {
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ DecArgs a, int C, int heads_pad) {
   constexpr int kVec = D / 32;
   __shared__ float so[kJoinWarps][D];
   __shared__ float2 sml[kJoinWarps];
   pdl_wait();
-  const int c = blockIdx.x + 1, h = blockIdx.y;
+  const int c = blockIdx.x, h = blockIdx.y;
   const DecMeta mt = a.meta[c];
   if (mt.row < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float m = -INFINITY, l = 0.f, o[kVec] = {};
-  for (int k = c - 1 + warp; k <= mt.last; k += kJoinWarps) {
-    const int64_t at = (int64_t(k) * 2 + (k == c - 1 ? mt.slot : 0)) * heads_pad + h;
+  for (int k = c + warp; k < C; k += kJoinWarps) {
+    const int2 share = *reinterpret_cast<const int2*>(a.meta + k);
+    if (share.x >= mt.end) break;
+    if (share.y == 0) continue;
+    const int64_t at = (int64_t(k) * 2 + (k == c ? mt.slot : 0)) * heads_pad + h;
     const float2 z = a.part_ml[at];
     float x[kVec];
 #pragma unroll

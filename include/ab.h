@@ -404,7 +404,7 @@ typedef struct {
   int32_t Hq, Hkv, d; /* query heads, key/value heads (Hq = G Hkv, G <= 16), head dim 64 or 128 */
   int32_t page;       /* tokens per page: 16, 32 or 64 */
   int32_t num_pages;  /* num_pages * page and num_pages * Hkv < 2^31 */
-  int32_t max_pages;  /* pages a sequence can have; max_pages * page <= 2^24, S * Hkv * max_pages * page < 2^37 */
+  int32_t max_pages;  /* pages a sequence can have; max_pages * page <= 2^24, S * Hkv * max_pages * page < 2^35 */
   int32_t recent;     /* newest pages that ab_paged_topk always keeps, >= 0 */
   float keep_ratio;   /* fraction of a sequence's pages that it keeps, in (0, 1] */
 } ab_paged_params;

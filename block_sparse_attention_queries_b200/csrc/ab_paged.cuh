@@ -364,60 +364,81 @@ template <typename F>
 __device__ __forceinline__ Share share_work(F work, int row_cost, int n_units, int c, int C, int2* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int chunks = (n_units + 31) / 32;
+  auto unit_work = [&](int u) { return u < n_units ? work(u) : UnitWork{0, 0}; };
   auto cost_of = [&](const UnitWork& w) { return w.tiles > 0 ? w.rows * (2 * w.tiles + row_cost) : 0; };
-  for (int k = warp; k < chunks; k += warps) {
-    const int u = k * 32 + lane;
-    const UnitWork w = u < n_units ? work(u) : UnitWork{0, 0};
-    const int cost = __reduce_add_sync(0xffffffffu, cost_of(w));
-    const int tiles = __reduce_add_sync(0xffffffffu, w.rows * w.tiles);
-    if (lane == 0) sums[k] = make_int2(cost, tiles);
-  }
-  __syncthreads();
-  // every warp works its CTA's share out by itself
-  int total = 0, total_tiles = 0;
-  for (int k = lane; k < chunks; k += 32) {
-    total += sums[k].x;
-    total_tiles += sums[k].y;
-  }
-  total = __reduce_add_sync(0xffffffffu, total);
-  total_tiles = __reduce_add_sync(0xffffffffu, total_tiles);
-  // the first tile at or behind cost p: its unit, place in the unit, place in the list
-  auto locate = [&](int p, int& unit, int& off) -> int {
-    unit = n_units;
-    off = 0;
-    if (p >= total) return total_tiles;
-    int base = 0, before = 0, chunk = 0;
-    for (int k0 = 0; k0 < chunks; k0 += 32) {
-      const int2 w = k0 + lane < chunks ? sums[k0 + lane] : make_int2(0, 0);
-      const int incl = warp_inclusive(w.x), tiles = warp_inclusive(w.y);
-      const uint32_t past = __ballot_sync(0xffffffffu, base + incl > p);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        chunk = k0 + l;
-        base += __shfl_sync(0xffffffffu, incl - w.x, l);
-        before += __shfl_sync(0xffffffffu, tiles - w.y, l);
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, incl, 31);
-      before += __shfl_sync(0xffffffffu, tiles, 31);
-    }
-    const int u = chunk * 32 + lane;
-    const UnitWork w = u < n_units ? work(u) : UnitWork{0, 0};
-    const int cost = cost_of(w), incl = warp_inclusive(cost), tiles = warp_inclusive(w.rows * w.tiles);
-    const int l = __ffs(__ballot_sync(0xffffffffu, base + incl > p) | 0x80000000u) - 1;
-    const int rest = p - base - __shfl_sync(0xffffffffu, incl - cost, l);
-    const int T = __shfl_sync(0xffffffffu, w.tiles, l);
-    const int row = rest / (2 * T + row_cost), x = rest - row * (2 * T + row_cost);
-    unit = chunk * 32 + l;
-    off = row * T + min((x + 1) / 2, T);
-    return before + __shfl_sync(0xffffffffu, tiles - w.rows * w.tiles, l) + off;
+  // the two ends of the share: cost p, and its chunk of 32 units with the sums before it
+  int p[2], chunk[2] = {0, 0}, base[2] = {0, 0}, before[2] = {0, 0}, total_tiles;
+  UnitWork w[2];
+  auto ends = [&](int total) {
+    const int q = total / C, r = total - q * C;
+    p[0] = c * q + min(c, r);
+    p[1] = p[0] + q + (c < r ? 1 : 0);
   };
-  const int q = total / C, r = total - q * C;
-  Share s;
-  int unit, off;
-  s.begin = locate(c * q + min(c, r), s.unit, s.off);
-  s.n = locate((c + 1) * q + min(c + 1, r), unit, off) - s.begin;
-  return s;
+  int total;
+  if (chunks == 1) {
+    w[0] = w[1] = unit_work(lane);
+    total = __reduce_add_sync(0xffffffffu, cost_of(w[0]));
+    total_tiles = __reduce_add_sync(0xffffffffu, w[0].rows * w[0].tiles);
+    ends(total);
+  } else {
+    for (int k = warp; k < chunks; k += warps) {
+      const UnitWork x = unit_work(k * 32 + lane);
+      const int cost = __reduce_add_sync(0xffffffffu, cost_of(x));
+      const int tiles = __reduce_add_sync(0xffffffffu, x.rows * x.tiles);
+      if (lane == 0) sums[k] = make_int2(cost, tiles);
+    }
+    __syncthreads();
+    // every warp works its CTA's share out by itself
+    total = total_tiles = 0;
+    for (int k = lane; k < chunks; k += 32) {
+      total += sums[k].x;
+      total_tiles += sums[k].y;
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    total_tiles = __reduce_add_sync(0xffffffffu, total_tiles);
+    ends(total);
+    int cost = 0, tiles = 0;  // of the chunks before
+    bool open[2] = {true, true};
+    for (int k0 = 0; k0 < chunks && (open[0] || open[1]); k0 += 32) {
+      const int2 x = k0 + lane < chunks ? sums[k0 + lane] : make_int2(0, 0);
+      const int incl = warp_inclusive(x.x), incl_tiles = warp_inclusive(x.y);
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const uint32_t past = __ballot_sync(0xffffffffu, cost + incl > p[z]);
+        if (open[z] && past) {
+          const int l = __ffs(past) - 1;
+          chunk[z] = k0 + l;
+          base[z] = cost + __shfl_sync(0xffffffffu, incl - x.x, l);
+          before[z] = tiles + __shfl_sync(0xffffffffu, incl_tiles - x.y, l);
+          open[z] = false;
+        }
+      }
+      cost += __shfl_sync(0xffffffffu, incl, 31);
+      tiles += __shfl_sync(0xffffffffu, incl_tiles, 31);
+    }
+    w[0] = unit_work(chunk[0] * 32 + lane);
+    w[1] = unit_work(chunk[1] * 32 + lane);
+  }
+  // the first tile at or behind cost p: its unit, place in the unit, place in the list
+  int unit[2], off[2], at[2];
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    const int cost = cost_of(w[z]), incl = warp_inclusive(cost), tiles = w[z].rows * w[z].tiles;
+    const int incl_tiles = warp_inclusive(tiles);
+    const int l = __ffs(__ballot_sync(0xffffffffu, base[z] + incl > p[z]) | 0x80000000u) - 1;
+    const int rest = p[z] - base[z] - __shfl_sync(0xffffffffu, incl - cost, l);
+    const int T = __shfl_sync(0xffffffffu, w[z].tiles, l), row_total = 2 * T + row_cost;
+    const int row = row_total > 0 ? rest / row_total : 0, x = rest - row * row_total;
+    unit[z] = chunk[z] * 32 + l;
+    off[z] = row * T + min((x + 1) / 2, T);
+    at[z] = before[z] + __shfl_sync(0xffffffffu, incl_tiles - tiles, l) + off[z];
+    if (p[z] >= total) {
+      unit[z] = n_units;
+      off[z] = 0;
+      at[z] = total_tiles;
+    }
+  }
+  return Share{unit[0], off[0], at[1] - at[0], at[0]};
 }
 
 // First unit from u on with tiles, n_units if there is none; whole warps, 32

@@ -333,16 +333,16 @@ ab_status run_paged_topk(const ab_paged_params* p, const float* P, const int32_t
   return launch_status();
 }
 
-template <int D, int RB, bool kLists>
+template <int D, bool kLists>
 ab_status launch_paged_attention(const DecArgs& a, int grid, cudaStream_t st) {
-  auto kern = paged_attention_kernel<D, RB, kLists>;
-  constexpr int smem = DecSmem<D, RB>::kAlloc;
+  auto kern = paged_attention_kernel<D, kLists>;
+  constexpr int smem = DecSmem<D>::kAlloc;
   if (set_smem(kern, smem) != cudaSuccess) return AB_ERR_CUDA;
-  kern<<<unsigned(grid), dec_threads(RB), smem, st>>>(a);
+  kern<<<unsigned(grid), kDecThreads, smem, st>>>(a);
   if (launch_status() != AB_OK) return AB_ERR_CUDA;
   if (grid == 1) return AB_OK;
   return launch_after(paged_join_kernel<D>, dim3(unsigned(grid - 1), unsigned(a.v.G)), 32 * kJoinWarps, 0, st, a, grid,
-                      RB * 8);
+                      a.v.G > 8 ? 16 : 8);
 }
 
 ab_status run_paged_attention(const ab_paged_params* p, const PagedView& v, const void* Q, const void* Kc,
@@ -364,17 +364,9 @@ ab_status run_paged_attention(const ab_paged_params* p, const PagedView& v, cons
   a.part_o = reinterpret_cast<float*>(ws + w.off_part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + w.off_ml);
   const int grid = sms < kDecMaxParts ? sms : kDecMaxParts;
-  auto by_lists = [&](auto dd, auto rb) -> ab_status {
-    constexpr int D = decltype(dd)::value, RB = decltype(rb)::value;
-    return idx ? launch_paged_attention<D, RB, true>(a, grid, st)
-               : launch_paged_attention<D, RB, false>(a, grid, st);
-  };
-  using T128 = std::integral_constant<int, 128>;
-  using T64 = std::integral_constant<int, 64>;
-  using R1 = std::integral_constant<int, 1>;
-  using R2 = std::integral_constant<int, 2>;
-  if (p->d == 128) return v.G <= 8 ? by_lists(T128{}, R1{}) : by_lists(T128{}, R2{});
-  return v.G <= 8 ? by_lists(T64{}, R1{}) : by_lists(T64{}, R2{});
+  if (p->d == 128)
+    return idx ? launch_paged_attention<128, true>(a, grid, st) : launch_paged_attention<128, false>(a, grid, st);
+  return idx ? launch_paged_attention<64, true>(a, grid, st) : launch_paged_attention<64, false>(a, grid, st);
 }
 
 }  // namespace

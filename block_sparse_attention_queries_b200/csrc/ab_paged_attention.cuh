@@ -22,28 +22,28 @@
 //    where a row begins.  (By TMA a tile of four 4 KB boxes each of K and V took
 //    1000 cycles, one of 2 KB boxes about as long: at most 32 bytes a cycle and
 //    about 100 cycles a box, where HBM needs 23 bytes a cycle.);
-//  - groups of four warps take the rows in turn (two groups for G <= 8, so that
-//    one row's start and end, about 2500 cycles, overlap the next one's tiles);
-//    a group's warps take 16 (32) keys of each tile each, with a softmax state
+//  - two groups of four warps take the rows in turn, so that one row's start and
+//    end, about 2000 cycles, overlap the next one's tiles (for G > 8 each group
+//    takes its half of the heads of every row); a group's warps take 16 (32) keys of each tile each, with a softmax state
 //    of their own, joined once per row.
 //
 // The G heads are the rows of an m16n8k16 product.  P is used as the sum of two
 // bfloat16 numbers, so that its rounding (2^-17) does not show next to the
-// output's own: for G <= 8 the upper part fills rows 0-7 of the P V product
-// and the lower part rows 8-15, at no cost; for G up to 16 two products run
-// per half.  V rows that lie behind the sequence's end are set to zero in the
+// output's own: a group has at most 8 heads, so the upper part fills rows 0-7
+// of the P V product and the lower part rows 8-15, at no cost.  V rows that lie behind the sequence's end are set to zero in the
 // operand, since 0 times what an unwritten page holds may be NaN.
 #pragma once
+
+#include <type_traits>
 
 #include "ab_norm_rope.cuh"
 #include "ab_paged.cuh"
 
 namespace ab {
 
-// groups of four consumer warps; warps that copy keys, values and queries; the
-// planning warp
-__host__ __device__ constexpr int dec_groups(int RB) { return RB == 1 ? 2 : 1; }
-__host__ __device__ constexpr int dec_threads(int RB) { return dec_groups(RB) * 128 + 128; }
+// two groups of four consumer warps, three warps that copy, the planning warp
+constexpr int kDecGroups = 2;
+constexpr int kDecThreads = kDecGroups * 128 + 128;
 // keys per tile: 32 KB of keys and values
 __host__ __device__ constexpr int dec_tile(int D) { return D == 128 ? 64 : 128; }
 constexpr int kDecRowCost = 1;     // a row's start and end, in halves of a tile
@@ -76,26 +76,25 @@ struct DecArgs {
   __nv_bfloat16* O;          // [S, Hq, d]
   float scale_log2;
   DecMeta* meta;             // workspace: [grid]
-  float* part_o;             // [grid, 2, 8 RB, d] unnormalised
-  float2* part_ml;           // [grid, 2, 8 RB]
+  float* part_o;             // [grid, 2, 8 or 16 heads, d] unnormalised
+  float2* part_ml;           // [grid, 2, 8 or 16 heads]
 };
 
-template <int D, int RB>
+template <int D>
 struct DecSmem {
   static constexpr int kRow = D * 2;
   static constexpr int kTile = dec_tile(D);
   static constexpr int kTileBytes = kTile * kRow;     // one of K, V
-  static constexpr int kGroups = dec_groups(RB);
   static constexpr int kStages = 5;
   static constexpr int kPitch = D + 8;                // floats; rows of a quad's lanes in different banks
   static constexpr int kQPitch = kRow + 16;           // bytes, for the same reason
-  static constexpr int kQBytes = RB * 8 * kQPitch;
+  static constexpr int kQBytes = kMaxGroup * kQPitch;
   static constexpr int kOffQ = kStages * 2 * kTileBytes;
   static constexpr int kOffMerge = kOffQ + kStages * kQBytes;
-  static constexpr int kMergeBytes = 4 * RB * 8 * kPitch * 4;
-  static constexpr int kOffMl = kOffMerge + kGroups * kMergeBytes;  // per group: 4 warps x 8 RB float2
-  static constexpr int kMlBytes = 4 * RB * 8 * 8;
-  static constexpr int kOffPlan = kOffMl + kGroups * kMlBytes;      // 2 x 32 planned tiles
+  static constexpr int kMergeBytes = 4 * 8 * kPitch * 4;
+  static constexpr int kOffMl = kOffMerge + kDecGroups * kMergeBytes;  // per group: 4 warps x 8 float2
+  static constexpr int kMlBytes = 4 * 8 * 8;
+  static constexpr int kOffPlan = kOffMl + kDecGroups * kMlBytes;      // 2 x 32 planned tiles
   static constexpr int kOffMeta = kOffPlan + 2 * 32 * int(sizeof(DecTile));  // per stage: valid, row, flags
   static constexpr int kOffBar = kOffMeta + kStages * 16;
   static constexpr int kNumBars = 2 * kStages + 4;
@@ -163,15 +162,14 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// D: head dim.  RB: blocks of 8 query heads per key/value head (1: G <= 8,
-// 2: G <= 16).  kLists: the pages of a list instead of all.
-template <int D, int RB, bool kLists>
-__global__ void __launch_bounds__(dec_threads(RB), 1) paged_attention_kernel(const __grid_constant__ DecArgs a) {
-  using SM = DecSmem<D, RB>;
+// D: head dim.  kLists: the pages of a list instead of all.
+template <int D, bool kLists>
+__global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const __grid_constant__ DecArgs a) {
+  using SM = DecSmem<D>;
   using Rows = DecRows<D, kLists>;
   constexpr int kStages = SM::kStages;
   constexpr int kHalves = D / 64;
-  constexpr int kGroups = dec_groups(RB), kCopyWarp = 4 * kGroups, kPlanWarp = kCopyWarp + 3;
+  constexpr int kCopyWarp = 4 * kDecGroups, kPlanWarp = kCopyWarp + 3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -189,7 +187,7 @@ __global__ void __launch_bounds__(dec_threads(RB), 1) paged_attention_kernel(con
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages; ++k) {
       mbar_init(full(k), 96);
-      mbar_init(empty(k), 4 * kGroups);
+      mbar_init(empty(k), 4 * kDecGroups);
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(plan_full(k), 1);
@@ -362,7 +360,7 @@ __global__ void __launch_bounds__(dec_threads(RB), 1) paged_attention_kernel(con
   } else {
     // ----------------------------------------------------------- consumers
     // units without keys: O = 0 (a lane looks at one, the warp writes)
-    for (int64_t k0 = int64_t(warp) * 32; blockIdx.x + k0 * gridDim.x < n_units; k0 += 128 * kGroups) {
+    for (int64_t k0 = int64_t(warp) * 32; blockIdx.x + k0 * gridDim.x < n_units; k0 += 128 * kDecGroups) {
       const int64_t u = blockIdx.x + (k0 + lane) * gridDim.x;
       const bool none = u < n_units && Rows::work(a, int(u)).tiles == 0 && query_row(v, kLists ? int(u) / v.Hkv : int(u)) >= 0;
       for (uint32_t some = __ballot_sync(0xffffffffu, none); some; some &= some - 1) {
@@ -380,13 +378,16 @@ __global__ void __launch_bounds__(dec_threads(RB), 1) paged_attention_kernel(con
     constexpr uint32_t kBlock = 8 * kHalves * 1024;  // 64 keys
     const int krow = gwarp * 16 + ((lane >> 4) << 3) + (lane & 7), kch = (lane >> 3) & 1;
     const int vrow = gwarp * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;
-    const uint32_t kbase = uint32_t(krow >> 3) * (kHalves * 1024u) + uint32_t(krow & 7) * 128u;
-    const uint32_t vbase = uint32_t(vrow >> 3) * (kHalves * 1024u) + uint32_t(vrow & 7) * 128u;
+    // column 2 k + ch of a row is at (row's base + ((ch ^ row & 7) << 4)) ^ (k << 5)
+    const uint32_t kbase = uint32_t(krow >> 3) * (kHalves * 1024u) + uint32_t(krow & 7) * 128u + uint32_t((kch ^ (krow & 7)) << 4);
+    const uint32_t vbase = uint32_t(vrow >> 3) * (kHalves * 1024u) + uint32_t(vrow & 7) * 128u + uint32_t((vch ^ (vrow & 7)) << 4);
     float* mrg = reinterpret_cast<float*>(smem + SM::kOffMerge + group * SM::kMergeBytes);
     float2* ml = reinterpret_cast<float2*>(smem + SM::kOffMl + group * SM::kMlBytes);
     bool started = false;  // the current row's first tile is this CTA's
-    uint32_t q0[D / 16][2], q1[D / 16][2];  // queries: rows g and g + 8 of the 16 x d operand
-    float o[RB][D / 8][4], m[RB], l[RB];
+    const bool split = v.G > 8;
+    const int head0 = split ? group * 8 : 0, heads = min(8, v.G - head0);  // this group's
+    uint32_t q[D / 16][2];  // queries: rows 0-7 of the 16 x d operand (8-15 are zero)
+    float o[D / 8][4], m = -INFINITY, l = 0.f;
     for (uint32_t use = 0; use < uint32_t(sh.n); ++use) {
       const int st = int(use % kStages);
       const bool got = mbar_wait(full(st), (use / kStages) & 1, abort_flag);
@@ -396,42 +397,35 @@ __global__ void __launch_bounds__(dec_threads(RB), 1) paged_attention_kernel(con
       }
       const int4 mt = *reinterpret_cast<const int4*>(smem + SM::kOffMeta + st * 16);
       const int flags = mt.w;
-      if (kGroups > 1 && ((flags >> kTileRow) & (kGroups - 1)) != group) {  // another group's row
+      if (!split && ((flags >> kTileRow) & 1) != group) {  // another group's row
         __syncwarp();
         if (lane == 0) mbar_arrive(empty(st));
         continue;
       }
       if (flags & kTileFirst) {
-        const uint8_t* q = smem + SM::kOffQ + st * SM::kQBytes + g * SM::kQPitch + 4 * t;
+        const uint8_t* from = smem + SM::kOffQ + st * SM::kQBytes + (head0 + g) * SM::kQPitch + 4 * t;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            q0[k][z] = g < v.G ? *reinterpret_cast<const uint32_t*>(q + 32 * k + 16 * z) : 0u;
-            q1[k][z] = RB == 2 && g + 8 < v.G
-                           ? *reinterpret_cast<const uint32_t*>(q + 8 * SM::kQPitch + 32 * k + 16 * z)
-                           : 0u;
-          }
+          for (int z = 0; z < 2; ++z) q[k][z] = g < heads ? *reinterpret_cast<const uint32_t*>(from + 32 * k + 16 * z) : 0u;
         }
+        m = -INFINITY;
+        l = 0.f;
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          m[r] = -INFINITY;
-          l[r] = 0.f;
+        for (int k = 0; k < D / 8; ++k)
 #pragma unroll
-          for (int k = 0; k < D / 8; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[r][k][e] = 0.f;
-        }
+          for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
         started = flags & kRowStart;
       }
       const uint64_t valid8 = uint64_t(uint32_t(mt.x)) | uint64_t(uint32_t(mt.y)) << 32;
       int valid[NB];  // keys of each 16
-      bool some = false;
+      bool some = false, all = true;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const int key = nb * 64 + gwarp * 16;
         valid[nb] = int(uint32_t(valid8 >> (8 * (key >> v.page_shift))) & 255u) - (key & (v.page - 1));
         some = some || valid[nb] > 0;
+        all = all && valid[nb] >= 16;
       }
       const uint32_t kt = sbase + uint32_t(st) * 2u * SM::kTileBytes, vt = kt + SM::kTileBytes;
       if (some) {
@@ -442,84 +436,79 @@ __global__ void __launch_bounds__(dec_threads(RB), 1) paged_attention_kernel(con
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             uint32_t b[4];
-            const int ch = 2 * kk + kch;
-            ldmatrix_x4(kt + nb * kBlock + kbase + uint32_t(ch >> 3) * 1024u + uint32_t(((ch & 7) ^ (krow & 7)) << 4), b);
-            mma_16816(c[2 * nb][kk & 1], q0[kk][0], q1[kk][0], q0[kk][1], q1[kk][1], b[0], b[1]);
-            mma_16816(c[2 * nb + 1][kk & 1], q0[kk][0], q1[kk][0], q0[kk][1], q1[kk][1], b[2], b[3]);
+            ldmatrix_x4(((kt + kbase) ^ uint32_t((kk & 3) << 5)) + nb * kBlock + uint32_t(kk >> 2) * 1024u, b);
+            mma_16816(c[2 * nb][kk & 1], q[kk][0], 0u, q[kk][1], 0u, b[0], b[1]);
+            mma_16816(c[2 * nb + 1][kk & 1], q[kk][0], 0u, q[kk][1], 0u, b[2], b[3]);
           }
         }
-        uint32_t hi[RB][NB][2], lo[RB][NB][2];  // P of keys (0-7: 2t, 2t+1), (8-15: 2t, 2t+1) as A operands
+        uint32_t hi[NB][2], lo[NB][2];  // P of keys (0-7: 2t, 2t+1), (8-15: 2t, 2t+1) as A operands
+        float x[NB][4];
+        float mx = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          float x[NB][4];
-          float mx = -INFINITY;
+        for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = (e >> 1) * 8 + 2 * t + (e & 1), n8 = 2 * nb + (e >> 1);
-              x[nb][e] = c[n8][0][2 * r + (e & 1)] + c[n8][1][2 * r + (e & 1)];
-              if (key >= valid[nb]) x[nb][e] = -INFINITY;
-            }
-            mx = fmaxf(fmaxf(mx, fmaxf(x[nb][0], x[nb][1])), fmaxf(x[nb][2], x[nb][3]));
+          for (int e = 0; e < 4; ++e) {
+            const int key = (e >> 1) * 8 + 2 * t + (e & 1), n8 = 2 * nb + (e >> 1);
+            x[nb][e] = c[n8][0][e & 1] + c[n8][1][e & 1];
+            if (!all && key >= valid[nb]) x[nb][e] = -INFINITY;
           }
-          mx *= a.scale_log2;
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          if (__any_sync(0xffffffffu, mx > m[r] + kDecLazy)) {
-            const float mn = fmaxf(m[r], mx);
-            const float al = mn == -INFINITY ? 1.f : ex2_approx(m[r] - mn);
-            m[r] = mn;
-            l[r] *= al;
+          mx = fmaxf(fmaxf(mx, fmaxf(x[nb][0], x[nb][1])), fmaxf(x[nb][2], x[nb][3]));
+        }
+        mx *= a.scale_log2;
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (__any_sync(0xffffffffu, mx > m + kDecLazy)) {
+          const float mn = fmaxf(m, mx);
+          const float al = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
+          m = mn;
+          l *= al;
 #pragma unroll
-            for (int k8 = 0; k8 < D / 8; ++k8)
+          for (int k8 = 0; k8 < D / 8; ++k8)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[r][k8][e] *= al;
+            for (int e = 0; e < 4; ++e) o[k8][e] *= al;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = ex2_approx(fmaf(x[nb][e], a.scale_log2, -ref));
+            l += p[e];
           }
-          const float ref = m[r] == -INFINITY ? 0.f : m[r];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            float p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              p[e] = ex2_approx(fmaf(x[nb][e], a.scale_log2, -ref));
-              l[r] += p[e];
-            }
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              hi[r][nb][z] = pack_bf16x2(p[2 * z], p[2 * z + 1]);
-              lo[r][nb][z] = pack_bf16x2(p[2 * z] - __uint_as_float(hi[r][nb][z] << 16),
-                                         p[2 * z + 1] - __uint_as_float(hi[r][nb][z] & 0xFFFF0000u));
-            }
+          for (int z = 0; z < 2; ++z) {
+            hi[nb][z] = pack_bf16x2(p[2 * z], p[2 * z + 1]);
+            lo[nb][z] = pack_bf16x2(p[2 * z] - __uint_as_float(hi[nb][z] << 16),
+                                    p[2 * z + 1] - __uint_as_float(hi[nb][z] & 0xFFFF0000u));
           }
         }
         // O += P V: rows 0-7 the upper part of P, rows 8-15 the lower; V rows
         // behind the end count as zero
+        auto add_pv = [&](auto partial) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-          if (valid[nb] < 16) {
+          for (int nb = 0; nb < NB; ++nb) {
+            uint32_t keep[2];
 #pragma unroll
             for (int z = 0; z < 2; ++z)
               keep[z] = (z * 8 + 2 * t < valid[nb] ? 0xFFFFu : 0u) | (z * 8 + 2 * t + 1 < valid[nb] ? 0xFFFF0000u : 0u);
-          }
 #pragma unroll
-          for (int np = 0; np < D / 16; ++np) {
-            uint32_t b[4];
-            const int ch = 2 * np + vch;
-            ldmatrix_x4_trans(vt + nb * kBlock + vbase + uint32_t(ch >> 3) * 1024u + uint32_t(((ch & 7) ^ (vrow & 7)) << 4),
-                              b);
-            b[0] &= keep[0];
-            b[1] &= keep[1];
-            b[2] &= keep[0];
-            b[3] &= keep[1];
-#pragma unroll
-            for (int r = 0; r < RB; ++r) {
-              mma_16816(o[r][2 * np], hi[r][nb][0], lo[r][nb][0], hi[r][nb][1], lo[r][nb][1], b[0], b[1]);
-              mma_16816(o[r][2 * np + 1], hi[r][nb][0], lo[r][nb][0], hi[r][nb][1], lo[r][nb][1], b[2], b[3]);
+            for (int np = 0; np < D / 16; ++np) {
+              uint32_t b[4];
+              ldmatrix_x4_trans(((vt + vbase) ^ uint32_t((np & 3) << 5)) + nb * kBlock + uint32_t(np >> 2) * 1024u, b);
+              if constexpr (decltype(partial)::value) {
+                b[0] &= keep[0];
+                b[1] &= keep[1];
+                b[2] &= keep[0];
+                b[3] &= keep[1];
+              }
+              mma_16816(o[2 * np], hi[nb][0], lo[nb][0], hi[nb][1], lo[nb][1], b[0], b[1]);
+              mma_16816(o[2 * np + 1], hi[nb][0], lo[nb][0], hi[nb][1], lo[nb][1], b[2], b[3]);
             }
           }
-        }
+        };
+        if (all) add_pv(std::false_type{});
+        else add_pv(std::true_type{});
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(st));
@@ -527,28 +516,24 @@ __global__ void __launch_bounds__(dec_threads(RB), 1) paged_attention_kernel(con
 
       // join the four warps' results of this row
       if (bar_any(1 + group, 128, false)) break;  // the buffer's last readers are done
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (t == 0) ml[gwarp * 8 + g] = make_float2(m, l);
+      float* dst = mrg + (gwarp * 8 + g) * SM::kPitch + 2 * t;
 #pragma unroll
-      for (int r = 0; r < RB; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        const int head = r * 8 + g;
-        if (t == 0) ml[gwarp * RB * 8 + head] = make_float2(m[r], l[r]);
-        float* dst = mrg + (gwarp * RB * 8 + head) * SM::kPitch + 2 * t;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k)
-          *reinterpret_cast<float2*>(dst + 8 * k) = make_float2(o[r][k][0] + o[r][k][2], o[r][k][1] + o[r][k][3]);
-      }
+      for (int k = 0; k < D / 8; ++k)
+        *reinterpret_cast<float2*>(dst + 8 * k) = make_float2(o[k][0] + o[k][2], o[k][1] + o[k][3]);
       if (bar_any(1 + group, 128, false)) break;
       const bool whole = started && (flags & kRowEnd);
       const int64_t row = mt.z;
       const int slot = flags >> kTileRow == 0 ? 0 : 1;  // a partial row is this CTA's first or its last
-      for (int e = gthread * 4; e < v.G * D; e += 512) {
+      for (int e = gthread * 4; e < heads * D; e += 512) {
         const int head = e / D, i = e % D;
         float2 z[4];
         float mm = -INFINITY;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          z[w] = ml[w * RB * 8 + head];
+          z[w] = ml[w * 8 + head];
           mm = fmaxf(mm, z[w].x);
         }
         const float ref = mm == -INFINITY ? 0.f : mm;
@@ -557,7 +542,7 @@ __global__ void __launch_bounds__(dec_threads(RB), 1) paged_attention_kernel(con
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const float f = ex2_approx(z[w].x - ref);
-          const float4 ow = *reinterpret_cast<const float4*>(mrg + (w * RB * 8 + head) * SM::kPitch + i);
+          const float4 ow = *reinterpret_cast<const float4*>(mrg + (w * 8 + head) * SM::kPitch + i);
           ll += z[w].y * f;
           s4.x += ow.x * f;
           s4.y += ow.y * f;
@@ -566,10 +551,10 @@ __global__ void __launch_bounds__(dec_threads(RB), 1) paged_attention_kernel(con
         }
         if (whole) {
           const float inv = ll > 0.f ? 1.f / ll : 0.f;
-          *reinterpret_cast<uint2*>(a.O + (row * v.G + head) * D + i) =
+          *reinterpret_cast<uint2*>(a.O + (row * v.G + head0 + head) * D + i) =
               make_uint2(pack_bf16x2(s4.x * inv, s4.y * inv), pack_bf16x2(s4.z * inv, s4.w * inv));
         } else {
-          const int64_t at = (int64_t(blockIdx.x) * 2 + slot) * (RB * 8) + head;
+          const int64_t at = (int64_t(blockIdx.x) * 2 + slot) * (split ? 16 : 8) + head0 + head;
           *reinterpret_cast<float4*>(a.part_o + at * D + i) = s4;
           if (i == 0) a.part_ml[at] = make_float2(mm, ll);
         }

@@ -10,6 +10,7 @@
 
 #include <climits>
 
+#include "ab_norm_rope.cuh"
 #include "ab_ptx.cuh"
 
 namespace ab {
@@ -473,137 +474,188 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 // and sum of exponentials per head) go to the workspace, then every chunk is
 // normalised with the row's sums.
 //
-// Scores: a warp takes 32 pages of one head, four products of 8 pages, with
-// the summaries loaded straight into the products' registers: the order of
-// the d products is free, so lane (g, t) takes 16-byte pieces t, t + 4, ... of
-// page g's summary, and the query's registers follow the same order.
-constexpr int kSelPages = 128;    // pages per CTA and step: 32 per warp
-constexpr int kSelThreads = 128;
+// Scores: a warp takes 32 pages of one head, four products of 8 pages.  The
+// order of the d products is free, so lane (g, t) takes the 16-byte pieces t,
+// t + 4, ... of page g's summary and the query's registers follow the same
+// order: what a lane needs it copies itself, one step of 32 pages ahead of its
+// use (cp.async into its own places, no barrier).  Bound by memory: 2 d bytes
+// of summary per page and head, and 8 G for its scores, mostly in L2.
+constexpr int kSelPages = 32;
+constexpr int kSelWarps = 8;
+constexpr int kSelStages = 3;
 
 struct SelectArgs {
   PagedView v;
   const __nv_bfloat16* Q;     // [T, Hq, d]
   const __nv_bfloat16* ksum;  // [num_pages, Hkv, d]
-  float* scores;              // [S, Hkv, G, max_pages], log2 domain
+  float* scores;              // [S, Hkv, G, pitch], log2 domain
   float2* part;               // [S, Hkv, G, chunks]: maximum, sum of exp2
   float* P;                   // [S, Hkv, max_pages]
-  int chunks;                 // ceil(max_pages / 128)
+  int chunks;                 // ceil(max_pages / 32)
+  int pitch;                  // max_pages rounded up to a multiple of 4
   float scale_log2;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kSelThreads, 4) page_score_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kSelWarps * 32, 1) page_score_kernel(const __grid_constant__ SelectArgs a) {
   constexpr int kPieces = D / 32;  // 16-byte pieces of a summary per lane
+  extern __shared__ uint4 sel_smem[];  // [warps][stages][4 kPieces][32 lanes]
   __shared__ int2 sums[kMaxSeqs / 32];
-  __shared__ float2 wpart[4][kMaxGroup];
+  pdl_wait();
+  pdl_trigger();
   const PagedView& v = a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  auto chunks_of = [&](int s) { return (pages_of(v, seq_len(v, s)) + kSelPages - 1) / kSelPages; };
-  auto tiles = [&](int s) { return query_row(v, s) < 0 ? 0 : chunks_of(s) * v.Hkv; };
-  const Share sh =
-      share_work([&](int s) { return UnitWork{1, tiles(s)}; }, 0, v.S, blockIdx.x, gridDim.x, sums);
-  int s = sh.unit, off = sh.off;
-  for (int left = sh.n; left > 0; --left, ++off) {
-    if (off >= tiles(s)) {
-      s = next_unit(tiles, v.S, s + 1);
-      off = 0;
-      if (s >= v.S) return;
+  auto chunks_of = [&](int s) {
+    return query_row(v, s) < 0 ? 0 : (pages_of(v, seq_len(v, s)) + kSelPages - 1) / kSelPages;
+  };
+  auto work = [&](int s) { return UnitWork{v.Hkv, chunks_of(s)}; };
+  const Share sh = share_work(work, 0, v.S, blockIdx.x * kSelWarps + warp, gridDim.x * kSelWarps, sums);
+  uint4* const mine = sel_smem + size_t(warp) * kSelStages * 4 * kPieces * 32 + lane;
+
+  // a step: head hk of pages [32 chunk, 32 chunk + 32) of sequence s, heads innermost
+  struct Step {
+    int s, chunk, hk, pages, len, row;  // row: of Q
+  };
+  auto open_seq = [&](Step& x) {
+    x.len = seq_len(v, x.s);
+    x.pages = pages_of(v, x.len);
+    x.row = query_row(v, x.s);
+  };
+  auto next = [&](Step& x) {
+    if (++x.hk < v.Hkv) return;
+    x.hk = 0;
+    if (++x.chunk * kSelPages < x.pages) return;
+    x.chunk = 0;
+    x.s = next_unit([&](int s) { return chunks_of(s); }, v.S, x.s + 1);
+    if (x.s < v.S) open_seq(x);
+  };
+  int id[4];  // this lane's pages of the step that is copied next
+  auto look_up = [&](const Step& x) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int j = x.chunk * kSelPages + n * 8 + g;
+      id[n] = -1;
+      if (j < x.pages) {
+        id[n] = __ldg(v.table + int64_t(x.s) * v.max_pages + j);
+        if (id[n] < 0 || id[n] >= v.num_pages) {
+          raise_error(AB_ERR_CAPACITY);
+          id[n] = -1;
+        }
+      }
     }
-    const int len = seq_len(v, s), pages = pages_of(v, len);
-    const int hk = off % v.Hkv, chunk = off / v.Hkv;
-    const int j0 = chunk * kSelPages + warp * 32;
+  };
+  auto issue = [&](const Step& x, int stage) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const __nv_bfloat16* src = a.ksum + (int64_t(id[n]) * v.Hkv + x.hk) * D + t * 8;
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        uint4* dst = mine + ((stage * 4 + n) * kPieces + p) * 32;
+        if (id[n] >= 0) cp_async16(smem_u32(dst), src + p * 32);
+        else *dst = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  };
+  if (sh.n == 0) return;
+  Step cur{sh.unit, 0, 0, 0, 0, 0};
+  int off = sh.off;
+  if (off >= v.Hkv * chunks_of(cur.s)) {
+    cur.s = next_unit([&](int s) { return chunks_of(s); }, v.S, cur.s + 1);
+    off = 0;
+  }
+  if (cur.s >= v.S) return;
+  open_seq(cur);
+  cur.chunk = off / v.Hkv;
+  cur.hk = off - cur.chunk * v.Hkv;
+  Step ahead = cur;
+  int left_ahead = sh.n;
+  look_up(ahead);
+  auto copy_next = [&](int stage) {
+    if (left_ahead > 0) {
+      issue(ahead, stage);
+      if (--left_ahead > 0) {
+        const int s = ahead.s, chunk = ahead.chunk;
+        next(ahead);
+        if (ahead.s >= v.S) left_ahead = 0;
+        else if (ahead.s != s || ahead.chunk != chunk) look_up(ahead);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kSelStages - 1; ++k) copy_next(k);
+
+  int stage = 0;
+  for (int left = sh.n; left > 0 && cur.s < v.S; --left) {
+    copy_next(stage == 0 ? kSelStages - 1 : stage - 1);
     // query: rows g and g + 8 of the 16 x d operand, pieces in the keys' order
-    const __nv_bfloat16* q = a.Q + (int64_t(query_row(v, s)) * v.Hkv + hk) * v.G * D + t * 8;
+    const __nv_bfloat16* q = a.Q + (int64_t(cur.row) * v.Hkv + cur.hk) * v.G * D + t * 8;
     uint4 qa[kPieces], qb[kPieces];
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
       qa[p] = g < v.G ? __ldg(reinterpret_cast<const uint4*>(q + g * D + p * 32)) : make_uint4(0u, 0u, 0u, 0u);
       qb[p] = g + 8 < v.G ? __ldg(reinterpret_cast<const uint4*>(q + (g + 8) * D + p * 32)) : make_uint4(0u, 0u, 0u, 0u);
     }
-    uint4 kx[4][kPieces];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int j = j0 + n * 8 + g;
-      int id = -1;
-      if (j < pages) {
-        id = __ldg(v.table + int64_t(s) * v.max_pages + j);
-        if (id < 0 || id >= v.num_pages) {
-          raise_error(AB_ERR_CAPACITY);
-          id = -1;
-        }
-      }
-      const uint4* src = reinterpret_cast<const uint4*>(a.ksum + (int64_t(id) * v.Hkv + hk) * D + t * 8);
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p) kx[n][p] = id >= 0 ? __ldg(src + p * 4) : make_uint4(0u, 0u, 0u, 0u);
-    }
+    cp_async_wait<kSelStages - 1>();
+    const uint4* kx = mine + stage * 4 * kPieces * 32;
     float m[2] = {-INFINITY, -INFINITY}, x[4][4];
+    const int j0 = cur.chunk * kSelPages;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       float c0[4] = {}, c1[4] = {};
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
-        mma_16816(c0, qa[p].x, qb[p].x, qa[p].y, qb[p].y, kx[n][p].x, kx[n][p].y);
-        mma_16816(c1, qa[p].z, qb[p].z, qa[p].w, qb[p].w, kx[n][p].z, kx[n][p].w);
+        const uint4 k = kx[(n * kPieces + p) * 32];
+        mma_16816(c0, qa[p].x, qb[p].x, qa[p].y, qb[p].y, k.x, k.y);
+        mma_16816(c1, qa[p].z, qb[p].z, qa[p].w, qb[p].w, k.z, k.w);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = j0 + n * 8 + t * 2 + (e & 1);
-        const int keys = min(v.page, len - (j << v.page_shift));
         // log2 of the number of keys: whole pages take the exact integer
-        const float bias = keys == v.page ? float(v.page_shift) : log2f(float(max(keys, 1)));
-        x[n][e] = j < pages ? fmaf(c0[e] + c1[e], a.scale_log2, bias) : -INFINITY;
+        const int keys = cur.len - (j << v.page_shift);
+        const float bias = keys >= v.page ? float(v.page_shift) : log2f(float(max(keys, 1)));
+        x[n][e] = j < cur.pages ? fmaf(c0[e] + c1[e], a.scale_log2, bias) : -INFINITY;
         m[e >> 1] = fmaxf(m[e >> 1], x[n][e]);
       }
     }
-    float l[2] = {0.f, 0.f};
+    const int64_t row = (int64_t(cur.s) * v.Hkv + cur.hk) * v.G;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
+      if (k * 8 >= v.G) break;
       m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 1));
       m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 2));
       const float ref = m[k] == -INFINITY ? 0.f : m[k];
+      float l = 0.f;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) l[k] += exp2f(x[n][2 * k] - ref) + exp2f(x[n][2 * k + 1] - ref);
-      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
-      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
-      if (t == 0) wpart[warp][g + 8 * k] = make_float2(m[k], l[k]);
-    }
-    const int64_t row = int64_t(s) * v.Hkv + hk;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
+      for (int n = 0; n < 4; ++n) l += ex2_approx(x[n][2 * k] - ref) + ex2_approx(x[n][2 * k + 1] - ref);
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
       const int h = g + 8 * k;
       if (h < v.G) {
-        float* dst = a.scores + (row * v.G + h) * v.max_pages;
+        if (t == 0) a.part[(row + h) * a.chunks + cur.chunk] = make_float2(m[k], l);
+        float* dst = a.scores + (row + h) * a.pitch + j0 + t * 2;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int j = j0 + n * 8 + t * 2;
-          if (j < pages) dst[j] = x[n][2 * k];
-          if (j + 1 < pages) dst[j + 1] = x[n][2 * k + 1];
-        }
+        for (int n = 0; n < 4; ++n)
+          if (j0 + n * 8 + t * 2 < a.pitch)  // the pitch is even, the pair lies inside
+            *reinterpret_cast<float2*>(dst + n * 8) = make_float2(x[n][2 * k], x[n][2 * k + 1]);
       }
     }
-    __syncthreads();
-    if (threadIdx.x < v.G) {
-      float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) mm = fmaxf(mm, wpart[w][threadIdx.x].x);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2 z = wpart[w][threadIdx.x];
-        ll += z.x == -INFINITY ? 0.f : z.y * exp2f(z.x - mm);
-      }
-      a.part[(row * v.G + threadIdx.x) * a.chunks + chunk] = make_float2(mm, ll);
-    }
-    __syncthreads();  // wpart is reused
+    next(cur);
+    stage = stage == kSelStages - 1 ? 0 : stage + 1;
   }
+  cp_async_wait<0>();
 }
 
 // Normalisation: every CTA joins the row's partial sums, then turns 1024
 // pages' scores into P, at most 8 steps apart along the row.
 constexpr int kNormThreads = 256;
 
-__global__ void __launch_bounds__(kNormThreads) page_mass_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kNormThreads) page_mass_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ float2 ml[kMaxGroup];  // maximum, 1 / (G sum)
+  pdl_wait();
+  pdl_trigger();
   const PagedView& v = a.v;
   const int s = blockIdx.z, hk = blockIdx.y;
   if (query_row(v, s) < 0) return;
@@ -615,13 +667,17 @@ __global__ void __launch_bounds__(kNormThreads) page_mass_kernel(const SelectArg
   for (int h = warp; h < v.G; h += kNormThreads / 32) {
     const float2* part = a.part + (row * v.G + h) * a.chunks;
     float m = -INFINITY, l = 0.f;
-    for (int k = lane; k < chunks; k += 32) {
-      const float2 z = part[k];
-      if (z.x > m) {
-        l *= exp2f(m - z.x);
-        m = z.x;
+    for (int k0 = lane; k0 < chunks; k0 += 128) {
+      float2 z[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) z[k] = k0 + 32 * k < chunks ? part[k0 + 32 * k] : make_float2(-INFINITY, 0.f);
+      const float mm = fmaxf(fmaxf(fmaxf(z[0].x, z[1].x), fmaxf(z[2].x, z[3].x)), m);
+      if (mm != -INFINITY) {
+        l *= exp2f(m - mm);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) l += z[k].y * exp2f(z[k].x - mm);
+        m = mm;
       }
-      if (z.x != -INFINITY) l += z.y * exp2f(z.x - m);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -633,17 +689,23 @@ __global__ void __launch_bounds__(kNormThreads) page_mass_kernel(const SelectArg
     if (lane == 0) ml[h] = make_float2(m, 1.f / (l * float(v.G)));
   }
   __syncthreads();
-  for (int j0 = blockIdx.x * 4 * kNormThreads; j0 < pages; j0 += gridDim.x * 4 * kNormThreads) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = j0 + k * kNormThreads + threadIdx.x;
-      if (j < pages) {
-        const float* src = a.scores + row * v.G * v.max_pages + j;
-        float p = 0.f;
-        for (int h = 0; h < v.G; ++h) p += exp2f(src[int64_t(h) * v.max_pages] - ml[h].x) * ml[h].y;
-        a.P[row * v.max_pages + j] = p;
-      }
+  for (int j = (blockIdx.x * kNormThreads + threadIdx.x) * 4; j < pages; j += gridDim.x * 4 * kNormThreads) {
+    const float* src = a.scores + row * v.G * a.pitch + j;
+    float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int h = 0; h < v.G; ++h) {
+      const float4 x = *reinterpret_cast<const float4*>(src + int64_t(h) * a.pitch);
+      const float2 z = ml[h];
+      p.x += ex2_approx(x.x - z.x) * z.y;
+      p.y += ex2_approx(x.y - z.x) * z.y;
+      p.z += ex2_approx(x.z - z.x) * z.y;
+      p.w += ex2_approx(x.w - z.x) * z.y;
     }
+    float* dst = a.P + row * v.max_pages + j;
+    dst[0] = p.x;
+    if (j + 1 < pages) dst[1] = p.y;
+    if (j + 2 < pages) dst[2] = p.z;
+    if (j + 3 < pages) dst[3] = p.w;
   }
 }
 
@@ -651,27 +713,36 @@ __global__ void __launch_bounds__(kNormThreads) page_mass_kernel(const SelectArg
 // The newest min(recent, Kb) pages and the Kb minus that many others of
 // largest P, in ascending order; ties go to the lower page.  Keys are P's bits
 // (P >= 0 orders as its bits; anything else counts as 0), the newest pages get
-// the largest key.  One CTA per row: a radix select over four digits of 8
-// bits, then one ordered pass.
+// the largest key.  One CTA per row, the row's keys in shared memory: a radix
+// select over digits of 11, 11 and 9 bits (the first holds exponent and three
+// bits of the fraction, so that the counters of a row's few octaves do not
+// collide), then every thread writes the kept pages of its own run of the row.
+// Bound by the latency of its steps.
 struct TopkArgs {
   const float* P;
   const int32_t* lens;
   int32_t *idx, *count;
   int Hkv, page, page_shift, max_pages, recent;
+  int cap;  // keys that fit in shared memory (longer rows are read anew in each step)
   double keep;
 };
-constexpr int kTopkThreads = 256;
+constexpr int kTopkThreads = 512;
+constexpr int kTopkMaxKeys = 24576;  // 96 KB: two CTAs an SM
+constexpr int kTopkBins = 2048;
 
 __device__ __forceinline__ int page_budget(int n, double keep) {
   const double kb = floor(keep * double(n) + 0.5);
   return kb < 1.0 ? min(1, n) : kb > double(n) ? n : int(kb);
 }
 
-__global__ void __launch_bounds__(kTopkThreads) page_topk_kernel(const TopkArgs a) {
-  __shared__ uint32_t hist[256];
+__global__ void __launch_bounds__(kTopkThreads) page_topk_kernel(const __grid_constant__ TopkArgs a) {
+  extern __shared__ uint32_t topk_keys[];
+  __shared__ uint32_t hist[kTopkBins];
   __shared__ uint32_t sel[2];
-  __shared__ uint32_t scan[8];
+  __shared__ uint32_t wsum[2][kTopkThreads / 32];
   const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
   int len = __ldg(a.lens + row / a.Hkv);
   if (len < 0 || len > a.max_pages << a.page_shift) {
     if (tid == 0) raise_error(AB_ERR_CAPACITY);
@@ -683,90 +754,96 @@ __global__ void __launch_bounds__(kTopkThreads) page_topk_kernel(const TopkArgs 
   if (n == 0) return;
   const int newest = n - min(a.recent, Kb);  // pages from here on are kept
   const float* P = a.P + int64_t(row) * a.max_pages;
-  auto key_of = [&](int j) -> uint32_t {
-    const float p = __ldg(P + j);
-    return j >= newest ? 0xFFFFFFFFu : p > 0.f ? __float_as_uint(p) : 0u;
+  auto make_key = [&](int j, float p) -> uint32_t {
+    return j >= newest ? 0x7FFFFFFFu : p > 0.f ? __float_as_uint(p) : 0u;
+  };
+  const bool cached = n <= a.cap;
+  if (cached) {
+    for (int j0 = tid; j0 < n; j0 += 4 * kTopkThreads) {
+      float p[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[k] = j0 + k * kTopkThreads < n ? __ldg(P + j0 + k * kTopkThreads) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j0 + k * kTopkThreads < n) topk_keys[j0 + k * kTopkThreads] = make_key(j0 + k * kTopkThreads, p[k]);
+    }
+  }
+  auto key_of = [&](int j) -> uint32_t { return cached ? topk_keys[j] : make_key(j, __ldg(P + j)); };
+  // inclusive sums over the block's threads of two counts
+  auto block_scan = [&](uint32_t& x, uint32_t& y) {
+    const uint32_t x0 = x, y0 = y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t p = __shfl_up_sync(0xffffffffu, x, o), q = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) {
+        x += p;
+        y += q;
+      }
+    }
+    if (lane == 31) {
+      wsum[0][warp] = x;
+      wsum[1][warp] = y;
+    }
+    __syncthreads();
+    uint32_t p = lane < warp ? wsum[0][lane & 15] : 0u, q = lane < warp ? wsum[1][lane & 15] : 0u;
+    p = __reduce_add_sync(0xffffffffu, p);
+    q = __reduce_add_sync(0xffffffffu, q);
+    x += p - x0;  // exclusive
+    y += q - y0;
   };
   uint32_t prefix = 0, pmask = 0, need = uint32_t(Kb);
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 20 : pass == 1 ? 9 : 0;
+    const uint32_t digits = pass == 2 ? 511u : 2047u;
+    for (int k = tid; k < kTopkBins; k += kTopkThreads) hist[k] = 0;
     __syncthreads();
     for (int j = tid; j < n; j += kTopkThreads) {
       const uint32_t k = key_of(j);
-      if ((k & pmask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      if ((k & pmask) == prefix) atomicAdd(&hist[(k >> shift) & digits], 1u);
     }
     __syncthreads();
-    if (warp == 0) {  // lane l: bins 255 - 8 l down to 248 - 8 l
-      uint32_t c[8], tot = 0;
+    // thread t: bins 2047 - 4 t down to 2044 - 4 t
+    constexpr int kPer = kTopkBins / kTopkThreads;
+    uint32_t c[kPer], tot = 0, none = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        c[k] = hist[255 - 8 * lane - k];
-        tot += c[k];
-      }
-      uint32_t incl = tot;
+    for (int k = 0; k < kPer; ++k) {
+      c[k] = hist[kTopkBins - 1 - kPer * tid - k];
+      tot += c[k];
+    }
+    uint32_t above = tot;
+    block_scan(above, none);
+    if (above < need && need <= above + tot) {  // exactly one thread
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      uint32_t above = incl - tot;
-      if (above < need && need <= incl) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (above < need && need <= above + c[k]) {
-            sel[0] = uint32_t(255 - 8 * lane - k);
-            sel[1] = need - above;
-          }
-          above += c[k];
+      for (int k = 0; k < kPer; ++k) {
+        if (above < need && need <= above + c[k]) {
+          sel[0] = uint32_t(kTopkBins - 1 - kPer * tid - k);
+          sel[1] = need - above;
         }
+        above += c[k];
       }
     }
     __syncthreads();
     prefix |= sel[0] << shift;
-    pmask |= 0xFFu << shift;
+    pmask |= digits << shift;
     need = sel[1];
   }
   // kept: keys above the threshold, and the lowest `need` pages of those equal to it
+  const int per = (n + kTopkThreads - 1) / kTopkThreads, first = tid * per, last = min(first + per, n);
+  uint32_t n_gt = 0, n_eq = 0;
+  for (int j = first; j < last; ++j) {
+    const uint32_t k = key_of(j);
+    n_gt += k > prefix ? 1u : 0u;
+    n_eq += k == prefix ? 1u : 0u;
+  }
+  block_scan(n_gt, n_eq);
   int32_t* out = a.idx + int64_t(row) * a.max_pages;
-  uint32_t base_gt = 0, base_eq = 0;
-  for (int c0 = 0; c0 < n; c0 += 4 * kTopkThreads) {
-    const int j0 = c0 + 4 * tid;
-    uint32_t gt = 0, eq = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (j0 + q < n) {
-        const uint32_t k = key_of(j0 + q);
-        gt |= (k > prefix ? 1u : 0u) << q;
-        eq |= (k == prefix ? 1u : 0u) << q;
-      }
-    }
-    const uint32_t mine = uint32_t(__popc(gt)) | (uint32_t(__popc(eq)) << 16);
-    uint32_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    __syncthreads();  // scan[] may still be read for the chunk before
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    uint32_t before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      if (w < warp) before += scan[w];
-      total += scan[w];
-    }
-    const uint32_t excl = before + incl - mine;
-    uint32_t n_gt = base_gt + (excl & 0xFFFFu), n_eq = base_eq + (excl >> 16);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const bool is_gt = (gt >> q) & 1u, is_eq = (eq >> q) & 1u;
-      if (is_gt || (is_eq && n_eq < need)) out[n_gt + min(n_eq, need)] = j0 + q;
-      n_gt += is_gt ? 1u : 0u;
-      n_eq += is_eq ? 1u : 0u;
-    }
-    base_gt += total & 0xFFFFu;
-    base_eq += total >> 16;
+  for (int j = first; j < last; ++j) {
+    const uint32_t k = key_of(j);
+    const bool gt = k > prefix, eq = k == prefix;
+    if (gt || (eq && n_eq < need)) out[n_gt + min(n_eq, need)] = j;
+    n_gt += gt ? 1u : 0u;
+    n_eq += eq ? 1u : 0u;
   }
 }
 

@@ -237,7 +237,7 @@ PagedWorkspace paged_workspace(const ab_paged_params* p) {
   PagedWorkspace w{};
   const size_t rows = size_t(p->S) * p->Hq;
   const size_t chunks = (size_t(p->max_pages) + kSelPages - 1) / kSelPages;
-  w.off_part = align256(w.off_scores + rows * p->max_pages * 4);
+  w.off_part = align256(w.off_scores + rows * ((size_t(p->max_pages) + 3) / 4 * 16));
   w.select = align256(w.off_part + rows * chunks * 8);
   const size_t heads = p->Hq / p->Hkv > 8 ? 16 : 8;
   w.off_part_o = align256(kDecMaxParts * sizeof(DecMeta));
@@ -312,15 +312,17 @@ ab_status run_paged_select(const ab_paged_params* p, const PagedView& v, const v
   a.scale_log2 = float(1.4426950408889634 / std::sqrt(double(p->d)));
   const int sms = sm_count();
   if (!sms) return AB_ERR_CUDA;
-  const int64_t most = int64_t(p->S) * p->Hkv * a.chunks;
-  const unsigned grid = unsigned(most < sms * 4 ? most : sms * 4);
-  if (p->d == 128) page_score_kernel<128><<<grid, kSelThreads, 0, st>>>(a);
-  else page_score_kernel<64><<<grid, kSelThreads, 0, st>>>(a);
+  a.pitch = (p->max_pages + 3) / 4 * 4;
+  const int64_t most = (int64_t(p->S) * p->Hkv * a.chunks + kSelWarps - 1) / kSelWarps;
+  const unsigned grid = unsigned(most < sms ? most : sms);
+  auto score = p->d == 128 ? page_score_kernel<128> : page_score_kernel<64>;
+  const int smem = kSelWarps * kSelStages * 32 * p->d * 2;
+  if (set_smem(score, smem) != cudaSuccess) return AB_ERR_CUDA;
+  score<<<grid, kSelWarps * 32, smem, st>>>(a);
   if (launch_status() != AB_OK) return AB_ERR_CUDA;
   int steps = (p->max_pages + 4 * kNormThreads - 1) / (4 * kNormThreads);
   steps = steps > 8 ? 8 : steps;
-  page_mass_kernel<<<dim3(unsigned(steps), unsigned(p->Hkv), unsigned(p->S)), kNormThreads, 0, st>>>(a);
-  return launch_status();
+  return launch_after(page_mass_kernel, dim3(unsigned(steps), unsigned(p->Hkv), unsigned(p->S)), kNormThreads, 0, st, a);
 }
 
 ab_status run_paged_topk(const ab_paged_params* p, const float* P, const int32_t* lens, int32_t* idx, int32_t* count,
@@ -329,7 +331,10 @@ ab_status run_paged_topk(const ab_paged_params* p, const float* P, const int32_t
   a.P = P; a.lens = lens; a.idx = idx; a.count = count;
   a.Hkv = p->Hkv; a.page = p->page; a.page_shift = log2_of(p->page); a.max_pages = p->max_pages;
   a.recent = p->recent; a.keep = double(p->keep_ratio);
-  page_topk_kernel<<<unsigned(p->S * p->Hkv), kTopkThreads, 0, st>>>(a);
+  a.cap = p->max_pages < kTopkMaxKeys ? p->max_pages : kTopkMaxKeys;
+  const int smem = a.cap * 4;
+  if (smem > 36 * 1024 && set_smem(page_topk_kernel, smem) != cudaSuccess) return AB_ERR_CUDA;
+  page_topk_kernel<<<unsigned(p->S * p->Hkv), kTopkThreads, smem, st>>>(a);
   return launch_status();
 }
 

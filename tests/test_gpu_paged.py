@@ -246,6 +246,17 @@ def test_topk(dev, keep, recent):
             assert (idx[s, h, len(want):] == -4).all()
 
 
+def test_topk_rows_beyond_shared_memory(dev):
+    n, most = 24577, 30000
+    P = torch.rand(2, 1, most, generator=torch.Generator().manual_seed(14))
+    P[1] = (P[1] * 50).round() / 50
+    pp = ab.PagedParams(2, 1, 1, 64, 16, 4, most, keep_ratio=0.3, recent=2)
+    idx, count = ab.ab_paged_topk(pp, P.to(dev), ints([n * 16, most * 16 - 5], dev))
+    for s, k in enumerate((n, most)):
+        want = ref.topk(P[s, 0], k, 0.3, 2)
+        assert count[s, 0] == len(want) and idx[s, 0, :len(want)].tolist() == want
+
+
 # --------------------------------------------------------------- attention
 def _check_attention(O, q, c, lists=None, rows=None):
     G = q.shape[1] // c.Hkv

@@ -482,7 +482,7 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 // of summary per page and head, and 8 G for its scores, mostly in L2.
 constexpr int kSelPages = 32;
 constexpr int kSelWarps = 8;
-constexpr int kSelStages = 3;
+__host__ __device__ constexpr int sel_stages(int D) { return D == 128 ? 3 : 6; }
 
 struct SelectArgs {
   PagedView v;
@@ -496,9 +496,12 @@ struct SelectArgs {
   float scale_log2;
 };
 
-template <int D>
+// kWide: more than 8 query heads per key/value head.
+template <int D, bool kWide>
 __global__ void __launch_bounds__(kSelWarps * 32, 1) page_score_kernel(const __grid_constant__ SelectArgs a) {
   constexpr int kPieces = D / 32;  // 16-byte pieces of a summary per lane
+  constexpr int kStages = sel_stages(D);
+  constexpr int kHalves = kWide ? 2 : 1;  // blocks of 8 heads
   extern __shared__ uint4 sel_smem[];  // [warps][stages][4 kPieces][32 lanes]
   __shared__ int2 sums[kMaxSeqs / 32];
   pdl_wait();
@@ -510,140 +513,166 @@ __global__ void __launch_bounds__(kSelWarps * 32, 1) page_score_kernel(const __g
     return query_row(v, s) < 0 ? 0 : (pages_of(v, seq_len(v, s)) + kSelPages - 1) / kSelPages;
   };
   auto work = [&](int s) { return UnitWork{v.Hkv, chunks_of(s)}; };
-  const Share sh = share_work(work, 0, v.S, blockIdx.x * kSelWarps + warp, gridDim.x * kSelWarps, sums);
-  uint4* const mine = sel_smem + size_t(warp) * kSelStages * 4 * kPieces * 32 + lane;
+  const Share sh = share_work(work, 0, v.S, blockIdx.x, gridDim.x, sums);
+  uint4* const mine = sel_smem + size_t(warp) * kStages * 4 * kPieces * 32 + lane;
+  const int n_steps = (sh.n - warp + kSelWarps - 1) / kSelWarps;  // this warp's: every 8th of the CTA's
+  if (n_steps <= 0) return;
 
-  // a step: head hk of pages [32 chunk, 32 chunk + 32) of sequence s, heads innermost
+  // A step is head hk of pages [32 chunk, 32 chunk + 32) of sequence s; heads
+  // are innermost, so the warps of a CTA read neighbouring heads of the same
+  // pages at about the same time (a page's summaries are contiguous).
   struct Step {
-    int s, chunk, hk, pages, len, row;  // row: of Q
+    int s, pages, len, row, chunk, hk;  // row: of Q
   };
   auto open_seq = [&](Step& x) {
     x.len = seq_len(v, x.s);
     x.pages = pages_of(v, x.len);
     x.row = query_row(v, x.s);
   };
-  auto next = [&](Step& x) {
-    if (++x.hk < v.Hkv) return;
-    x.hk = 0;
-    if (++x.chunk * kSelPages < x.pages) return;
-    x.chunk = 0;
-    x.s = next_unit([&](int s) { return chunks_of(s); }, v.S, x.s + 1);
-    if (x.s < v.S) open_seq(x);
-  };
-  int id[4];  // this lane's pages of the step that is copied next
-  auto look_up = [&](const Step& x) {
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int j = x.chunk * kSelPages + n * 8 + g;
-      id[n] = -1;
-      if (j < x.pages) {
-        id[n] = __ldg(v.table + int64_t(x.s) * v.max_pages + j);
-        if (id[n] < 0 || id[n] >= v.num_pages) {
-          raise_error(AB_ERR_CAPACITY);
-          id[n] = -1;
-        }
+  auto settle = [&](Step& x) -> bool {  // the step `hk` heads behind the start of its chunk
+    while (x.hk >= v.Hkv) {
+      x.hk -= v.Hkv;
+      if (++x.chunk * kSelPages >= x.pages) {
+        x.chunk = 0;
+        x.s = next_unit([&](int s) { return chunks_of(s); }, v.S, x.s + 1);
+        if (x.s >= v.S) return false;
+        open_seq(x);
       }
     }
+    return true;
   };
-  auto issue = [&](const Step& x, int stage) {
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const __nv_bfloat16* src = a.ksum + (int64_t(id[n]) * v.Hkv + x.hk) * D + t * 8;
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p) {
-        uint4* dst = mine + ((stage * 4 + n) * kPieces + p) * 32;
-        if (id[n] >= 0) cp_async16(smem_u32(dst), src + p * 32);
-        else *dst = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-  };
-  if (sh.n == 0) return;
-  Step cur{sh.unit, 0, 0, 0, 0, 0};
-  int off = sh.off;
-  if (off >= v.Hkv * chunks_of(cur.s)) {
-    cur.s = next_unit([&](int s) { return chunks_of(s); }, v.S, cur.s + 1);
-    off = 0;
-  }
-  if (cur.s >= v.S) return;
+  Step cur{sh.unit, 0, 0, 0, sh.off / v.Hkv, 0};
   open_seq(cur);
-  cur.chunk = off / v.Hkv;
-  cur.hk = off - cur.chunk * v.Hkv;
+  cur.hk = sh.off - cur.chunk * v.Hkv + warp;
+  if (cur.chunk * kSelPages >= cur.pages) {  // one past the unit's last step
+    --cur.chunk;
+    cur.hk += v.Hkv;
+  }
+  if (!settle(cur)) return;
+
+  // copies, kStages - 1 steps ahead
   Step ahead = cur;
-  int left_ahead = sh.n;
-  look_up(ahead);
+  int left_ahead = n_steps;
+  int id[4];  // this lane's pages of the step ahead, as read: looked at when they are copied
+  auto look_up = [&]() {
+    const int32_t* from = v.table + int64_t(ahead.s) * v.max_pages + ahead.chunk * kSelPages + g;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) id[n] = ahead.chunk * kSelPages + n * 8 + g < ahead.pages ? __ldg(from + n * 8) : 0;
+  };
+  look_up();
   auto copy_next = [&](int stage) {
     if (left_ahead > 0) {
-      issue(ahead, stage);
+      uint4* dst = mine + stage * 4 * kPieces * 32;
+      const __nv_bfloat16* base = a.ksum + int64_t(ahead.hk) * D + t * 8;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const bool there = uint32_t(id[n]) < uint32_t(v.num_pages);
+        if (!there) raise_error(AB_ERR_CAPACITY);  // its score is that of a zero summary
+        const __nv_bfloat16* src = base + int64_t(id[n]) * v.Hkv * D;
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+          if (there) cp_async16(smem_u32(dst + (n * kPieces + p) * 32), src + p * 32);
+          else dst[(n * kPieces + p) * 32] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
       if (--left_ahead > 0) {
         const int s = ahead.s, chunk = ahead.chunk;
-        next(ahead);
-        if (ahead.s >= v.S) left_ahead = 0;
-        else if (ahead.s != s || ahead.chunk != chunk) look_up(ahead);
+        ahead.hk += kSelWarps;
+        if (!settle(ahead)) left_ahead = 0;
+        else if (ahead.s != s || ahead.chunk != chunk) look_up();
       }
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int k = 0; k < kSelStages - 1; ++k) copy_next(k);
+  for (int k = 0; k < kStages - 1; ++k) copy_next(k);
 
-  int stage = 0;
-  for (int left = sh.n; left > 0 && cur.s < v.S; --left) {
-    copy_next(stage == 0 ? kSelStages - 1 : stage - 1);
-    // query: rows g and g + 8 of the 16 x d operand, pieces in the keys' order
-    const __nv_bfloat16* q = a.Q + (int64_t(cur.row) * v.Hkv + cur.hk) * v.G * D + t * 8;
-    uint4 qa[kPieces], qb[kPieces];
+  // query: rows g (and g + 8) of the 16 x d operand, pieces in the keys' order,
+  // read a step ahead
+  uint4 qx[kHalves][kPieces], qn[kHalves][kPieces];
+  auto read_query = [&](const Step& x) {
+    const __nv_bfloat16* q = a.Q + ((int64_t(x.row) * v.Hkv + x.hk) * v.G + g) * D + t * 8;
 #pragma unroll
-    for (int p = 0; p < kPieces; ++p) {
-      qa[p] = g < v.G ? __ldg(reinterpret_cast<const uint4*>(q + g * D + p * 32)) : make_uint4(0u, 0u, 0u, 0u);
-      qb[p] = g + 8 < v.G ? __ldg(reinterpret_cast<const uint4*>(q + (g + 8) * D + p * 32)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int k = 0; k < kHalves; ++k)
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+        qn[k][p] = g + 8 * k < v.G ? __ldg(reinterpret_cast<const uint4*>(q + k * 8 * D + p * 32)) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  read_query(cur);
+  int stage = 0;
+  for (int left = n_steps; left > 0; --left) {
+    copy_next(stage == 0 ? kStages - 1 : stage - 1);
+#pragma unroll
+    for (int k = 0; k < kHalves; ++k)
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) qx[k][p] = qn[k][p];
+    Step nxt = cur;
+    if (left > 1) {
+      nxt.hk += kSelWarps;
+      if (settle(nxt)) read_query(nxt);
+      else left = 1;
     }
-    cp_async_wait<kSelStages - 1>();
+    const int64_t row = (int64_t(cur.s) * v.Hkv + cur.hk) * v.G + g;
+    cp_async_wait<kStages - 1>();
     const uint4* kx = mine + stage * 4 * kPieces * 32;
-    float m[2] = {-INFINITY, -INFINITY}, x[4][4];
-    const int j0 = cur.chunk * kSelPages;
+    float x[kHalves][8];
+    const float bias = float(v.page_shift);  // log2 of a whole page's keys
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       float c0[4] = {}, c1[4] = {};
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
         const uint4 k = kx[(n * kPieces + p) * 32];
-        mma_16816(c0, qa[p].x, qb[p].x, qa[p].y, qb[p].y, k.x, k.y);
-        mma_16816(c1, qa[p].z, qb[p].z, qa[p].w, qb[p].w, k.z, k.w);
+        const uint4 q0 = qx[0][p], q1 = kWide ? qx[kHalves - 1][p] : make_uint4(0u, 0u, 0u, 0u);
+        mma_16816(c0, q0.x, q1.x, q0.y, q1.y, k.x, k.y);
+        mma_16816(c1, q0.z, q1.z, q0.w, q1.w, k.z, k.w);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = j0 + n * 8 + t * 2 + (e & 1);
-        // log2 of the number of keys: whole pages take the exact integer
-        const int keys = cur.len - (j << v.page_shift);
-        const float bias = keys >= v.page ? float(v.page_shift) : log2f(float(max(keys, 1)));
-        x[n][e] = j < cur.pages ? fmaf(c0[e] + c1[e], a.scale_log2, bias) : -INFINITY;
-        m[e >> 1] = fmaxf(m[e >> 1], x[n][e]);
-      }
+      for (int k = 0; k < kHalves; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) x[k][2 * n + e] = fmaf(c0[2 * k + e] + c1[2 * k + e], a.scale_log2, bias);
     }
-    const int64_t row = (int64_t(cur.s) * v.Hkv + cur.hk) * v.G;
+    const int rest = cur.pages - cur.chunk * kSelPages;  // pages of this chunk and behind
+    if (rest <= kSelPages) {  // the last page may have fewer keys, behind it there is none
+      const float last_bias = log2f(float(cur.len - ((cur.pages - 1) << v.page_shift))) - bias;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (k * 8 >= v.G) break;
-      m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 1));
-      m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 2));
-      const float ref = m[k] == -INFINITY ? 0.f : m[k];
+      for (int k = 0; k < kHalves; ++k)
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const int j = (n >> 1) * 8 + t * 2 + (n & 1);
+          if (j == rest - 1) x[k][n] += last_bias;
+          if (j >= rest) x[k][n] = -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kHalves; ++k) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) m = fmaxf(m, x[k][n]);
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const float ref = m == -INFINITY ? 0.f : m;
       float l = 0.f;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) l += ex2_approx(x[n][2 * k] - ref) + ex2_approx(x[n][2 * k + 1] - ref);
+      for (int n = 0; n < 8; ++n) l += ex2_approx(x[k][n] - ref);
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const int h = g + 8 * k;
-      if (h < v.G) {
-        if (t == 0) a.part[(row + h) * a.chunks + cur.chunk] = make_float2(m[k], l);
-        float* dst = a.scores + (row + h) * a.pitch + j0 + t * 2;
+      if (g + 8 * k < v.G) {
+        if (t == 0) a.part[(row + 8 * k) * a.chunks + cur.chunk] = make_float2(m, l);
+        float* dst = a.scores + (row + 8 * k) * a.pitch + cur.chunk * kSelPages + t * 2;
+        if (rest >= kSelPages) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-          if (j0 + n * 8 + t * 2 < a.pitch)  // the pitch is even, the pair lies inside
-            *reinterpret_cast<float2*>(dst + n * 8) = make_float2(x[n][2 * k], x[n][2 * k + 1]);
+          for (int n = 0; n < 4; ++n) *reinterpret_cast<float2*>(dst + n * 8) = make_float2(x[k][2 * n], x[k][2 * n + 1]);
+        } else {
+#pragma unroll
+          for (int n = 0; n < 4; ++n)  // up to the end of a group of 4: the pitch is a multiple of it
+            if (n * 8 + t * 2 < ((rest + 3) & ~3))
+              *reinterpret_cast<float2*>(dst + n * 8) = make_float2(x[k][2 * n], x[k][2 * n + 1]);
+        }
       }
     }
-    next(cur);
-    stage = stage == kSelStages - 1 ? 0 : stage + 1;
+    cur = nxt;
+    stage = stage == kStages - 1 ? 0 : stage + 1;
   }
   cp_async_wait<0>();
 }

@@ -315,8 +315,10 @@ ab_status run_paged_select(const ab_paged_params* p, const PagedView& v, const v
   a.pitch = (p->max_pages + 3) / 4 * 4;
   const int64_t most = (int64_t(p->S) * p->Hkv * a.chunks + kSelWarps - 1) / kSelWarps;
   const unsigned grid = unsigned(most < sms ? most : sms);
-  auto score = p->d == 128 ? page_score_kernel<128> : page_score_kernel<64>;
-  const int smem = kSelWarps * kSelStages * 32 * p->d * 2;
+  const bool wide = v.G > 8;
+  auto score = p->d == 128 ? (wide ? page_score_kernel<128, true> : page_score_kernel<128, false>)
+                           : (wide ? page_score_kernel<64, true> : page_score_kernel<64, false>);
+  const int smem = kSelWarps * sel_stages(p->d) * 32 * p->d * 2;
   if (set_smem(score, smem) != cudaSuccess) return AB_ERR_CUDA;
   score<<<grid, kSelWarps * 32, smem, st>>>(a);
   if (launch_status() != AB_OK) return AB_ERR_CUDA;

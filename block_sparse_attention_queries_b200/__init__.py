@@ -143,19 +143,24 @@ class NormRope:
         self.norm, self.interleaved, self.eps = norm, bool(interleaved), float(eps)
         self.wq, self.wk, self.cos, self.sin = wq, wk, cos, sin
         self.device = tensors[0].device if tensors else None
+        self._index = tensors[0].get_device() if tensors else None
+        self._fits = None
         self.n_pos = 0 if cos is None else cos.shape[0]
         self._c = ab_norm_rope(NORMS[norm], int(self.interleaved), self.eps, self.n_pos,
                                *(0 if t is None else t.data_ptr() for t in (wq, wk, cos, sin)))
 
-    def check(self, Hq: int, Hk: int, d: int, device):
-        """The weights and tables belong to Hq query and Hk key heads of d on `device`."""
+    def check(self, Hq: int, Hk: int, d: int, index: int):
+        """The weights and tables belong to Hq query and Hk key heads of d on CUDA device `index`."""
+        if self._fits == (Hq, Hk, d, index):
+            return
         for t, H in ((self.wq, Hq), (self.wk, Hk)):
             if t is not None and tuple(t.shape) != ((H, d) if self.norm == "token" else (d,)):
                 raise ValueError(f"norm weights {tuple(t.shape)} do not fit {H} heads of {d}")
         if self.cos is not None and self.cos.shape[1] != d // 2:
             raise ValueError(f"cos and sin have {self.cos.shape[1]} columns, {d // 2} expected")
-        if self.device is not None and self.device != device:
-            raise ValueError(f"weights and tables are on {self.device}, the tokens on {device}")
+        if self._index is not None and self._index != index:
+            raise ValueError(f"weights and tables are on {self.device}, the tokens on cuda:{index}")
+        self._fits = (Hq, Hk, d, index)
 
 
 @dataclass(frozen=True)
@@ -486,42 +491,48 @@ def ab_forward_host(p: Params, Qh, Kh, Vh, Oh, Qd, Kd, Vd, bufs: Buffers, device
 
 
 # ------------------------------------------- norm and rotation, paged cache
-def _check_tensor(t, dtype, shape, device, name):
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name}: expected contiguous {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)}"
+def _check_tensor(t, dtype, shape, index, name):
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {list(shape)} on cuda:{index}, got {t.dtype} {list(t.shape)}"
                          f"{'' if t.is_contiguous() else ' (strided)'} on {t.device}")
 
 
-def _call(fn_name, device, *args):
-    """The library's function on `device` and its current stream."""
+_fns = {}
+
+
+def _call(fn_name, index, *args):
+    """The library's function on CUDA device `index` and its current stream."""
     import torch
-    fn = getattr(lib(), fn_name)
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    fn = _fns.get(fn_name)
+    if fn is None:
+        fn = _fns[fn_name] = getattr(lib(), fn_name)
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != AB_OK:
         raise AbError(status, fn_name)
 
 
-def _cuda_device(t):
-    if not t.is_cuda:
+def _cuda_index(t):
+    index = t.get_device()
+    if index < 0:
         raise ValueError("expected a CUDA tensor")
-    return t.device
+    return index
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _tokens(t, shape, device, name):
+def _tokens(t, shape, index, name):
     """The strided tokens [(B,) T, H, d] as the library takes them."""
     import torch
-    if t.dtype != torch.bfloat16 or t.shape != shape or t.device != device or t.stride(-1) != 1:
-        raise ValueError(f"{name}: expected bf16 {list(shape)} with contiguous heads on {device}, got {t.dtype} "
-                         f"{list(t.shape)}, strides {t.stride()}, on {t.device}")
     st = t.stride()
+    if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape or st[-1] != 1:
+        raise ValueError(f"{name}: expected bf16 {list(shape)} with contiguous heads on cuda:{index}, got {t.dtype} "
+                         f"{list(t.shape)}, strides {st}, on {t.device}")
     return ab_tokens(t.data_ptr(), st[0] if len(shape) == 4 else 0, st[-3], st[-2])
 
 
@@ -531,7 +542,7 @@ def _dense_tokens(p: Params, nr: NormRope, q, k, v, pos_q, pos_k):
     given = [t for t in (q, k, v) if t is not None]
     if not given:
         raise ValueError("none of q, k, v is given")
-    dev = _cuda_device(given[0])
+    dev = _cuda_index(given[0])
     nr.check(p.H, p.H, p.d, dev)
     tok = [None if t is None else _tokens(t, (p.B, n, p.H, p.d), dev, name)
            for t, n, name in ((q, p.L, "q"), (k, p.Lk, "k"), (v, p.Lk, "v"))]
@@ -570,7 +581,7 @@ def ab_forward_qkv(p: Params, nr: NormRope, q, k, v, pos_q=None, pos_k=None, buf
     dev, tok = _dense_tokens(p, nr, q, k, v, pos_q, pos_k)
     if None in tok:
         raise ValueError("q, k and v are all needed")
-    b = Buffers(p, dev) if bufs is None else bufs
+    b = Buffers(p, q.device) if bufs is None else bufs
     for name, n in (("Q", p.L), ("K", p.Lk), ("V", p.Lk)):
         if getattr(b, name, None) is None:
             setattr(b, name, torch.empty(p.B, p.H, n, p.d, dtype=torch.bfloat16, device=dev))
@@ -625,7 +636,7 @@ def ab_paged_plan(pp: PagedParams, n_new, lens, table, free_pages, free_count, T
     slots).  `out` = (cu_new, slots, positions) writes into caller-owned
     tensors."""
     import torch
-    dev = _cuda_device(n_new)
+    dev = _cuda_index(n_new)
     i32 = torch.int32
     if out is None:
         if T is None:
@@ -649,7 +660,7 @@ def ab_paged_plan(pp: PagedParams, n_new, lens, table, free_pages, free_count, T
 def _paged_tokens(pp: PagedParams, nr: NormRope, q, k, v, slots, positions, K, V, ksum, Q):
     """Checked arguments of the calls that write tokens into the cache."""
     import torch
-    dev = _cuda_device(q)
+    dev = _cuda_index(q)
     T = q.shape[0]
     nr.check(pp.Hq, pp.Hkv, pp.d, dev)
     tok = (_tokens(q, (T, pp.Hq, pp.d), dev, "q"), _tokens(k, (T, pp.Hkv, pp.d), dev, "k"),
@@ -681,7 +692,7 @@ def ab_paged_append(pp: PagedParams, nr: NormRope, q, k, v, slots, positions, K,
 
 def _paged_rows(pp: PagedParams, Q, table, lens, cu_new):
     import torch
-    dev = _cuda_device(Q)
+    dev = _cuda_index(Q)
     T = Q.shape[0]
     if cu_new is None and T != pp.S:
         raise ValueError(f"Q has {T} rows, {pp.S} expected without cu_new")
@@ -721,7 +732,7 @@ def ab_paged_topk(pp: PagedParams, P, lens, out=None):
     """The pages to attend to: (idx [S, Hkv, max_pages], count [S, Hkv]) int32,
     the newest `recent` pages and those of largest P, keep_ratio of them in all."""
     import torch
-    dev = _cuda_device(P)
+    dev = _cuda_index(P)
     shape = (pp.S, pp.Hkv, pp.max_pages)
     _check_tensor(P, torch.float32, shape, dev, "P")
     _check_tensor(lens, torch.int32, (pp.S,), dev, "lens")
@@ -777,7 +788,7 @@ def ab_paged_forward(pp: PagedParams, nr: NormRope, q, k, v, cache: PagedCache, 
     each sequence's newest token."""
     import torch
     T = q.shape[0]
-    b = PagedBuffers(pp, T, _cuda_device(q)) if bufs is None else bufs
+    b = PagedBuffers(pp, T, torch.device("cuda", _cuda_index(q))) if bufs is None else bufs
     c = cache
     dev, T, tok, Q = _paged_tokens(pp, nr, q, k, v, slots, positions, c.K, c.V, c.ksum, b.Q)
     _paged_rows(pp, Q, c.table, c.lens, cu_new)

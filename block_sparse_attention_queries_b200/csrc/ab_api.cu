@@ -1,6 +1,7 @@
 // C ABI of the AB-Attention hot path (declared in include/ab.h): argument
 // checks, workspace layout, TMA descriptors and kernel launches.  The library
 // allocates no memory; every buffer belongs to the caller.
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <initializer_list>

@@ -19,7 +19,9 @@
 // that the CTAs walk together, so that the cheap ones (v is only moved) even
 // out: token by token where a warp takes a unit (a fused projection is then
 // read front to back), tensor by tensor where a CTA does and keeps a tensor's
-// weights in registers.  The factor r of a token's norm goes into its cos and sin once.
+// weights in registers.  Runs of 8 tokens are taken at about the same time, so
+// that a head's output, rows of 128 or 256 bytes that lie a sequence apart, is
+// written in longer pieces.  The factor r of a token's norm goes into its cos and sin once.
 #pragma once
 
 #include "ab_ptx.cuh"
@@ -48,8 +50,9 @@ struct NormRopeArgs {
   int tokens[3];           // tokens in all
   int units[3];            // end of each one's units in the list; if merged, of each one's units within a token
   int groups[3];           // units of a token
-  bool merged;             // token by token (all three have the same tokens)
-  int n_units;
+  bool merged;             // token by token (all three have the same tokens, tokens_all)
+  int tokens_all, n_units;
+  int run_shift;           // log2 of the tokens of a run
   // paged destination
   const int32_t* slots;    // [T], null: the dense destination
   int page_shift, num_pages;
@@ -100,7 +103,10 @@ __global__ void __launch_bounds__(NORM == kNormToken ? 640 : kRopeThreads)
   int4* const places = reinterpret_cast<int4*>(rope_smem + STAGES * (NV + 1) * threads) + warp;
 
   const int n_units = a.n_units;
-  const int step = kTeam ? int(gridDim.x) : int(gridDim.x) * warps;
+  // a CTA that takes whole tokens takes runs of them
+  const int run_mask = kTeam ? (1 << a.run_shift) - 1 : 0;
+  const int step = kTeam ? int(gridDim.x) << a.run_shift : int(gridDim.x) * warps;
+  auto next_unit = [&](int n) { return (n & run_mask) != run_mask ? n + 1 : n + step - run_mask; };
   // What a unit is, worked out once, ahead of its copies: x position, y slot,
   // z token, w side | group << 2 | batch element << 12 (B H <= 2^20).
   auto read_place = [&](int n) {
@@ -108,9 +114,12 @@ __global__ void __launch_bounds__(NORM == kNormToken ? 640 : kRopeThreads)
     if (n < n_units) {
       int side, group;
       if (!kTeam && a.merged) {
-        p.z = int(uint32_t(n) / uint32_t(a.units[2]));
-        const int local = n - p.z * a.units[2];
-        side = local < a.units[0] ? 0 : local < a.units[1] ? 1 : 2;
+        // runs of tokens, the units of a token, all runs
+        const int per_run = a.units[2] << a.run_shift;
+        const int run = int(uint32_t(n) / uint32_t(per_run));
+        const int local = (n - run * per_run) >> a.run_shift;
+        p.z = (run << a.run_shift) + (n & ((1 << a.run_shift) - 1));
+        side = p.z >= a.tokens_all ? 3 : local < a.units[0] ? 0 : local < a.units[1] ? 1 : 2;
         group = local - (side == 0 ? 0 : a.units[side - 1]);
       } else {
         side = n < a.units[0] ? 0 : n < a.units[1] ? 1 : 2;
@@ -122,8 +131,10 @@ __global__ void __launch_bounds__(NORM == kNormToken ? 640 : kRopeThreads)
           group = local - p.z * a.groups[side];
         }
       }
+      p.w = side;
+      if (side == 3) return p;  // behind the last token of a run
       const int b = a.len[side] == a.tokens[side] ? 0 : int(uint32_t(p.z) / uint32_t(a.len[side]));
-      p.w = side | group << 2 | b << 12;
+      p.w |= group << 2 | b << 12;
       if (side < 2 && a.cos_t) p.x = a.pos[side] ? __ldg(a.pos[side] + p.z) : p.z - b * a.len[side];
       if (a.slots) p.y = __ldg(a.slots + p.z);
     }
@@ -134,7 +145,9 @@ __global__ void __launch_bounds__(NORM == kNormToken ? 640 : kRopeThreads)
   const int hstep = kTeam ? warps * kRows : kRows;
 
   auto issue = [&](int n, int4 p, int stage) {
-    if (n < n_units) {
+    if (n < n_units && (p.w & 3) == 3) {
+      if (lane == 0) places[stage * warps] = p;
+    } else if (n < n_units) {
       const int side = p.w & 3, b = int(uint32_t(p.w) >> 12);
       const TokenView& x = a.in[side];
       const int H = a.heads[side];
@@ -158,13 +171,13 @@ __global__ void __launch_bounds__(NORM == kNormToken ? 640 : kRopeThreads)
     cp_async_commit();
   };
 
-  int n = kTeam ? int(blockIdx.x) : int(blockIdx.x) * warps + warp;
+  int n = kTeam ? int(blockIdx.x) << a.run_shift : int(blockIdx.x) * warps + warp;
   int ahead = n;
   int4 place = read_place(ahead);
 #pragma unroll
   for (int k = 0; k < STAGES - 1; ++k) {
     issue(ahead, place, k);
-    ahead += step;
+    ahead = next_unit(ahead);
     place = read_place(ahead);
   }
 
@@ -181,16 +194,21 @@ __global__ void __launch_bounds__(NORM == kNormToken ? 640 : kRopeThreads)
   constexpr int kW = kTeam ? NV : 1;
   float wv[kW][8];  // weights of this lane, for all units of a side
   int side = -1;
-  for (int stage = 0, flip = 0; n < n_units; n += step) {
+  for (int stage = 0, flip = 0; n < n_units; n = next_unit(n)) {
     __syncwarp();  // the warp is done with the stage that is filled next
     issue(ahead, place, stage == 0 ? STAGES - 1 : stage - 1);
-    ahead += step;
+    ahead = next_unit(ahead);
     place = read_place(ahead);
     cp_async_wait<STAGES - 1>();
     __syncwarp();
     const uint4* in = pieces + stage * NV * threads;
     const int4 here = places[stage * warps];
-    const int cur = here.w & 3, H = a.heads[cur];
+    const int cur = here.w & 3;
+    if (cur == 3) {
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
+      continue;
+    }
+    const int H = a.heads[cur];
     if (NORM != kNormNone && cur != side && cur < 2) {
       const float* w = a.w[cur];
 #pragma unroll

@@ -11,11 +11,14 @@ int log2_of(int x) {
   return k;
 }
 
+// SMs of the current device (0: unknown), read from the driver once per device.
 int sm_count() {
+  static std::atomic<int> known[kMaxDevices];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-    return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (dev < kMaxDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 0;
+  if (dev < kMaxDevices) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -41,7 +44,7 @@ ab_status launch_after(void (*kern)(Params...), dim3 grid, int threads, int smem
 }
 
 // ------------------------------------------------------ norm and rotation
-constexpr int64_t kRopeMaxUnits = int64_t(1) << 30;  // positions in the list of units stay in 32 bits
+constexpr int64_t kRopeMaxUnits = int64_t(1) << 29;  // positions in the list of units stay in 32 bits
 
 ab_status check_norm_rope(const ab_norm_rope* nr) {
   if (!nr) return AB_ERR_INVALID_ARG;
@@ -99,9 +102,15 @@ ab_status launch_norm_rope(NormRopeArgs a, int d, const ab_norm_rope* nr, cudaSt
     if (tokens && a.tokens[k] != tokens) a.merged = false;
     tokens = a.tokens[k];
   }
-  if (a.merged)
-    for (int k = 0; k < 3; ++k) a.units[k] = units += a.tokens[k] ? a.groups[k] : 0;
+  a.run_shift = all >= 16 * int64_t(sms) * per_sm ? 3 : 0;
   a.n_units = int(all);
+  if (a.merged) {
+    for (int k = 0; k < 3; ++k) a.units[k] = units += a.tokens[k] ? a.groups[k] : 0;
+    a.tokens_all = tokens;
+    const int run = 1 << a.run_shift;
+    a.n_units = (tokens + run - 1) / run * run * units;
+    all = a.n_units;
+  }
   const int per_cta = team ? 1 : threads / 32;
   const int64_t most = (all + per_cta - 1) / per_cta;
   const int64_t blocks = most < int64_t(sms) * per_sm ? most : int64_t(sms) * per_sm;

@@ -15,19 +15,6 @@
 
 namespace ab {
 
-// A kernel that follows one of this library's in the same call is launched
-// while that one still runs, and waits here for its end and its results;
-// pdl_trigger lets the next one be launched.
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// Untiled copy into shared memory: 16-byte aligned, a multiple of 16 bytes.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
 constexpr int kMaxSeqs = 8192;   // sequences of a block table: their prefix sums fit in shared memory
 constexpr int kMaxGroup = 16;    // query heads per key/value head
 
@@ -277,14 +264,18 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 // Mean of a page's keys, for every page that a slot list touches: the last
 // slot of each run of slots in one page owns the page, and the mean is over
 // the page's keys up to that slot.  A warp takes one (page, head), a run of at
-// most 16 KB.  Bound by memory (the page's keys are read once).
+// most 16 KB, eight heads a CTA.  Bound by memory (the page's keys are read
+// once) or, for single tokens, by latency.
 template <int D>
 __global__ void __launch_bounds__(256)
     page_sum_kernel(const int32_t* slots, int T, int per_cta, const __nv_bfloat16* K, __nv_bfloat16* ksum, int Hkv,
                     int page_shift, int num_pages) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = blockIdx.y * 8 + warp;
   const int t0 = blockIdx.x * per_cta;
+  pdl_wait();
+  pdl_trigger();
+  if (head >= Hkv) return;
   int slot = -1;
   if (lane < per_cta && t0 + lane < T) {
     slot = __ldg(slots + t0 + lane);
@@ -293,41 +284,39 @@ __global__ void __launch_bounds__(256)
   }
   uint32_t owners = __ballot_sync(0xffffffffu, slot >= 0);
   const int sub = lane % kLanes, row0 = lane / kLanes;
-  for (int item = warp; owners; owners &= owners - 1, item -= Hkv) {
+  for (; owners; owners &= owners - 1) {
     const int sl = __shfl_sync(0xffffffffu, slot, __ffs(owners) - 1);
     const int64_t id = sl >> page_shift;
     const int n = (sl & ((1 << page_shift) - 1)) + 1;
-    for (; item < Hkv; item += 8) {
-      const __nv_bfloat16* src = K + (((id * Hkv + item) << page_shift) * D) + sub * 8;
-      float acc[8] = {};
-      for (int r0 = 0; r0 < n; r0 += 8 * kRows) {
-        uint4 x[8];
+    const __nv_bfloat16* src = K + (((id * Hkv + head) << page_shift) * D) + sub * 8;
+    float acc[8] = {};
+    for (int r0 = 0; r0 < n; r0 += 8 * kRows) {
+      uint4 x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = r0 + k * kRows + row0;
-          x[k] = r < n ? *reinterpret_cast<const uint4*>(src + int64_t(r) * D) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[2 * e] += __uint_as_float(u[e] << 16);
-            acc[2 * e + 1] += __uint_as_float(u[e] & 0xFFFF0000u);
-          }
-        }
+      for (int k = 0; k < 8; ++k) {
+        const int r = r0 + k * kRows + row0;
+        x[k] = r < n ? *reinterpret_cast<const uint4*>(src + int64_t(r) * D) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
-        for (int o = kLanes; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
-        acc[e] /= float(n);
+        for (int e = 0; e < 4; ++e) {
+          acc[2 * e] += __uint_as_float(u[e] << 16);
+          acc[2 * e + 1] += __uint_as_float(u[e] & 0xFFFF0000u);
+        }
       }
-      if (row0 == 0)
-        *reinterpret_cast<uint4*>(ksum + (id * Hkv + item) * D + sub * 8) =
-            make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
-                       pack_bf16x2(acc[6], acc[7]));
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+      for (int o = kLanes; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
+      acc[e] /= float(n);
+    }
+    if (row0 == 0)
+      *reinterpret_cast<uint4*>(ksum + (id * Hkv + head) * D + sub * 8) =
+          make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+                     pack_bf16x2(acc[6], acc[7]));
   }
 }
 

@@ -77,63 +77,75 @@ int rope_max_heads(int d) { return 16 * (256 / d) * kRopeRowsMany; }
 ab_status launch_norm_rope(NormRopeArgs a, int d, const ab_norm_rope* nr, cudaStream_t st) {
   const int sms = sm_count();
   if (!sms) return AB_ERR_CUDA;
-  int heads = 0;
-  for (int k = 0; k < 3; ++k)
-    if (a.tokens[k]) heads = a.heads[k] > heads ? a.heads[k] : heads;
-  const int rows = 256 / d;  // head rows a warp covers at once
-  const bool team = nr->norm == kNormToken, many = team && heads > 16 * rows * kRopeRows;
-  const int nv = many ? kRopeRowsMany : kRopeRows, stages = many ? kRopeStagesMany : kRopeStages;
-  const int per_warp = rows * nv;
-  const int threads = team ? 32 * ((heads + per_warp - 1) / per_warp) : kRopeThreads;
-  const int smem = rope_smem_bytes(nv, stages, threads);
-  // resident CTAs: as many as shared memory and the registers (96 or 80 a thread) allow
-  int per_sm = (team ? 640 : 768) / threads;
-  if (per_sm > 220 * 1024 / smem) per_sm = 220 * 1024 / smem;
-  if (per_sm < 1) per_sm = 1;
+  int heads = 0, tokens = 0;
   int64_t all = 0;
-  int tokens = 0, units = 0;
-  a.merged = !team;
+  a.merged = true;
   for (int k = 0; k < 3; ++k) {
-    a.groups[k] = team ? 1 : (a.heads[k] + per_warp - 1) / per_warp;
-    all += int64_t(a.tokens[k]) * a.groups[k];
-    if (all > kRopeMaxUnits) return AB_ERR_UNSUPPORTED;
-    a.units[k] = int(all);
     if (!a.tokens[k]) continue;
+    heads = a.heads[k] > heads ? a.heads[k] : heads;
     if (tokens && a.tokens[k] != tokens) a.merged = false;
     tokens = a.tokens[k];
+    all += a.tokens[k];
   }
-  a.run_shift = all >= 16 * int64_t(sms) * per_sm ? 3 : 0;
-  a.n_units = int(all);
-  if (a.merged) {
-    for (int k = 0; k < 3; ++k) a.units[k] = units += a.tokens[k] ? a.groups[k] : 0;
-    a.tokens_all = tokens;
-    const int run = 1 << a.run_shift;
-    a.n_units = (tokens + run - 1) / run * run * units;
-    all = a.n_units;
-  }
-  const int per_cta = team ? 1 : threads / 32;
-  const int64_t most = (all + per_cta - 1) / per_cta;
-  const int64_t blocks = most < int64_t(sms) * per_sm ? most : int64_t(sms) * per_sm;
-  auto go = [&](auto kern) -> ab_status {
+  if (all > kRopeMaxUnits) return AB_ERR_UNSUPPORTED;
+  const int rows = 256 / d;  // head rows a warp covers at once
+  auto go = [&](auto kern, int64_t blocks, int threads, int smem) -> ab_status {
     if (smem > 48 * 1024 && set_smem(kern, smem) != cudaSuccess) return AB_ERR_CUDA;
     kern<<<unsigned(blocks), unsigned(threads), smem, st>>>(a);
     return launch_status();
   };
-  auto by_norm = [&](auto dd, auto il) -> ab_status {
-    constexpr int D = decltype(dd)::value;
-    constexpr bool I = decltype(il)::value;
-    switch (nr->norm) {
-      case kNormNone: return go(norm_rope_kernel<D, kNormNone, I, kRopeRows, kRopeStages>);
-      case kNormHead: return go(norm_rope_kernel<D, kNormHead, I, kRopeRows, kRopeStages>);
-      default:
-        return many ? go(norm_rope_kernel<D, kNormToken, I, kRopeRowsMany, kRopeStagesMany>)
-                    : go(norm_rope_kernel<D, kNormToken, I, kRopeRows, kRopeStages>);
-    }
-  };
   using T128 = std::integral_constant<int, 128>;
   using T64 = std::integral_constant<int, 64>;
-  if (d == 128) return nr->interleaved ? by_norm(T128{}, std::true_type{}) : by_norm(T128{}, std::false_type{});
-  return nr->interleaved ? by_norm(T64{}, std::true_type{}) : by_norm(T64{}, std::false_type{});
+  auto by_type = [&](auto f) -> ab_status {
+    if (d == 128) return nr->interleaved ? f(T128{}, std::true_type{}) : f(T128{}, std::false_type{});
+    return nr->interleaved ? f(T64{}, std::true_type{}) : f(T64{}, std::false_type{});
+  };
+  if (nr->norm == kNormToken) {
+    a.merged = false;
+    const bool many = heads > 16 * rows * kRopeRows;
+    const int nv = many ? kRopeRowsMany : kRopeRows, stages = many ? kRopeStagesMany : kRopeStages;
+    const int threads = 32 * ((heads + rows * nv - 1) / (rows * nv));
+    const int smem = rope_smem_bytes(nv, stages, threads);
+    // resident CTAs: as many as shared memory and the registers (96 a thread) allow
+    int per_sm = 640 / threads;
+    if (per_sm > 220 * 1024 / smem) per_sm = 220 * 1024 / smem;
+    if (per_sm < 1) per_sm = 1;
+    int units = 0;
+    for (int k = 0; k < 3; ++k) a.units[k] = units += a.tokens[k];
+    a.n_units = units;
+    const int64_t blocks = units < int64_t(sms) * per_sm ? units : int64_t(sms) * per_sm;
+    return by_type([&](auto dd, auto il) -> ab_status {
+      constexpr int D = decltype(dd)::value;
+      constexpr bool I = decltype(il)::value;
+      return many ? go(token_norm_rope_kernel<D, I, kRopeRowsMany, kRopeStagesMany>, blocks, threads, smem)
+                  : go(token_norm_rope_kernel<D, I, kRopeRows, kRopeStages>, blocks, threads, smem);
+    });
+  }
+  constexpr int threads = kRopeThreads, warps = threads / 32;
+  constexpr int smem = rope_smem_bytes(kRopeRows, kRopeStages, threads);
+  const int64_t resident = int64_t(sms) * 5;  // CTAs: 41 KB, 96 registers a thread
+  // a unit takes all heads of its token where that leaves every warp four units, else one step of them
+  const bool whole = all >= 4 * resident * warps;
+  int64_t units = 0;
+  for (int k = 0; k < 3; ++k) {
+    const int steps = (a.heads[k] + rows * kRopeRows - 1) / (rows * kRopeRows);
+    a.steps[k] = whole ? steps : 1;
+    const int groups = a.tokens[k] ? (whole ? 1 : steps) : 0;
+    units += a.merged ? groups : int64_t(a.tokens[k]) * groups;
+    if (units > kRopeMaxUnits) return AB_ERR_UNSUPPORTED;
+    a.units[k] = int(units);
+  }
+  if (a.merged) units *= tokens;
+  if (units > kRopeMaxUnits) return AB_ERR_UNSUPPORTED;
+  a.n_units = int(units);
+  int64_t blocks = (units + warps - 1) / warps;
+  blocks = blocks < resident ? blocks : resident;
+  return by_type([&](auto dd, auto il) -> ab_status {
+    constexpr int D = decltype(dd)::value;
+    constexpr bool I = decltype(il)::value;
+    return nr->norm == kNormHead ? go(norm_rope_kernel<D, true, I>, blocks, threads, smem)
+                                 : go(norm_rope_kernel<D, false, I>, blocks, threads, smem);
+  });
 }
 
 // Bytes [first, last) that tokens reach over.
@@ -297,14 +309,11 @@ ab_status run_append(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T
   // a CTA looks at 1 to 32 slots: few where there are few, so that pages spread over the SMs
   int per_cta = (T + 1183) / 1184;
   per_cta = per_cta > 32 ? 32 : per_cta;
-  const unsigned grid = unsigned((T + per_cta - 1) / per_cta);
+  const dim3 grid(unsigned((T + per_cta - 1) / per_cta), unsigned((p->Hkv + 7) / 8));
   const auto* kc = static_cast<const __nv_bfloat16*>(Kc);
   auto* ks = static_cast<__nv_bfloat16*>(ksum);
-  if (p->d == 128)
-    page_sum_kernel<128><<<grid, 256, 0, st>>>(a.slots, T, per_cta, kc, ks, p->Hkv, a.page_shift, a.num_pages);
-  else
-    page_sum_kernel<64><<<grid, 256, 0, st>>>(a.slots, T, per_cta, kc, ks, p->Hkv, a.page_shift, a.num_pages);
-  return launch_status();
+  return launch_after(p->d == 128 ? page_sum_kernel<128> : page_sum_kernel<64>, grid, 256, 0, st, a.slots, T, per_cta, kc,
+                      ks, p->Hkv, a.page_shift, a.num_pages);
 }
 
 ab_status run_paged_select(const ab_paged_params* p, const PagedView& v, const void* Q, const void* ksum, float* P,

@@ -58,9 +58,9 @@ struct NormRopeArgs {
   int page_shift, num_pages;
 };
 
-// A kernel that follows one of this library's in the same call is launched
-// while that one still runs, and waits here for its end and its results;
-// pdl_trigger lets the next one be launched.
+// The kernels of the paged path are launched while the kernel before them in
+// the stream still runs, and wait here for its end and its results; pdl_trigger
+// lets the next one be launched.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_kernel(const __grid
   uint4* const pieces = rope_smem + threadIdx.x;
   uint4* const tables = rope_smem + STAGES * NV * kRopeThreads + warp * 32;
   int4* const places = reinterpret_cast<int4*>(rope_smem + STAGES * (NV + 1) * kRopeThreads) + warp;
+  pdl_wait();
   pdl_trigger();
   const int n_units = a.n_units, step = int(gridDim.x) * kWarps;
 
@@ -375,6 +376,7 @@ __global__ void __launch_bounds__(640) token_norm_rope_kernel(const __grid_const
   uint4* const pieces = rope_smem + threadIdx.x;
   uint4* const tables = rope_smem + STAGES * NV * threads + warp * 32;
   int4* const places = reinterpret_cast<int4*>(rope_smem + STAGES * (NV + 1) * threads) + warp;
+  pdl_wait();
   pdl_trigger();
   if (threadIdx.x < 32) part[threadIdx.x >> 4][threadIdx.x & 15] = 0.f;
   __syncthreads();

@@ -71,11 +71,20 @@ struct PlanArgs {
   int32_t *cu_new, *slots, *positions;
 };
 
+// Counts that stop at 2^31 - 1 (more than any list or slot map holds).
 struct PlanScan {
-  int64_t rel, need, want;
+  uint32_t rel, need, want;
 };
 __device__ __forceinline__ PlanScan operator+(const PlanScan& a, const PlanScan& b) {
-  return {a.rel + b.rel, a.need + b.need, a.want + b.want};
+  constexpr uint32_t kMost = 0x7FFFFFFFu;
+  return {min(a.rel + b.rel, kMost), min(a.need + b.need, kMost), min(a.want + b.want, kMost)};
+}
+__device__ __forceinline__ PlanScan shfl_up(const PlanScan& a, int o) {
+  return {__shfl_up_sync(0xffffffffu, a.rel, o), __shfl_up_sync(0xffffffffu, a.need, o),
+          __shfl_up_sync(0xffffffffu, a.want, o)};
+}
+__device__ __forceinline__ PlanScan shfl_at(const PlanScan& a, int l) {
+  return {__shfl_sync(0xffffffffu, a.rel, l), __shfl_sync(0xffffffffu, a.need, l), __shfl_sync(0xffffffffu, a.want, l)};
 }
 
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
@@ -87,6 +96,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   int32_t* old_len = cu_rel + a.S + 1;          // [S]
   __shared__ PlanScan warp_sum[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
 
   int F0 = *a.free_count;
   if (F0 < 0 || F0 > a.num_pages) {
@@ -109,13 +120,13 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     old_len[s] = len;
     const int old = (len + a.page - 1) >> a.page_shift;
     if (!bad && n == -1) {
-      v.rel = old;
+      v.rel = uint32_t(old);
     } else if (!bad && n > 0) {
       if (n > cap - len) {
         bad = true;  // longer than its row of the table: not served
       } else {
-        v.need = ((len + n + a.page - 1) >> a.page_shift) - old;
-        v.want = n;
+        v.need = uint32_t(((len + n + a.page - 1) >> a.page_shift) - old);
+        v.want = uint32_t(n);
       }
     }
     if (bad) raise_error(AB_ERR_CAPACITY);
@@ -124,31 +135,26 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   auto block_scan = [&](PlanScan v, PlanScan& total) -> PlanScan {  // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const PlanScan y{__shfl_up_sync(0xffffffffu, v.rel, o), __shfl_up_sync(0xffffffffu, v.need, o),
-                       __shfl_up_sync(0xffffffffu, v.want, o)};
+      const PlanScan y = shfl_up(v, o);
       if (lane >= o) v = v + y;
     }
     __syncthreads();  // warp_sum is reused
     if (lane == 31) warp_sum[warp] = v;
     __syncthreads();
     PlanScan w = warp_sum[lane];
-    const PlanScan mine = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const PlanScan y{__shfl_up_sync(0xffffffffu, w.rel, o), __shfl_up_sync(0xffffffffu, w.need, o),
-                       __shfl_up_sync(0xffffffffu, w.want, o)};
+      const PlanScan y = shfl_up(w, o);
       if (lane >= o) w = w + y;
     }
-    total = {__shfl_sync(0xffffffffu, w.rel, 31), __shfl_sync(0xffffffffu, w.need, 31),
-             __shfl_sync(0xffffffffu, w.want, 31)};
-    const PlanScan before{w.rel - mine.rel, w.need - mine.need, w.want - mine.want};
-    return v + PlanScan{__shfl_sync(0xffffffffu, before.rel, warp), __shfl_sync(0xffffffffu, before.need, warp),
-                        __shfl_sync(0xffffffffu, before.want, warp)};
+    total = shfl_at(w, 31);
+    const PlanScan before = shfl_at(w, warp - 1 < 0 ? 0 : warp - 1);
+    return warp == 0 ? v : v + before;
   };
 
   // all pages given back (they can be handed out again in this step)
   PlanScan total{0, 0, 0}, t;
-  int64_t rel_all = 0;
+  int64_t rel_all = 0;  // at most 8 chunks of less than 2^31
   const bool one_chunk = a.S <= kPlanThreads;
   PlanScan v{0, 0, 0}, incl{0, 0, 0};
   for (int s0 = 0; s0 < a.S; s0 += kPlanThreads) {
@@ -172,15 +178,15 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const PlanScan c = total + incl;
     if (s < a.S) {
       // sums beyond the first that does not fit are mended below
-      cu_rel[s + 1] = int(c.rel < rel_all ? c.rel : rel_all);
-      cu_need[s + 1] = c.need <= F && c.want <= a.T ? int(c.need) : -1;
-      cu_want[s + 1] = int(c.want < a.T ? c.want : a.T);
+      cu_rel[s + 1] = min(int(c.rel), int(rel_all));
+      cu_need[s + 1] = int(c.need) <= F && int(c.want) <= a.T ? int(c.need) : -1;
+      cu_want[s + 1] = min(int(c.want), a.T);
     }
     total = total + t;
   }
   if (tid == 0) cu_want[0] = cu_need[0] = cu_rel[0] = 0;
   __syncthreads();
-  if (total.need > F || total.want > a.T) {
+  if (int(total.need) > F || int(total.want) > a.T) {
     // the served sequences are a prefix: find its end, repeat its sums behind it
     if (tid == 0) raise_error(AB_ERR_CAPACITY);
     int lo = 0, hi = a.S;  // cu_need[lo] >= 0, the answer is the last such index
@@ -219,23 +225,32 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     return at >= F0 ? given_back(at - F0) : a.free_pages[at];
   };
   const int64_t gtid = int64_t(blockIdx.x) * kPlanThreads + tid, gstep = int64_t(kPlanCtas) * kPlanThreads;
-  for (int64_t t64 = gtid; t64 < a.T; t64 += gstep) {
-    const int tk = int(t64);
-    int slot = -1, pos = 0;
-    if (tk < n_want) {
-      const int s = find(cu_want, tk);
-      const int len = old_len[s], old = (len + a.page - 1) >> a.page_shift;
-      pos = len + tk - cu_want[s];
-      const int j = pos >> a.page_shift;
-      const int id = j < old ? a.table[int64_t(s) * a.max_pages + j] : handed_out(cu_need[s] + j - old);
-      if (id >= 0 && id < a.num_pages) {
-        slot = (id << a.page_shift) + (pos & (a.page - 1));
-      } else {
-        raise_error(AB_ERR_CAPACITY);
+  constexpr int kBatch = 4;  // tokens a thread looks up at once
+  for (int64_t t0 = gtid; t0 < a.T; t0 += kBatch * gstep) {
+    int pos[kBatch], id[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t tk = t0 + k * gstep;
+      pos[k] = 0;
+      id[k] = -1;
+      if (tk < n_want) {
+        const int s = find(cu_want, int(tk));
+        const int len = old_len[s], old = (len + a.page - 1) >> a.page_shift;
+        pos[k] = len + int(tk) - cu_want[s];
+        const int j = pos[k] >> a.page_shift;
+        id[k] = j < old ? a.table[int64_t(s) * a.max_pages + j] : handed_out(cu_need[s] + j - old);
       }
     }
-    a.slots[tk] = slot;
-    a.positions[tk] = pos;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t tk = t0 + k * gstep;
+      if (tk >= a.T) break;
+      int slot = -1;
+      if (id[k] >= 0 && id[k] < a.num_pages) slot = (id[k] << a.page_shift) + (pos[k] & (a.page - 1));
+      else if (tk < n_want) raise_error(AB_ERR_CAPACITY);
+      a.slots[tk] = slot;
+      a.positions[tk] = pos[k];
+    }
   }
   // The table rows written here (served sequences, entries from their old
   // number of pages on) are never read above, the list entries written here

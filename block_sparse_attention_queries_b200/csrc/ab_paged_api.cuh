@@ -22,8 +22,8 @@ int sm_count() {
   return n;
 }
 
-// Launch of a kernel that begins with pdl_wait, behind another kernel of the
-// same call.
+// Launch of a kernel that begins with pdl_wait: it may be started while the
+// kernel before it in the stream still runs.
 template <typename... Params, typename... Args>
 ab_status launch_after(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t st, const Args&... args) {
   cudaLaunchConfig_t cfg{};
@@ -91,8 +91,7 @@ ab_status launch_norm_rope(NormRopeArgs a, int d, const ab_norm_rope* nr, cudaSt
   const int rows = 256 / d;  // head rows a warp covers at once
   auto go = [&](auto kern, int64_t blocks, int threads, int smem) -> ab_status {
     if (smem > 48 * 1024 && set_smem(kern, smem) != cudaSuccess) return AB_ERR_CUDA;
-    kern<<<unsigned(blocks), unsigned(threads), smem, st>>>(a);
-    return launch_status();
+    return launch_after(kern, dim3(unsigned(blocks)), threads, smem, st, a);
   };
   using T128 = std::integral_constant<int, 128>;
   using T64 = std::integral_constant<int, 64>;
@@ -338,8 +337,7 @@ ab_status run_paged_select(const ab_paged_params* p, const PagedView& v, const v
                            : (wide ? page_score_kernel<64, true> : page_score_kernel<64, false>);
   const int smem = kSelWarps * sel_stages(p->d) * 32 * p->d * 2;
   if (set_smem(score, smem) != cudaSuccess) return AB_ERR_CUDA;
-  score<<<grid, kSelWarps * 32, smem, st>>>(a);
-  if (launch_status() != AB_OK) return AB_ERR_CUDA;
+  if (launch_after(score, dim3(grid), kSelWarps * 32, smem, st, a) != AB_OK) return AB_ERR_CUDA;
   int steps = (p->max_pages + 4 * kNormThreads - 1) / (4 * kNormThreads);
   steps = steps > 8 ? 8 : steps;
   return launch_after(page_mass_kernel, dim3(unsigned(steps), unsigned(p->Hkv), unsigned(p->S)), kNormThreads, 0, st, a);
@@ -354,8 +352,7 @@ ab_status run_paged_topk(const ab_paged_params* p, const float* P, const int32_t
   a.cap = p->max_pages < kTopkMaxKeys ? p->max_pages : kTopkMaxKeys;
   const int smem = a.cap * 4;
   if (smem > 36 * 1024 && set_smem(page_topk_kernel, smem) != cudaSuccess) return AB_ERR_CUDA;
-  page_topk_kernel<<<unsigned(p->S * p->Hkv), kTopkThreads, smem, st>>>(a);
-  return launch_status();
+  return launch_after(page_topk_kernel, dim3(unsigned(p->S * p->Hkv)), kTopkThreads, smem, st, a);
 }
 
 template <int D, bool kLists>
@@ -363,8 +360,7 @@ ab_status launch_paged_attention(const DecArgs& a, int grid, cudaStream_t st) {
   auto kern = paged_attention_kernel<D, kLists>;
   constexpr int smem = DecSmem<D>::kAlloc;
   if (set_smem(kern, smem) != cudaSuccess) return AB_ERR_CUDA;
-  kern<<<unsigned(grid), kDecThreads, smem, st>>>(a);
-  if (launch_status() != AB_OK) return AB_ERR_CUDA;
+  if (launch_after(kern, dim3(unsigned(grid)), kDecThreads, smem, st, a) != AB_OK) return AB_ERR_CUDA;
   if (grid == 1) return AB_OK;
   return launch_after(paged_join_kernel<D>, dim3(unsigned(grid - 1), unsigned(a.v.G)), 32 * kJoinWarps, 0, st, a, grid,
                       a.v.G > 8 ? 16 : 8);
@@ -456,8 +452,7 @@ ab_status ab_paged_plan(const ab_paged_params* p, int32_t T, const int32_t* n_ne
   a.cu_new = cu_new; a.slots = slots; a.positions = positions;
   const int smem = (4 * p->S + 3) * 4;
   if (smem > 40 * 1024 && set_smem(plan_kernel, smem) != cudaSuccess) return AB_ERR_CUDA;
-  plan_kernel<<<kPlanCtas, kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
-  return launch_status();
+  return launch_after(plan_kernel, dim3(kPlanCtas), kPlanThreads, smem, static_cast<cudaStream_t>(stream), a);
 }
 
 ab_status ab_paged_append(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T, const ab_tokens* q,

@@ -526,6 +526,15 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _c(p: Params) -> ab_params:
+    """p.c(), made once (Params are immutable)."""
+    c = p.__dict__.get("_c")
+    if c is None:
+        c = p.c()
+        object.__setattr__(p, "_c", c)
+    return c
+
+
 def _tokens(t, shape, index, name):
     """The strided tokens [(B,) T, H, d] as the library takes them."""
     import torch
@@ -568,8 +577,10 @@ def ab_qk_norm_rope(p: Params, nr: NormRope, q, k=None, v=None, pos_q=None, pos_
     else:
         for t, s, name in zip(out, shapes, "QKV"):
             if s is not None:
+                if t is None:
+                    raise ValueError(f"out has no {name}")
                 _check_tensor(t, torch.bfloat16, s, dev, name)
-    _call("ab_qk_norm_rope", dev, p.c(), nr._c, *tok, _p(pos_q), _p(pos_k), *(_p(t) for t in out))
+    _call("ab_qk_norm_rope", dev, _c(p), nr._c, *tok, _p(pos_q), _p(pos_k), *(_p(t) for t in out))
     return tuple(t if s is not None else None for t, s in zip(out, shapes))
 
 
@@ -589,7 +600,7 @@ def ab_forward_qkv(p: Params, nr: NormRope, q, k, v, pos_q=None, pos_k=None, buf
     for name, shape in (("P", (p.B, p.H, p.Nq, p.Nkv)), ("idx", (p.B, p.H, p.Nq, p.Nkv)),
                         ("pi_q32", (p.B, p.H, p.Nq, p.Nkv)), ("count", (p.B, p.H, p.Nq)), ("O", (p.B, p.H, p.L, p.d))):
         _check_tensor(getattr(b, name), getattr(b, name).dtype, shape, dev, name)
-    _call("ab_forward_qkv", dev, p.c(), nr._c, *tok, _p(pos_q), _p(pos_k), _p(b.Q), _p(b.K), _p(b.V), _p(b.P),
+    _call("ab_forward_qkv", dev, _c(p), nr._c, *tok, _p(pos_q), _p(pos_k), _p(b.Q), _p(b.K), _p(b.V), _p(b.P),
           _p(b.idx), _p(b.pi_q32), _p(b.count), _p(b.O), _p(b.ws), b.ws.numel())
     return b
 
@@ -647,13 +658,23 @@ def ab_paged_plan(pp: PagedParams, n_new, lens, table, free_pages, free_count, T
         T = out[1].numel()
     lens_out = lens if lens_out is None else lens_out
     free_count_out = free_count if free_count_out is None else free_count_out
-    for t, shape, name in ((n_new, (pp.S,), "n_new"), (lens, (pp.S,), "lens"), (lens_out, (pp.S,), "lens_out"),
-                           (table, (pp.S, pp.max_pages), "table"), (free_pages, (pp.num_pages,), "free_pages"),
-                           (free_count, (1,), "free_count"), (free_count_out, (1,), "free_count_out"),
-                           (out[0], (pp.S + 1,), "cu_new"), (out[1], (T,), "slots"), (out[2], (T,), "positions")):
-        _check_tensor(t, i32, shape, dev, name)
-    _call("ab_paged_plan", dev, pp.c(), T, *(t.data_ptr() for t in (n_new, lens, lens_out, table, free_pages, free_count,
-                                                                  free_count_out, *out)))
+    cu_new, slots, positions = out
+    per_seq = (pp.S,)
+    _check_tensor(n_new, i32, per_seq, dev, "n_new")
+    _check_tensor(lens, i32, per_seq, dev, "lens")
+    if lens_out is not lens:
+        _check_tensor(lens_out, i32, per_seq, dev, "lens_out")
+    _check_tensor(table, i32, (pp.S, pp.max_pages), dev, "table")
+    _check_tensor(free_pages, i32, (pp.num_pages,), dev, "free_pages")
+    _check_tensor(free_count, i32, (1,), dev, "free_count")
+    if free_count_out is not free_count:
+        _check_tensor(free_count_out, i32, (1,), dev, "free_count_out")
+    _check_tensor(cu_new, i32, (pp.S + 1,), dev, "cu_new")
+    _check_tensor(slots, i32, (T,), dev, "slots")
+    _check_tensor(positions, i32, (T,), dev, "positions")
+    _call("ab_paged_plan", dev, pp.c(), T, n_new.data_ptr(), lens.data_ptr(), lens_out.data_ptr(), table.data_ptr(),
+          free_pages.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
+          positions.data_ptr())
     return out
 
 
@@ -686,7 +707,8 @@ def ab_paged_append(pp: PagedParams, nr: NormRope, q, k, v, slots, positions, K,
     queries Q [T, Hq, d] (`out` if given)."""
     dev, T, tok, Q = _paged_tokens(pp, nr, q, k, v, slots, positions, K, V, ksum, out)
     if T:
-        _call("ab_paged_append", dev, pp.c(), nr._c, T, *tok, _p(slots), _p(positions), _p(Q), _p(K), _p(V), _p(ksum))
+        _call("ab_paged_append", dev, pp.c(), nr._c, T, *tok, slots.data_ptr(), positions.data_ptr(), Q.data_ptr(),
+              K.data_ptr(), V.data_ptr(), _p(ksum))
     return Q
 
 
@@ -724,7 +746,8 @@ def ab_paged_select(pp: PagedParams, Q, ksum, table, lens, cu_new=None, workspac
     P = torch.zeros(shape, dtype=torch.float32, device=dev) if out is None else out
     _check_tensor(P, torch.float32, shape, dev, "P")
     ws = _paged_ws(pp, workspace, dev, True)
-    _call("ab_paged_select", dev, pp.c(), T, _p(Q), _p(ksum), _p(table), _p(lens), _p(cu_new), _p(P), _p(ws), ws.numel())
+    _call("ab_paged_select", dev, pp.c(), T, Q.data_ptr(), ksum.data_ptr(), table.data_ptr(), lens.data_ptr(), _p(cu_new),
+          P.data_ptr(), ws.data_ptr(), ws.numel())
     return P
 
 
@@ -740,7 +763,7 @@ def ab_paged_topk(pp: PagedParams, P, lens, out=None):
         out = (torch.zeros(shape, dtype=torch.int32, device=dev), torch.zeros(shape[:2], dtype=torch.int32, device=dev))
     _check_tensor(out[0], torch.int32, shape, dev, "idx")
     _check_tensor(out[1], torch.int32, shape[:2], dev, "count")
-    _call("ab_paged_topk", dev, pp.c(), _p(P), _p(lens), _p(out[0]), _p(out[1]))
+    _call("ab_paged_topk", dev, pp.c(), P.data_ptr(), lens.data_ptr(), out[0].data_ptr(), out[1].data_ptr())
     return out
 
 
@@ -763,8 +786,8 @@ def ab_attention_paged(pp: PagedParams, Q, K, V, table, lens, idx=None, count=No
     O = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if out is None else out
     _check_tensor(O, torch.bfloat16, shape, dev, "O")
     ws = _paged_ws(pp, workspace, dev, False)
-    _call("ab_attention_paged", dev, pp.c(), T, _p(Q), _p(K), _p(V), _p(table), _p(lens), _p(cu_new), _p(idx), _p(count),
-          _p(O), _p(ws), ws.numel())
+    _call("ab_attention_paged", dev, pp.c(), T, Q.data_ptr(), K.data_ptr(), V.data_ptr(), table.data_ptr(), lens.data_ptr(),
+          _p(cu_new), _p(idx), _p(count), O.data_ptr(), ws.data_ptr(), ws.numel())
     return O
 
 

@@ -21,17 +21,19 @@
 //    bytes a lane and copy, only the rows that hold keys, and the row's queries
 //    where a row begins.  (By TMA a tile of four 4 KB boxes each of K and V took
 //    1000 cycles, one of 2 KB boxes about as long: at most 32 bytes a cycle and
-//    about 100 cycles a box, where HBM needs 23 bytes a cycle.);
+//    about 100 cycles a box, where HBM needs 23 bytes a cycle.)
 //  - two groups of four warps take the rows in turn, so that one row's start and
 //    end, about 2000 cycles, overlap the next one's tiles (for G > 8 each group
-//    takes its half of the heads of every row); a group's warps take 16 (32) keys of each tile each, with a softmax state
-//    of their own, joined once per row.
+//    takes its half of the heads of every row); a group's warps take 16 (32)
+//    keys of each tile each, with a softmax state of their own, joined once per
+//    row.
 //
 // The G heads are the rows of an m16n8k16 product.  P is used as the sum of two
 // bfloat16 numbers, so that its rounding (2^-17) does not show next to the
 // output's own: a group has at most 8 heads, so the upper part fills rows 0-7
-// of the P V product and the lower part rows 8-15, at no cost.  V rows that lie behind the sequence's end are set to zero in the
-// operand, since 0 times what an unwritten page holds may be NaN.
+// of the P V product and the lower part rows 8-15, at no cost.  V rows that lie
+// behind the sequence's end are set to zero in the operand, since 0 times what
+// an unwritten page holds may be NaN.
 #pragma once
 
 #include <type_traits>
@@ -97,7 +99,7 @@ struct DecSmem {
   static constexpr int kOffPlan = kOffMl + kDecGroups * kMlBytes;      // 2 x 32 planned tiles
   static constexpr int kOffMeta = kOffPlan + 2 * 32 * int(sizeof(DecTile));  // per stage: valid, row, flags
   static constexpr int kOffBar = kOffMeta + kStages * 16;
-  static constexpr int kNumBars = 2 * kStages + 4;
+  static constexpr int kNumBars = 2 * kStages + 4 + kDecGroups;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 64;
   static constexpr int kAlloc = kBytes + 1024;
@@ -144,18 +146,6 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                : "memory");
 }
 
-// Barrier among `threads` threads that tells all of them whether any came with `p`.
-__device__ __forceinline__ bool bar_any(int id, int threads, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"(p ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
-
 // Arrive on `bar` when all of this thread's cp.async copies so far have landed
 // (counted among the barrier's arrivals).
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
@@ -177,6 +167,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
   auto empty = [&](int k) { return sbase + SM::kOffBar + 16u * uint32_t(k) + 8u; };
   auto plan_full = [&](int k) { return full(kStages + k); };
   auto plan_empty = [&](int k) { return empty(kStages + k); };
+  auto join_bar = [&](int k) { return full(kStages + 2) + 8u * uint32_t(k); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::kOffMisc);
   DecTile* plan = reinterpret_cast<DecTile*>(smem + SM::kOffPlan);
   // the prefix sums' scratch: stage memory that no copy has been issued into yet
@@ -193,6 +184,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
       mbar_init(plan_full(k), 1);
       mbar_init(plan_empty(k), 3);
     }
+    for (int k = 0; k < kDecGroups; ++k) mbar_init(join_bar(k), 4);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -388,13 +380,17 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
     const int head0 = split ? group * 8 : 0, heads = min(8, v.G - head0);  // this group's
     uint32_t q[D / 16][2];  // queries: rows 0-7 of the 16 x d operand (8-15 are zero)
     float o[D / 8][4], m = -INFINITY, l = 0.f;
+    // all of the group's warps are here (bounded like every wait: one of them may have given up)
+    uint32_t joins = 0;
+    auto group_sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(join_bar(group));
+      return warp_wait(join_bar(group), joins++ & 1, abort_flag);
+    };
     for (uint32_t use = 0; use < uint32_t(sh.n); ++use) {
       const int st = int(use % kStages);
       const bool got = mbar_wait(full(st), (use / kStages) & 1, abort_flag);
-      if (!__all_sync(0xffffffffu, got)) {
-        bar_any(1 + group, 128, true);  // the group's other warps learn of it at their next barrier
-        break;
-      }
+      if (!__all_sync(0xffffffffu, got)) break;
       const int4 mt = *reinterpret_cast<const int4*>(smem + SM::kOffMeta + st * 16);
       const int flags = mt.w;
       if (!split && ((flags >> kTileRow) & 1) != group) {  // another group's row
@@ -515,7 +511,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
       if (!(flags & kTileLast)) continue;
 
       // join the four warps' results of this row
-      if (bar_any(1 + group, 128, false)) break;  // the buffer's last readers are done
+      if (!group_sync()) break;  // the buffer's last readers are done
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       if (t == 0) ml[gwarp * 8 + g] = make_float2(m, l);
@@ -523,7 +519,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
 #pragma unroll
       for (int k = 0; k < D / 8; ++k)
         *reinterpret_cast<float2*>(dst + 8 * k) = make_float2(o[k][0] + o[k][2], o[k][1] + o[k][3]);
-      if (bar_any(1 + group, 128, false)) break;
+      if (!group_sync()) break;
       const bool whole = started && (flags & kRowEnd);
       const int64_t row = mt.z;
       const int slot = flags >> kTileRow == 0 ? 0 : 1;  // a partial row is this CTA's first or its last

@@ -28,7 +28,9 @@
 //    keys of each tile each, with a softmax state of their own, joined once per
 //    row.
 //
-// The G heads are the rows of an m16n8k16 product.  P is used as the sum of two
+// The products are m16n8k16, which this chip runs at one in about 16 cycles a
+// quarter of an SM, so their number counts: S is taken transposed, 16 keys by 8
+// heads, and P turned back on its way into P V (heads by dims).  P is used as the sum of two
 // bfloat16 numbers, so that its rounding (2^-17) does not show next to the
 // output's own: a group has at most 8 heads, so the upper part fills rows 0-7
 // of the P V product and the lower part rows 8-15, at no cost.  V rows that lie
@@ -150,6 +152,13 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
 // (counted among the barrier's arrivals).
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values, two in a row per lane.
+__device__ __forceinline__ uint32_t turn_8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // D: head dim.  kLists: the pages of a list instead of all.
@@ -365,21 +374,22 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
     const int group = warp >> 2, gwarp = warp & 3, gthread = threadIdx.x & 127;
     // this warp's keys of a tile: 16 of every 64.  Row addresses of the operand
     // loads (128-byte swizzle, 8-row groups of kHalves KB): K as stored, V
-    // transposed
+    // transposed, both by the same addresses
     constexpr int NB = SM::kTile / 64;
     constexpr uint32_t kBlock = 8 * kHalves * 1024;  // 64 keys
-    const int krow = gwarp * 16 + ((lane >> 4) << 3) + (lane & 7), kch = (lane >> 3) & 1;
-    const int vrow = gwarp * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;
-    // column 2 k + ch of a row is at (row's base + ((ch ^ row & 7) << 4)) ^ (k << 5)
-    const uint32_t kbase = uint32_t(krow >> 3) * (kHalves * 1024u) + uint32_t(krow & 7) * 128u + uint32_t((kch ^ (krow & 7)) << 4);
-    const uint32_t vbase = uint32_t(vrow >> 3) * (kHalves * 1024u) + uint32_t(vrow & 7) * 128u + uint32_t((vch ^ (vrow & 7)) << 4);
+    // 16 rows of a warp: lanes 0-15 the first 16-byte column of a pair, 16-31 the second
+    const int lrow = gwarp * 16 + (lane & 15);
+    // column 2 k + (lane >> 4) of a row is at (base + row) ^ (k << 5)
+    const uint32_t lbase = uint32_t(lrow >> 3) * (kHalves * 1024u) + uint32_t(lrow & 7) * 128u +
+                           uint32_t(((lane >> 4) ^ (lrow & 7)) << 4);
     float* mrg = reinterpret_cast<float*>(smem + SM::kOffMerge + group * SM::kMergeBytes);
     float2* ml = reinterpret_cast<float2*>(smem + SM::kOffMl + group * SM::kMlBytes);
     bool started = false;  // the current row's first tile is this CTA's
     const bool split = v.G > 8;
     const int head0 = split ? group * 8 : 0, heads = min(8, v.G - head0);  // this group's
-    uint32_t q[D / 16][2];  // queries: rows 0-7 of the 16 x d operand (8-15 are zero)
-    float o[D / 8][4], m = -INFINITY, l = 0.f;
+    uint32_t q[D / 16][2];  // queries: the d x 8 operand
+    float o[D / 8][4];      // head g and dims 8 k + 2 t, + 1: upper and lower part of P
+    float m[2], l[2];       // of heads 2 t, 2 t + 1 (l: this lane's keys)
     // all of the group's warps are here (bounded like every wait: one of them may have given up)
     uint32_t joins = 0;
     auto group_sync = [&]() -> bool {
@@ -405,8 +415,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
 #pragma unroll
           for (int z = 0; z < 2; ++z) q[k][z] = g < heads ? *reinterpret_cast<const uint32_t*>(from + 32 * k + 16 * z) : 0u;
         }
-        m = -INFINITY;
-        l = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 8; ++k)
 #pragma unroll
@@ -425,58 +435,63 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
       }
       const uint32_t kt = sbase + uint32_t(st) * 2u * SM::kTileBytes, vt = kt + SM::kTileBytes;
       if (some) {
-        // S = Q K^T, 8 keys by 8 keys, each in two accumulators
-        float c[2 * NB][2][4] = {};
+        // S^T = K Q^T, 16 keys by 8 heads, each in two accumulators
+        float c[NB][2][4] = {};
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            uint32_t b[4];
-            ldmatrix_x4(((kt + kbase) ^ uint32_t((kk & 3) << 5)) + nb * kBlock + uint32_t(kk >> 2) * 1024u, b);
-            mma_16816(c[2 * nb][kk & 1], q[kk][0], 0u, q[kk][1], 0u, b[0], b[1]);
-            mma_16816(c[2 * nb + 1][kk & 1], q[kk][0], 0u, q[kk][1], 0u, b[2], b[3]);
+            uint32_t k[4];
+            ldmatrix_x4(((kt + lbase) ^ uint32_t((kk & 3) << 5)) + nb * kBlock + uint32_t(kk >> 2) * 1024u, k);
+            mma_16816(c[nb][kk & 1], k[0], k[1], k[2], k[3], q[kk][0], q[kk][1]);
           }
         }
-        uint32_t hi[NB][2], lo[NB][2];  // P of keys (0-7: 2t, 2t+1), (8-15: 2t, 2t+1) as A operands
-        float x[NB][4];
-        float mx = -INFINITY;
+        float x[NB][4];  // key g, heads 2 t and 2 t + 1; key g + 8, the same heads
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int key = (e >> 1) * 8 + 2 * t + (e & 1), n8 = 2 * nb + (e >> 1);
-            x[nb][e] = c[n8][0][e & 1] + c[n8][1][e & 1];
-            if (!all && key >= valid[nb]) x[nb][e] = -INFINITY;
+            x[nb][e] = c[nb][0][e] + c[nb][1][e];
+            if (!all && (e >> 1) * 8 + g >= valid[nb]) x[nb][e] = -INFINITY;
+            mx[e & 1] = fmaxf(mx[e & 1], x[nb][e]);
           }
-          mx = fmaxf(fmaxf(mx, fmaxf(x[nb][0], x[nb][1])), fmaxf(x[nb][2], x[nb][3]));
         }
-        mx *= a.scale_log2;
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if (__any_sync(0xffffffffu, mx > m + kDecLazy)) {
-          const float mn = fmaxf(m, mx);
-          const float al = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
-          m = mn;
-          l *= al;
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) mx[z] = fmaxf(mx[z], __shfl_xor_sync(0xffffffffu, mx[z], off));
+        mx[0] *= a.scale_log2;
+        mx[1] *= a.scale_log2;
+        if (__any_sync(0xffffffffu, mx[0] > m[0] + kDecLazy || mx[1] > m[1] + kDecLazy)) {
+          float al[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const float mn = fmaxf(m[z], mx[z]);
+            al[z] = mn == -INFINITY ? 1.f : ex2_approx(m[z] - mn);
+            m[z] = mn;
+            l[z] *= al[z];
+          }
+          const float a0 = __shfl_sync(0xffffffffu, al[0], g >> 1), a1 = __shfl_sync(0xffffffffu, al[1], g >> 1);
+          const float of_g = g & 1 ? a1 : a0;
 #pragma unroll
           for (int k8 = 0; k8 < D / 8; ++k8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[k8][e] *= al;
+            for (int e = 0; e < 4; ++e) o[k8][e] *= of_g;
         }
-        const float ref = m == -INFINITY ? 0.f : m;
+        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        uint32_t hi[NB][2], lo[NB][2];  // P of head g, keys (0-7: 2t, 2t+1), (8-15: 2t, 2t+1), as A operands
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = ex2_approx(fmaf(x[nb][e], a.scale_log2, -ref));
-            l += p[e];
-          }
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            hi[nb][z] = pack_bf16x2(p[2 * z], p[2 * z + 1]);
-            lo[nb][z] = pack_bf16x2(p[2 * z] - __uint_as_float(hi[nb][z] << 16),
-                                    p[2 * z + 1] - __uint_as_float(hi[nb][z] & 0xFFFF0000u));
+            const float p0 = ex2_approx(fmaf(x[nb][2 * z], a.scale_log2, -ref[0]));
+            const float p1 = ex2_approx(fmaf(x[nb][2 * z + 1], a.scale_log2, -ref[1]));
+            l[0] += p0;
+            l[1] += p1;
+            const uint32_t up = pack_bf16x2(p0, p1);
+            hi[nb][z] = turn_8x8(up);
+            lo[nb][z] = turn_8x8(pack_bf16x2(p0 - __uint_as_float(up << 16), p1 - __uint_as_float(up & 0xFFFF0000u)));
           }
         }
         // O += P V: rows 0-7 the upper part of P, rows 8-15 the lower; V rows
@@ -491,7 +506,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
 #pragma unroll
             for (int np = 0; np < D / 16; ++np) {
               uint32_t b[4];
-              ldmatrix_x4_trans(((vt + vbase) ^ uint32_t((np & 3) << 5)) + nb * kBlock + uint32_t(np >> 2) * 1024u, b);
+              ldmatrix_x4_trans(((vt + lbase) ^ uint32_t((np & 3) << 5)) + nb * kBlock + uint32_t(np >> 2) * 1024u, b);
               if constexpr (decltype(partial)::value) {
                 b[0] &= keep[0];
                 b[1] &= keep[1];
@@ -512,9 +527,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
 
       // join the four warps' results of this row
       if (!group_sync()) break;  // the buffer's last readers are done
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (t == 0) ml[gwarp * 8 + g] = make_float2(m, l);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) l[z] += __shfl_xor_sync(0xffffffffu, l[z], off);
+      if (g == 0) {
+        ml[gwarp * 8 + 2 * t] = make_float2(m[0], l[0]);
+        ml[gwarp * 8 + 2 * t + 1] = make_float2(m[1], l[1]);
+      }
       float* dst = mrg + (gwarp * 8 + g) * SM::kPitch + 2 * t;
 #pragma unroll
       for (int k = 0; k < D / 8; ++k)

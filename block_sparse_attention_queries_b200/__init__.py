@@ -491,21 +491,41 @@ def ab_forward_host(p: Params, Qh, Kh, Vh, Oh, Qd, Kd, Vd, bufs: Buffers, device
 
 
 # ------------------------------------------- norm and rotation, paged cache
-def _check_tensor(t, dtype, shape, index, name):
-    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {dtype} {list(shape)} on cuda:{index}, got {t.dtype} {list(t.shape)}"
-                         f"{'' if t.is_contiguous() else ' (strided)'} on {t.device}")
+_marshal_module = None
+
+
+def _m():
+    """The built checks of tensors (csrc/marshal.cpp)."""
+    global _marshal_module
+    if _marshal_module is None:
+        import torch  # noqa: F401  (its libraries are loaded first)
+        try:
+            from . import _marshal
+        except ImportError as e:
+            raise RuntimeError("_marshal.so not built; run block_sparse_attention_queries_b200/build.py") from e
+        _marshal_module = _marshal
+    return _marshal_module
 
 
 _fns = {}
 
 
+def _fn(fn_name):
+    """The library's function with every pointer as an address or bytes."""
+    ref = getattr(lib(), fn_name)
+    fn = lib()[fn_name]
+    scalars = (ctypes.c_int32, ctypes.c_size_t)
+    fn.argtypes = [t if t in scalars or t in (ctypes.POINTER(ab_params), ctypes.POINTER(ab_paged_params),
+                                              ctypes.POINTER(ab_norm_rope)) else ctypes.c_void_p for t in ref.argtypes]
+    fn.restype = ref.restype
+    _fns[fn_name] = fn
+    return fn
+
+
 def _call(fn_name, index, *args):
     """The library's function on CUDA device `index` and its current stream."""
     import torch
-    fn = _fns.get(fn_name)
-    if fn is None:
-        fn = _fns[fn_name] = getattr(lib(), fn_name)
+    fn = _fns.get(fn_name) or _fn(fn_name)
     if index == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
@@ -522,10 +542,6 @@ def _cuda_index(t):
     return index
 
 
-def _p(t):
-    return None if t is None else t.data_ptr()
-
-
 def _c(p: Params) -> ab_params:
     """p.c(), made once (Params are immutable)."""
     c = p.__dict__.get("_c")
@@ -535,30 +551,21 @@ def _c(p: Params) -> ab_params:
     return c
 
 
-def _tokens(t, shape, index, name):
-    """The strided tokens [(B,) T, H, d] as the library takes them."""
-    import torch
-    st = t.stride()
-    if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape or st[-1] != 1:
-        raise ValueError(f"{name}: expected bf16 {list(shape)} with contiguous heads on cuda:{index}, got {t.dtype} "
-                         f"{list(t.shape)}, strides {st}, on {t.device}")
-    return ab_tokens(t.data_ptr(), st[0] if len(shape) == 4 else 0, st[-3], st[-2])
-
-
 def _dense_tokens(p: Params, nr: NormRope, q, k, v, pos_q, pos_k):
-    """Checked arguments of the calls from the projections' layout."""
+    """Checked arguments of the calls from the projections' layout: device, tokens, positions."""
     import torch
-    given = [t for t in (q, k, v) if t is not None]
-    if not given:
+    first = q if q is not None else k if k is not None else v
+    if first is None:
         raise ValueError("none of q, k, v is given")
-    dev = _cuda_index(given[0])
+    dev = _cuda_index(first)
     nr.check(p.H, p.H, p.d, dev)
-    tok = [None if t is None else _tokens(t, (p.B, n, p.H, p.d), dev, name)
-           for t, n, name in ((q, p.L, "q"), (k, p.Lk, "k"), (v, p.Lk, "v"))]
-    for pos, n, name in ((pos_q, p.L, "pos_q"), (pos_k, p.Lk, "pos_k")):
-        if pos is not None:
-            _check_tensor(pos, torch.int32, (p.B, n), dev, name)
-    return dev, tok
+    m, L, Lk = _m(), p.L, p.Lk
+    kv = (p.B, Lk, p.H, p.d)
+    tok = (None if q is None else m.tokens(dev, q, (p.B, L, p.H, p.d), "q"), None if k is None else m.tokens(dev, k, kv, "k"),
+           None if v is None else m.tokens(dev, v, kv, "v"))
+    pos = (None, None) if pos_q is None and pos_k is None else \
+        m.tensors(dev, pos_q, torch.int32, (p.B, L), "pos_q", pos_k, torch.int32, (p.B, Lk), "pos_k")
+    return dev, tok, pos
 
 
 def ab_qk_norm_rope(p: Params, nr: NormRope, q, k=None, v=None, pos_q=None, pos_k=None, out=None):
@@ -570,18 +577,16 @@ def ab_qk_norm_rope(p: Params, nr: NormRope, q, k=None, v=None, pos_q=None, pos_
     the tables (None: 0, 1, 2, ...).  `out` = (Q, K, V) writes into caller-owned
     tensors."""
     import torch
-    dev, tok = _dense_tokens(p, nr, q, k, v, pos_q, pos_k)
-    shapes = [None if t is None else (p.B, p.H, n, p.d) for t, n in ((q, p.L), (k, p.Lk), (v, p.Lk))]
+    bf16 = torch.bfloat16
+    dev, tok, pos = _dense_tokens(p, nr, q, k, v, pos_q, pos_k)
+    sq, sk = (p.B, p.H, p.L, p.d), (p.B, p.H, p.Lk, p.d)
     if out is None:
-        out = tuple(None if s is None else torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes)
+        out = tuple(torch.empty(s, dtype=bf16, device=dev) if t is not None else None for t, s in ((q, sq), (k, sk), (v, sk)))
     else:
-        for t, s, name in zip(out, shapes, "QKV"):
-            if s is not None:
-                if t is None:
-                    raise ValueError(f"out has no {name}")
-                _check_tensor(t, torch.bfloat16, s, dev, name)
-    _call("ab_qk_norm_rope", dev, _c(p), nr._c, *tok, _p(pos_q), _p(pos_k), *(_p(t) for t in out))
-    return tuple(t if s is not None else None for t, s in zip(out, shapes))
+        out = tuple(o if t is not None else None for t, o in zip((q, k, v), out))
+    ptrs = _m().tensors(dev, out[0], bf16, sq, "Q", out[1], bf16, sk, "K", out[2], bf16, sk, "V")
+    _call("ab_qk_norm_rope", dev, _c(p), nr._c, *tok, *pos, *ptrs)
+    return out
 
 
 def ab_forward_qkv(p: Params, nr: NormRope, q, k, v, pos_q=None, pos_k=None, bufs: Buffers | None = None) -> Buffers:
@@ -589,19 +594,19 @@ def ab_forward_qkv(p: Params, nr: NormRope, q, k, v, pos_q=None, pos_k=None, buf
     [B, L, H, d], k and v [B, Lk, H, d].  The rotated tensors are the returned
     buffers' Q, K and V (made on the first call if `bufs` has none)."""
     import torch
-    dev, tok = _dense_tokens(p, nr, q, k, v, pos_q, pos_k)
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    dev, tok, pos = _dense_tokens(p, nr, q, k, v, pos_q, pos_k)
     if None in tok:
         raise ValueError("q, k and v are all needed")
     b = Buffers(p, q.device) if bufs is None else bufs
     for name, n in (("Q", p.L), ("K", p.Lk), ("V", p.Lk)):
         if getattr(b, name, None) is None:
-            setattr(b, name, torch.empty(p.B, p.H, n, p.d, dtype=torch.bfloat16, device=dev))
-        _check_tensor(getattr(b, name), torch.bfloat16, (p.B, p.H, n, p.d), dev, name)
-    for name, shape in (("P", (p.B, p.H, p.Nq, p.Nkv)), ("idx", (p.B, p.H, p.Nq, p.Nkv)),
-                        ("pi_q32", (p.B, p.H, p.Nq, p.Nkv)), ("count", (p.B, p.H, p.Nq)), ("O", (p.B, p.H, p.L, p.d))):
-        _check_tensor(getattr(b, name), getattr(b, name).dtype, shape, dev, name)
-    _call("ab_forward_qkv", dev, _c(p), nr._c, *tok, _p(pos_q), _p(pos_k), _p(b.Q), _p(b.K), _p(b.V), _p(b.P),
-          _p(b.idx), _p(b.pi_q32), _p(b.count), _p(b.O), _p(b.ws), b.ws.numel())
+            setattr(b, name, torch.empty(p.B, p.H, n, p.d, dtype=bf16, device=dev))
+    sq, sk, rows = (p.B, p.H, p.L, p.d), (p.B, p.H, p.Lk, p.d), (p.B, p.H, p.Nq, p.Nkv)
+    ptrs = _m().tensors(dev, b.Q, bf16, sq, "Q", b.K, bf16, sk, "K", b.V, bf16, sk, "V", b.P, f32, rows, "P", b.idx, i32, rows,
+                        "idx", b.pi_q32, b.pi_q32.dtype, rows, "pi_q32", b.count, i32, rows[:3], "count", b.O, bf16, sq, "O",
+                        b.ws, torch.uint8, (b.ws.numel(),), "ws")
+    _call("ab_forward_qkv", dev, _c(p), nr._c, *tok, *pos, *ptrs, b.ws.numel())
     return b
 
 
@@ -648,7 +653,7 @@ def ab_paged_plan(pp: PagedParams, n_new, lens, table, free_pages, free_count, T
     tensors."""
     import torch
     dev = _cuda_index(n_new)
-    i32 = torch.int32
+    i32, seqs, one = torch.int32, (pp.S,), (1,)
     if out is None:
         if T is None:
             raise ValueError("T or out is needed")
@@ -656,48 +661,23 @@ def ab_paged_plan(pp: PagedParams, n_new, lens, table, free_pages, free_count, T
                torch.empty(T, dtype=i32, device=dev))
     elif T is None:
         T = out[1].numel()
-    lens_out = lens if lens_out is None else lens_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    cu_new, slots, positions = out
-    per_seq = (pp.S,)
-    _check_tensor(n_new, i32, per_seq, dev, "n_new")
-    _check_tensor(lens, i32, per_seq, dev, "lens")
-    if lens_out is not lens:
-        _check_tensor(lens_out, i32, per_seq, dev, "lens_out")
-    _check_tensor(table, i32, (pp.S, pp.max_pages), dev, "table")
-    _check_tensor(free_pages, i32, (pp.num_pages,), dev, "free_pages")
-    _check_tensor(free_count, i32, (1,), dev, "free_count")
-    if free_count_out is not free_count:
-        _check_tensor(free_count_out, i32, (1,), dev, "free_count_out")
-    _check_tensor(cu_new, i32, (pp.S + 1,), dev, "cu_new")
-    _check_tensor(slots, i32, (T,), dev, "slots")
-    _check_tensor(positions, i32, (T,), dev, "positions")
-    _call("ab_paged_plan", dev, pp.c(), T, n_new.data_ptr(), lens.data_ptr(), lens_out.data_ptr(), table.data_ptr(),
-          free_pages.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
-          positions.data_ptr())
+    ptrs = _m().tensors(dev, n_new, i32, seqs, "n_new", lens, i32, seqs, "lens",
+                        lens if lens_out is None else lens_out, i32, seqs, "lens_out",
+                        table, i32, (pp.S, pp.max_pages), "table", free_pages, i32, (pp.num_pages,), "free_pages",
+                        free_count, i32, one, "free_count", free_count if free_count_out is None else free_count_out, i32, one,
+                        "free_count_out", out[0], i32, (pp.S + 1,), "cu_new", out[1], i32, (T,), "slots",
+                        out[2], i32, (T,), "positions")
+    _call("ab_paged_plan", dev, pp.c(), T, *ptrs)
     return out
 
 
-def _paged_tokens(pp: PagedParams, nr: NormRope, q, k, v, slots, positions, K, V, ksum, Q):
-    """Checked arguments of the calls that write tokens into the cache."""
-    import torch
+def _paged_tokens(pp: PagedParams, nr: NormRope, q, k, v):
+    """Checked new tokens: device, their number, the library's arguments."""
     dev = _cuda_index(q)
-    T = q.shape[0]
-    nr.check(pp.Hq, pp.Hkv, pp.d, dev)
-    tok = (_tokens(q, (T, pp.Hq, pp.d), dev, "q"), _tokens(k, (T, pp.Hkv, pp.d), dev, "k"),
-           _tokens(v, (T, pp.Hkv, pp.d), dev, "v"))
-    _check_tensor(slots, torch.int32, (T,), dev, "slots")
-    _check_tensor(positions, torch.int32, (T,), dev, "positions")
-    kv = (pp.num_pages, pp.Hkv, pp.page, pp.d)
-    _check_tensor(K, torch.bfloat16, kv, dev, "K")
-    _check_tensor(V, torch.bfloat16, kv, dev, "V")
-    if ksum is not None:
-        _check_tensor(ksum, torch.bfloat16, (pp.num_pages, pp.Hkv, pp.d), dev, "ksum")
-    if Q is None:
-        Q = torch.empty(T, pp.Hq, pp.d, dtype=torch.bfloat16, device=dev)
-    else:
-        _check_tensor(Q, torch.bfloat16, (T, pp.Hq, pp.d), dev, "Q")
-    return dev, T, tok, Q
+    T, Hq, Hkv, d = q.shape[0], pp.Hq, pp.Hkv, pp.d
+    nr.check(Hq, Hkv, d, dev)
+    m, kv = _m(), (T, Hkv, d)
+    return dev, T, (m.tokens(dev, q, (T, Hq, d), "q"), m.tokens(dev, k, kv, "k"), m.tokens(dev, v, kv, "v"))
 
 
 def ab_paged_append(pp: PagedParams, nr: NormRope, q, k, v, slots, positions, K, V, ksum=None, out=None):
@@ -705,33 +685,23 @@ def ab_paged_append(pp: PagedParams, nr: NormRope, q, k, v, slots, positions, K,
     (strides as for ab_qk_norm_rope), keys and values written to their slots of
     the cache, the touched pages' means to ksum (None: not kept); returns the
     queries Q [T, Hq, d] (`out` if given)."""
-    dev, T, tok, Q = _paged_tokens(pp, nr, q, k, v, slots, positions, K, V, ksum, out)
+    import torch
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev, T, tok = _paged_tokens(pp, nr, q, k, v)
+    rows, kv = (T, pp.Hq, pp.d), (pp.num_pages, pp.Hkv, pp.page, pp.d)
+    Q = torch.empty(rows, dtype=bf16, device=dev) if out is None else out
+    ptrs = _m().tensors(dev, slots, i32, (T,), "slots", positions, i32, (T,), "positions", Q, bf16, rows, "Q", K, bf16, kv, "K",
+                        V, bf16, kv, "V", ksum, bf16, (pp.num_pages, pp.Hkv, pp.d), "ksum")
     if T:
-        _call("ab_paged_append", dev, pp.c(), nr._c, T, *tok, slots.data_ptr(), positions.data_ptr(), Q.data_ptr(),
-              K.data_ptr(), V.data_ptr(), _p(ksum))
+        _call("ab_paged_append", dev, pp.c(), nr._c, T, *tok, *ptrs)
     return Q
 
 
-def _paged_rows(pp: PagedParams, Q, table, lens, cu_new):
-    import torch
-    dev = _cuda_index(Q)
+def _query_rows(pp: PagedParams, Q, cu_new) -> int:
     T = Q.shape[0]
     if cu_new is None and T != pp.S:
         raise ValueError(f"Q has {T} rows, {pp.S} expected without cu_new")
-    _check_tensor(Q, torch.bfloat16, (T, pp.Hq, pp.d), dev, "Q")
-    _check_tensor(table, torch.int32, (pp.S, pp.max_pages), dev, "table")
-    _check_tensor(lens, torch.int32, (pp.S,), dev, "lens")
-    if cu_new is not None:
-        _check_tensor(cu_new, torch.int32, (pp.S + 1,), dev, "cu_new")
-    return dev, T
-
-
-def _paged_ws(pp: PagedParams, workspace, dev, select):
-    import torch
-    if workspace is None:
-        return alloc_paged_workspace(pp, dev, select)
-    _check_tensor(workspace, torch.uint8, (workspace.numel(),), dev, "workspace")
-    return workspace
+    return T
 
 
 def ab_paged_select(pp: PagedParams, Q, ksum, table, lens, cu_new=None, workspace=None, out=None):
@@ -740,14 +710,16 @@ def ab_paged_select(pp: PagedParams, Q, ksum, table, lens, cu_new=None, workspac
     are left as they were, 0 in a new P).  Q [S, Hq, d], or [T, Hq, d] with
     cu_new [S + 1] as ab_paged_plan returns it."""
     import torch
-    dev, T = _paged_rows(pp, Q, table, lens, cu_new)
-    _check_tensor(ksum, torch.bfloat16, (pp.num_pages, pp.Hkv, pp.d), dev, "ksum")
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    dev, T = _cuda_index(Q), _query_rows(pp, Q, cu_new)
     shape = (pp.S, pp.Hkv, pp.max_pages)
-    P = torch.zeros(shape, dtype=torch.float32, device=dev) if out is None else out
-    _check_tensor(P, torch.float32, shape, dev, "P")
-    ws = _paged_ws(pp, workspace, dev, True)
-    _call("ab_paged_select", dev, pp.c(), T, Q.data_ptr(), ksum.data_ptr(), table.data_ptr(), lens.data_ptr(), _p(cu_new),
-          P.data_ptr(), ws.data_ptr(), ws.numel())
+    P = torch.zeros(shape, dtype=f32, device=dev) if out is None else out
+    ws = alloc_paged_workspace(pp, dev, True) if workspace is None else workspace
+    n = ws.numel()
+    ptrs = _m().tensors(dev, Q, bf16, (T, pp.Hq, pp.d), "Q", ksum, bf16, (pp.num_pages, pp.Hkv, pp.d), "ksum",
+                        table, i32, (pp.S, pp.max_pages), "table", lens, i32, (pp.S,), "lens", cu_new, i32, (pp.S + 1,), "cu_new",
+                        P, f32, shape, "P", ws, torch.uint8, (n,), "workspace")
+    _call("ab_paged_select", dev, pp.c(), T, *ptrs, n)
     return P
 
 
@@ -755,15 +727,14 @@ def ab_paged_topk(pp: PagedParams, P, lens, out=None):
     """The pages to attend to: (idx [S, Hkv, max_pages], count [S, Hkv]) int32,
     the newest `recent` pages and those of largest P, keep_ratio of them in all."""
     import torch
+    i32 = torch.int32
     dev = _cuda_index(P)
     shape = (pp.S, pp.Hkv, pp.max_pages)
-    _check_tensor(P, torch.float32, shape, dev, "P")
-    _check_tensor(lens, torch.int32, (pp.S,), dev, "lens")
     if out is None:
-        out = (torch.zeros(shape, dtype=torch.int32, device=dev), torch.zeros(shape[:2], dtype=torch.int32, device=dev))
-    _check_tensor(out[0], torch.int32, shape, dev, "idx")
-    _check_tensor(out[1], torch.int32, shape[:2], dev, "count")
-    _call("ab_paged_topk", dev, pp.c(), P.data_ptr(), lens.data_ptr(), out[0].data_ptr(), out[1].data_ptr())
+        out = (torch.zeros(shape, dtype=i32, device=dev), torch.zeros(shape[:2], dtype=i32, device=dev))
+    ptrs = _m().tensors(dev, P, torch.float32, shape, "P", lens, i32, (pp.S,), "lens", out[0], i32, shape, "idx",
+                        out[1], i32, shape[:2], "count")
+    _call("ab_paged_topk", dev, pp.c(), *ptrs)
     return out
 
 
@@ -773,21 +744,19 @@ def ab_attention_paged(pp: PagedParams, Q, K, V, table, lens, idx=None, count=No
     the listed ones); Q as for ab_paged_select; returns O [S, Hq, d] bf16 (rows
     of sequences without a new token are left as they were, 0 in a new O)."""
     import torch
-    dev, T = _paged_rows(pp, Q, table, lens, cu_new)
-    kv = (pp.num_pages, pp.Hkv, pp.page, pp.d)
-    _check_tensor(K, torch.bfloat16, kv, dev, "K")
-    _check_tensor(V, torch.bfloat16, kv, dev, "V")
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev, T = _cuda_index(Q), _query_rows(pp, Q, cu_new)
     if (idx is None) != (count is None):
         raise ValueError("idx and count come together")
-    if idx is not None:
-        _check_tensor(idx, torch.int32, (pp.S, pp.Hkv, pp.max_pages), dev, "idx")
-        _check_tensor(count, torch.int32, (pp.S, pp.Hkv), dev, "count")
-    shape = (pp.S, pp.Hq, pp.d)
-    O = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if out is None else out
-    _check_tensor(O, torch.bfloat16, shape, dev, "O")
-    ws = _paged_ws(pp, workspace, dev, False)
-    _call("ab_attention_paged", dev, pp.c(), T, Q.data_ptr(), K.data_ptr(), V.data_ptr(), table.data_ptr(), lens.data_ptr(),
-          _p(cu_new), _p(idx), _p(count), O.data_ptr(), ws.data_ptr(), ws.numel())
+    kv, shape, lists = (pp.num_pages, pp.Hkv, pp.page, pp.d), (pp.S, pp.Hq, pp.d), (pp.S, pp.Hkv, pp.max_pages)
+    O = torch.zeros(shape, dtype=bf16, device=dev) if out is None else out
+    ws = alloc_paged_workspace(pp, dev, False) if workspace is None else workspace
+    n = ws.numel()
+    ptrs = _m().tensors(dev, Q, bf16, (T, pp.Hq, pp.d), "Q", K, bf16, kv, "K", V, bf16, kv, "V",
+                        table, i32, (pp.S, pp.max_pages), "table", lens, i32, (pp.S,), "lens", cu_new, i32, (pp.S + 1,), "cu_new",
+                        idx, i32, lists, "idx", count, i32, lists[:2], "count", O, bf16, shape, "O",
+                        ws, torch.uint8, (n,), "workspace")
+    _call("ab_attention_paged", dev, pp.c(), T, *ptrs, n)
     return O
 
 
@@ -810,21 +779,19 @@ def ab_paged_forward(pp: PagedParams, nr: NormRope, q, k, v, cache: PagedCache, 
     and v [T, Hkv, d], after ab_paged_plan: append, select, top-k, attention of
     each sequence's newest token."""
     import torch
-    T = q.shape[0]
-    b = PagedBuffers(pp, T, torch.device("cuda", _cuda_index(q))) if bufs is None else bufs
-    c = cache
-    dev, T, tok, Q = _paged_tokens(pp, nr, q, k, v, slots, positions, c.K, c.V, c.ksum, b.Q)
-    _paged_rows(pp, Q, c.table, c.lens, cu_new)
+    bf16, i32 = torch.bfloat16, torch.int32
     if cu_new is None:
         raise ValueError("cu_new is needed")
-    shape = (pp.S, pp.Hkv, pp.max_pages)
-    for t, dtype, s, name in ((c.ksum, torch.bfloat16, (pp.num_pages, pp.Hkv, pp.d), "ksum"), (b.P, torch.float32, shape, "P"),
-                              (b.idx, torch.int32, shape, "idx"), (b.count, torch.int32, shape[:2], "count"),
-                              (b.O, torch.bfloat16, (pp.S, pp.Hq, pp.d), "O")):
-        _check_tensor(t, dtype, s, dev, name)
-    ws = _paged_ws(pp, c.ws, dev, True)
-    _call("ab_paged_forward", dev, pp.c(), nr._c, T, *tok, _p(slots), _p(positions), _p(c.table), _p(c.lens), _p(cu_new),
-          _p(Q), _p(c.K), _p(c.V), _p(c.ksum), _p(b.P), _p(b.idx), _p(b.count), _p(b.O), _p(ws), ws.numel())
+    dev, T, tok = _paged_tokens(pp, nr, q, k, v)
+    c, b = cache, PagedBuffers(pp, T, dev) if bufs is None else bufs
+    kv, shape = (pp.num_pages, pp.Hkv, pp.page, pp.d), (pp.S, pp.Hkv, pp.max_pages)
+    n = c.ws.numel()
+    ptrs = _m().tensors(dev, slots, i32, (T,), "slots", positions, i32, (T,), "positions",
+                        c.table, i32, (pp.S, pp.max_pages), "table", c.lens, i32, (pp.S,), "lens", cu_new, i32, (pp.S + 1,), "cu_new",
+                        b.Q, bf16, (T, pp.Hq, pp.d), "Q", c.K, bf16, kv, "K", c.V, bf16, kv, "V",
+                        c.ksum, bf16, (pp.num_pages, pp.Hkv, pp.d), "ksum", b.P, torch.float32, shape, "P", b.idx, i32, shape, "idx",
+                        b.count, i32, shape[:2], "count", b.O, bf16, (pp.S, pp.Hq, pp.d), "O", c.ws, torch.uint8, (n,), "workspace")
+    _call("ab_paged_forward", dev, pp.c(), nr._c, T, *tok, *ptrs, n)
     return b
 
 

@@ -225,7 +225,7 @@ ab_status check_paged(const ab_paged_params* p) {
   if (p->page != 16 && p->page != 32 && p->page != 64) return p->page > 0 ? AB_ERR_UNSUPPORTED : AB_ERR_INVALID_ARG;
   if (int64_t(p->max_pages) * p->page > (int64_t(1) << 24)) return AB_ERR_INVALID_ARG;
   if (int64_t(p->num_pages) * p->page > INT_MAX || int64_t(p->num_pages) * p->Hkv > INT_MAX) return AB_ERR_INVALID_ARG;
-  if (p->S > kMaxSeqs || p->Hq / p->Hkv > kMaxGroup || int64_t(p->S) * p->Hkv > kShareMaxUnits)
+  if (p->S > kMaxSeqs || p->Hkv > 65535 || p->Hq / p->Hkv > kMaxGroup || int64_t(p->S) * p->Hkv > kShareMaxUnits)
     return AB_ERR_UNSUPPORTED;
   // positions in the list of all tiles of 64 keys, and their cost, stay in 32 bits
   if (int64_t(p->S) * p->Hkv * ((int64_t(p->max_pages) * p->page + 63) / 64) > INT_MAX / 4)

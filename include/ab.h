@@ -469,6 +469,7 @@ ab_status ab_paged_append(const ab_paged_params* p, const ab_norm_rope* nr, int3
  * clusters).
  *   P  device, out, fp32 [S, Hkv, max_pages]; entries behind the sequence's
  *      last page are left as they were.
+ * A page whose table entry is out of range counts as one whose mean is zero.
  */
 ab_status ab_paged_select(const ab_paged_params* p, int32_t T, const void* Q, const void* ksum, const int32_t* table,
                           const int32_t* lens, const int32_t* cu_new, float* P, void* workspace, size_t ws_bytes,

@@ -494,3 +494,94 @@ def test_other_stream_and_shared_workspace(dev):
         O2 = ab.ab_attention_paged(pp, *args, workspace=ws)
     torch.cuda.current_stream(dev).wait_stream(st)
     assert torch.equal(O, want) and torch.equal(O2, want)
+
+
+def test_offsets_beyond_32_bits(dev):
+    # K and V of 2.3e9 elements each, the sequence in the last pages
+    num_pages, Hkv, page, d = 70000, 4, 64, 128
+    K, V = (torch.zeros(num_pages, Hkv, page, d, dtype=BF16, device=dev) for _ in range(2))
+    ksum = torch.zeros(num_pages, Hkv, d, dtype=BF16, device=dev)
+    lens = [300, 7]
+    c = ref.Cache(lens, Hkv, d, page, 95)
+    c.table = torch.where(c.table >= 0, c.table + (num_pages - c.num_pages), c.table)
+    for t, small in ((K, c.K), (V, c.V), (ksum, c.ksum)):
+        t[num_pages - c.num_pages:] = small.to(dev)
+    pp = ab.PagedParams(2, 8, Hkv, d, page, num_pages, c.max_pages)
+    q = torch.randn(2, 8, d, generator=torch.Generator().manual_seed(96)).to(BF16)
+    O = ab.ab_attention_paged(pp, q.to(dev), K, V, c.table.to(dev), ints(lens, dev))
+    _check_attention(O.cpu(), q, c)
+    small_pp = ab.PagedParams(2, 8, Hkv, d, page, c.num_pages, c.max_pages)
+    small_table = torch.where(c.table >= 0, c.table - (num_pages - c.num_pages), c.table).to(dev)
+    assert torch.equal(ab.ab_paged_select(pp, q.to(dev), ksum, c.table.to(dev), ints(lens, dev)),
+                       ab.ab_paged_select(small_pp, q.to(dev), c.ksum.to(dev), small_table, ints(lens, dev)))
+    # one more token, in the last slot of the cache
+    x = torch.randn(1, 16, d, generator=torch.Generator().manual_seed(97)).to(BF16).to(dev)
+    slot = num_pages * page - 1
+    Q = ab.ab_paged_append(pp, ab.NormRope("none"), x[:, :8], x[:, 8:12], x[:, 12:], ints([slot], dev), ints([0], dev), K, V, ksum=ksum)
+    assert torch.equal(Q, x[:, :8]) and torch.equal(K[-1, :, -1], x[0, 8:12]) and torch.equal(V[-1, :, -1], x[0, 12:])
+    mean = K[-1].double().mean(1)
+    assert torch.isnan(mean).any() or ((ksum[-1].double() - mean).abs() <= 2 * ref.HALF * mean.abs() + 1e-5).all()
+
+
+def test_two_streams_at_once(dev):
+    # calls that overlap, each with its own workspace
+    g = torch.Generator().manual_seed(98)
+    work = []
+    for k in range(2):
+        lens = [3000 + 999 * k, 50, 2000]
+        c = ref.Cache(lens, 2, 64, 16, 99 + k)
+        q = torch.randn(3, 6, 64, generator=g).to(BF16)
+        pp = ab.PagedParams(3, 6, 2, 64, 16, c.num_pages, c.max_pages, keep_ratio=0.4)
+        args = [t.to(dev) for t in (q, c.K, c.V, c.table, c.ksum)] + [ints(lens, dev)]
+        work.append((pp, c, q, args, ab.alloc_paged_workspace(pp, dev), torch.cuda.Stream(dev)))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for k, (pp, c, q, (Q, K, V, table, ksum, lens), ws, st) in enumerate(work):
+            with torch.cuda.stream(st):
+                P = ab.ab_paged_select(pp, Q, ksum, table, lens, workspace=ws)
+                idx, count = ab.ab_paged_topk(pp, P, lens)
+                got[k].append((ab.ab_attention_paged(pp, Q, K, V, table, lens, workspace=ws),
+                               ab.ab_attention_paged(pp, Q, K, V, table, lens, idx=idx, count=count, workspace=ws)))
+    torch.cuda.synchronize()
+    for k, (pp, c, q, *_) in enumerate(work):
+        _check_attention(got[k][0][0].cpu(), q, c)
+        for O, S in got[k][1:]:
+            assert torch.equal(O, got[k][0][0]) and torch.equal(S, got[k][0][1])
+
+
+def test_two_graphs_share_a_workspace(dev):
+    cases = []
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device=dev)
+    for k, (Hq, d, page, lens) in enumerate(((4, 128, 16, [700, 3]), (12, 64, 32, [64, 1500, 0]))):
+        c = ref.Cache(lens, 2 if k == 0 else 1, d, page, 110 + k)
+        q = torch.randn(len(lens), Hq, d, generator=torch.Generator().manual_seed(k)).to(BF16)
+        pp = ab.PagedParams(len(lens), Hq, c.Hkv, d, page, c.num_pages, c.max_pages)
+        w = ab.alloc_paged_workspace(pp, dev) if ws.numel() < ab.paged_workspace_size(pp) else ws
+        ws = w
+        cases.append((pp, c, q, [t.to(dev) for t in (q, c.K, c.V, c.table)] + [ints(lens, dev)]))
+    graphs = []
+    for pp, c, q, args in cases:
+        O = torch.zeros(len(c.lens), pp.Hq, pp.d, dtype=BF16, device=dev)
+        ab.ab_attention_paged(pp, *args, workspace=ws, out=O)
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            ab.ab_attention_paged(pp, *args, workspace=ws, out=O)
+        graphs.append((gr, O))
+    for _ in range(5):
+        for gr, O in graphs:
+            O.zero_()
+            gr.replay()
+    for (gr, O), (pp, c, q, args) in zip(graphs, cases):
+        _check_attention(O.cpu(), q, c)
+        # other lengths in the same graph
+        args[4].clamp_(max=1)
+        gr.replay()
+        torch.cuda.synchronize()
+        short = ref.Cache.__new__(ref.Cache)
+        short.__dict__.update(c.__dict__)
+        short.lens = [min(n, 1) for n in c.lens]
+        short.keys = [k[:1] for k in c.keys]
+        short.values = [v[:1] for v in c.values]
+        _check_attention(O.cpu(), q, short)

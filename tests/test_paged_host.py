@@ -47,6 +47,7 @@ def test_parameters(lib, field, value, status):
 
 def test_too_many_rows(lib):
     assert _size(lib, replace(PP, S=8192, Hq=9, Hkv=9))[0] == 2
+    assert _size(lib, replace(PP, S=1, Hq=65536, Hkv=65536, max_pages=1))[0] == 2
     assert _size(lib, replace(PP, S=8192, Hq=8, Hkv=8, max_pages=4))[0] == 0
     assert _size(lib, replace(PP, S=8192, Hq=8, Hkv=8, max_pages=2 ** 15))[0] == 2   # 2^35 keys of all heads
 

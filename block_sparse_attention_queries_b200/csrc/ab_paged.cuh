@@ -225,6 +225,23 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     return at >= F0 ? given_back(at - F0) : a.free_pages[at];
   };
   const int64_t gtid = int64_t(blockIdx.x) * kPlanThreads + tid, gstep = int64_t(kPlanCtas) * kPlanThreads;
+  // The table rows written below (served sequences, entries from their old
+  // number of pages on) are read nowhere, the list entries written (from F0 on)
+  // neither.  What a thread reads first for each list is under way before it
+  // writes anything.
+  struct Entry {
+    int64_t at;
+    int page;
+  };
+  auto new_entry = [&](int64_t i) -> Entry {
+    const int s = find(cu_need, int(i));
+    const int old = (old_len[s] + a.page - 1) >> a.page_shift;
+    return {int64_t(s) * a.max_pages + old + (int(i) - cu_need[s]), handed_out(int(i))};
+  };
+  Entry entry0{0, 0};
+  int back0 = 0;
+  if (gtid < n_need) entry0 = new_entry(gtid);
+  if (gtid < n_rel) back0 = given_back(int(gtid));
   constexpr int kBatch = 4;  // tokens a thread looks up at once
   for (int64_t t0 = gtid; t0 < a.T; t0 += kBatch * gstep) {
     int pos[kBatch], id[kBatch];
@@ -252,15 +269,11 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       a.positions[tk] = pos[k];
     }
   }
-  // The table rows written here (served sequences, entries from their old
-  // number of pages on) are never read above, the list entries written here
-  // (from F0 on) neither.
   for (int64_t i = gtid; i < n_need; i += gstep) {
-    const int s = find(cu_need, int(i));
-    const int old = (old_len[s] + a.page - 1) >> a.page_shift;
-    a.table[int64_t(s) * a.max_pages + old + (int(i) - cu_need[s])] = handed_out(int(i));
+    const Entry e = i == gtid ? entry0 : new_entry(i);
+    a.table[e.at] = e.page;
   }
-  for (int64_t i = gtid; i < n_rel; i += gstep) a.free_pages[F0 + i] = given_back(int(i));
+  for (int64_t i = gtid; i < n_rel; i += gstep) a.free_pages[F0 + i] = i == gtid ? back0 : given_back(int(i));
 
   // every CTA has read lens and free_count
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
@@ -750,7 +763,11 @@ __global__ void __launch_bounds__(kNormThreads) page_mass_kernel(const __grid_co
 // select over digits of 11, 11 and 9 bits (the first holds exponent and three
 // bits of the fraction, so that the counters of a row's few octaves do not
 // collide), then every thread writes the kept pages of its own run of the row.
-// Bound by the latency of its steps.
+// Rows of at most 256 pages count instead how many keys come before each.
+// Bound by the latency of the steps: 256 threads for tables of up to 2560 pages
+// (2047 pages in 320 rows: 8.6 us, with 512 threads 10.8), 512 up to 8192 (4096
+// pages in 512 rows: 14.7 us, 17.8 with 256), else 1024 (one row of 20000 pages:
+// 13.8 us, 18.4 with 512).
 struct TopkArgs {
   const float* P;
   const int32_t* lens;
@@ -759,7 +776,7 @@ struct TopkArgs {
   int cap;  // keys that fit in shared memory (longer rows are read anew in each step)
   double keep;
 };
-constexpr int kTopkThreads = 512;
+constexpr int kTopkCount = 256;      // pages of a row that is counted
 constexpr int kTopkMaxKeys = 24576;  // 96 KB: two CTAs an SM
 constexpr int kTopkBins = 2048;
 
@@ -768,8 +785,10 @@ __device__ __forceinline__ int page_budget(int n, double keep) {
   return kb < 1.0 ? min(1, n) : kb > double(n) ? n : int(kb);
 }
 
+template <int kTopkThreads>
 __global__ void __launch_bounds__(kTopkThreads) page_topk_kernel(const __grid_constant__ TopkArgs a) {
-  extern __shared__ uint32_t topk_keys[];
+  extern __shared__ uint4 topk_smem[];
+  uint32_t* const topk_keys = reinterpret_cast<uint32_t*>(topk_smem);
   __shared__ uint32_t hist[kTopkBins];
   __shared__ uint32_t sel[2];
   __shared__ uint32_t wsum[2][kTopkThreads / 32];
@@ -790,6 +809,32 @@ __global__ void __launch_bounds__(kTopkThreads) page_topk_kernel(const __grid_co
   auto make_key = [&](int j, float p) -> uint32_t {
     return j >= newest ? 0x7FFFFFFFu : p > 0.f ? __float_as_uint(p) : 0u;
   };
+  int32_t* out = a.idx + int64_t(row) * a.max_pages;
+  if (n <= kTopkCount) {
+    static_assert(kTopkCount <= kTopkThreads, "a thread per page");
+    const int j = tid;
+    const uint32_t mine = j < n ? make_key(j, __ldg(P + j)) : 0u;
+    if (j < kTopkCount) topk_keys[j] = mine;  // 0 behind the row: it comes before nothing
+    __syncthreads();
+    // keys before this one: larger, or equal and of a lower page
+    int rank = 0;
+    if (warp * 32 < n) {
+      const int below = j >> 2;  // groups of four pages below this one's group
+      for (int i = 0; i < (n + 3) >> 2; ++i) {
+        const uint4 k = topk_smem[i];
+        const uint32_t least = mine + (i < below ? 0u : 1u);
+        rank += int(k.x >= least) + int(k.y >= least) + int(k.z >= least) + int(k.w >= least);
+      }
+      for (int i = j & ~3; i < j; ++i) rank += int(topk_keys[i] == mine);
+    }
+    const bool kept = j < n && rank < Kb;
+    const uint32_t some = __ballot_sync(0xffffffffu, kept);
+    if (lane == 0) wsum[0][warp] = uint32_t(__popc(some));
+    __syncthreads();
+    const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[0][lane] : 0u);
+    if (kept) out[before + __popc(some & ((1u << lane) - 1u))] = j;
+    return;
+  }
   const bool cached = n <= a.cap;
   if (cached) {
     for (int j0 = tid; j0 < n; j0 += 4 * kTopkThreads) {
@@ -818,7 +863,7 @@ __global__ void __launch_bounds__(kTopkThreads) page_topk_kernel(const __grid_co
       wsum[1][warp] = y;
     }
     __syncthreads();
-    uint32_t p = lane < warp ? wsum[0][lane & 15] : 0u, q = lane < warp ? wsum[1][lane & 15] : 0u;
+    uint32_t p = lane < warp ? wsum[0][lane] : 0u, q = lane < warp ? wsum[1][lane] : 0u;
     p = __reduce_add_sync(0xffffffffu, p);
     q = __reduce_add_sync(0xffffffffu, q);
     x += p - x0;  // exclusive
@@ -870,7 +915,6 @@ __global__ void __launch_bounds__(kTopkThreads) page_topk_kernel(const __grid_co
     n_eq += k == prefix ? 1u : 0u;
   }
   block_scan(n_gt, n_eq);
-  int32_t* out = a.idx + int64_t(row) * a.max_pages;
   for (int j = first; j < last; ++j) {
     const uint32_t k = key_of(j);
     const bool gt = k > prefix, eq = k == prefix;

@@ -350,9 +350,13 @@ ab_status run_paged_topk(const ab_paged_params* p, const float* P, const int32_t
   a.Hkv = p->Hkv; a.page = p->page; a.page_shift = log2_of(p->page); a.max_pages = p->max_pages;
   a.recent = p->recent; a.keep = double(p->keep_ratio);
   a.cap = p->max_pages < kTopkMaxKeys ? p->max_pages : kTopkMaxKeys;
-  const int smem = a.cap * 4;
-  if (smem > 36 * 1024 && set_smem(page_topk_kernel, smem) != cudaSuccess) return AB_ERR_CUDA;
-  return launch_after(page_topk_kernel, dim3(unsigned(p->S * p->Hkv)), kTopkThreads, smem, st, a);
+  const int smem = (a.cap > kTopkCount ? a.cap : kTopkCount) * 4;
+  auto go = [&](auto kern, int threads) -> ab_status {
+    if (smem > 36 * 1024 && set_smem(kern, smem) != cudaSuccess) return AB_ERR_CUDA;
+    return launch_after(kern, dim3(unsigned(p->S * p->Hkv)), threads, smem, st, a);
+  };
+  if (p->max_pages <= 2560) return go(page_topk_kernel<256>, 256);
+  return p->max_pages <= 8192 ? go(page_topk_kernel<512>, 512) : go(page_topk_kernel<1024>, 1024);
 }
 
 template <int D, bool kLists>

@@ -246,6 +246,22 @@ def test_topk(dev, keep, recent):
             assert (idx[s, h, len(want):] == -4).all()
 
 
+@pytest.mark.parametrize("most", [300, 2000, 6000, 9000])
+def test_topk_widths(dev, most):
+    # tables of several widths, rows around the lengths where the method changes
+    g = torch.Generator().manual_seed(most)
+    pages = sorted({1, 3, 31, 32, 33, 255, 256, 257, most - 1, most} & set(range(most + 1)))
+    P = torch.rand(len(pages), 2, most, generator=g)
+    P[:, 1] = (P[:, 1] * 5).floor() / 5
+    for keep, recent in ((0.07, 0), (0.5, 2)):
+        pp = ab.PagedParams(len(pages), 2, 2, 64, 16, 4, most, keep_ratio=keep, recent=recent)
+        idx, count = ab.ab_paged_topk(pp, P.to(dev), ints([n * 16 for n in pages], dev))
+        for s, n in enumerate(pages):
+            for h in range(2):
+                want = ref.topk(P[s, h], n, keep, recent)
+                assert count[s, h] == len(want) and idx[s, h, :len(want)].tolist() == want
+
+
 def test_topk_rows_beyond_shared_memory(dev):
     n, most = 24577, 30000
     P = torch.rand(2, 1, most, generator=torch.Generator().manual_seed(14))

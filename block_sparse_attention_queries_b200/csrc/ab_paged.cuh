@@ -294,8 +294,15 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 // the page's keys up to that slot.  A warp takes one (page, head), a run of at
 // most 16 KB, eight heads a CTA.  Bound by memory (the page's keys are read
 // once) or, for single tokens, by latency.
+// A load that stays in its place: eight of them are under way at once.
+__device__ __forceinline__ uint4 load_16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     page_sum_kernel(const int32_t* slots, int T, int per_cta, const __nv_bfloat16* K, __nv_bfloat16* ksum, int Hkv,
                     int page_shift, int num_pages) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
@@ -323,7 +330,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int r = r0 + k * kRows + row0;
-        x[k] = r < n ? *reinterpret_cast<const uint4*>(src + int64_t(r) * D) : make_uint4(0u, 0u, 0u, 0u);
+        x[k] = r < n ? load_16(src + int64_t(r) * D) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {

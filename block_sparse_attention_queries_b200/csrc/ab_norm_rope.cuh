@@ -23,6 +23,10 @@
 //  - norm 2: a CTA takes a token of one tensor at a time, tensor after tensor,
 //    so that the weights of its lanes' heads stay in registers; r goes into cos
 //    and sin.
+// Measured on 32760 tokens of 40 heads of 128, q, k and v (2.03 GB): norm 2
+// 351 us (5.8 TB/s), norm 1 355, rotation alone 346; with one CTA a token and
+// nothing copied ahead norm 2 took 473.  Copies of rows to places a sequence apart
+// keep the last tenth of the copy rate away: rotation alone is no faster.
 #pragma once
 
 #include "ab_ptx.cuh"
@@ -83,7 +87,7 @@ __device__ __forceinline__ void square_add(uint32_t v, float& acc) {
 
 constexpr int kRopeThreads = 128;  // of a CTA whose warps take units of their own
 constexpr int kRopeRows = 4;       // head rows a lane takes in a step
-constexpr int kRopeRowsMany = 8;   // and of a CTA per token with many heads
+constexpr int kRopeRowsMany = 8;   // of a CTA per token whose 16 warps would not hold its heads by fours
 constexpr int kRopeStages = 4, kRopeStagesMany = 2;  // steps in flight
 
 // Bytes of shared memory: the pieces, the table rows, and the place per warp.

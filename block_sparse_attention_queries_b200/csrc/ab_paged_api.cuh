@@ -123,7 +123,10 @@ ab_status launch_norm_rope(NormRopeArgs a, int d, const ab_norm_rope* nr, cudaSt
   constexpr int threads = kRopeThreads, warps = threads / 32;
   constexpr int smem = rope_smem_bytes(kRopeRows, kRopeStages, threads);
   const int64_t resident = int64_t(sms) * 5;  // CTAs: 41 KB, 96 registers a thread
-  // a unit takes all heads of its token where that leaves every warp four units, else one step of them
+  // A unit takes all heads of its token where that leaves every warp four units,
+  // else one step of them: 32760 tokens of 40 heads, rotation alone, 346 us
+  // against 376 in single steps; 233 tokens of 32 + 8 + 8 heads with their plan
+  // 12.1 us in single steps against 13.4.
   const bool whole = all >= 4 * resident * warps;
   int64_t units = 0;
   for (int k = 0; k < 3; ++k) {
@@ -305,7 +308,8 @@ ab_status run_append(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T
                      void* ksum, cudaStream_t st) {
   ab_status s = launch_norm_rope(a, p->d, nr, st);
   if (s != AB_OK || !ksum) return s;
-  // a CTA looks at 1 to 32 slots: few where there are few, so that pages spread over the SMs
+  // a CTA looks at 1 to 32 slots: one each up to 1184 (8 CTAs an SM), so that the
+  // pages of single tokens spread over the SMs; 32 are a ballot
   int per_cta = (T + 1183) / 1184;
   per_cta = per_cta > 32 ? 32 : per_cta;
   const dim3 grid(unsigned((T + per_cta - 1) / per_cta), unsigned((p->Hkv + 7) / 8));

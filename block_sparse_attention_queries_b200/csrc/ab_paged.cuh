@@ -766,6 +766,131 @@ __global__ void __launch_bounds__(kNormThreads) page_mass_kernel(const __grid_co
   }
 }
 
+// The whole selection of a row in one launch, for tables of few pages: a CTA
+// takes a (sequence, key/value head), eight warps 32 pages at a time, and the
+// scores stay in shared memory.  Bound by latency (table, then summaries, then
+// the join of the warps): 2.6 us for 3 sequences of 12 heads and 47 pages, 3.5
+// for 8 of 8 heads and 256.
+constexpr int kRowPages = 1024;                      // columns of the table at most
+constexpr int64_t kRowBytes = int64_t(160) << 20;    // of all summaries of a full table
+constexpr int kRowThreads = 256;
+
+template <int D, bool kWide>
+__global__ void __launch_bounds__(kRowThreads) page_row_kernel(const __grid_constant__ SelectArgs a) {
+  constexpr int kPieces = D / 32;
+  constexpr int kHalves = kWide ? 2 : 1;
+  constexpr int kWarps = kRowThreads / 32;
+  extern __shared__ float row_smem[];  // [G][pitch] scores, log2 domain
+  __shared__ float2 wpart[kWarps][kMaxGroup];
+  pdl_wait();
+  pdl_trigger();
+  const PagedView& v = a.v;
+  const int s = blockIdx.x / v.Hkv, hk = blockIdx.x - s * v.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int qrow = query_row(v, s);
+  if (qrow < 0) return;
+  const int len = seq_len(v, s), pages = pages_of(v, len);
+  // queries: rows g (and g + 8) of the 16 x d operand, 16-byte pieces t, t + 4, ...
+  const __nv_bfloat16* q = a.Q + ((int64_t(qrow) * v.Hkv + hk) * v.G + g) * D + t * 8;
+  uint4 qx[kHalves][kPieces];
+#pragma unroll
+  for (int k = 0; k < kHalves; ++k)
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p)
+      qx[k][p] = g + 8 * k < v.G ? __ldg(reinterpret_cast<const uint4*>(q + k * 8 * D + p * 32)) : make_uint4(0u, 0u, 0u, 0u);
+  float m[kHalves], l[kHalves];
+#pragma unroll
+  for (int k = 0; k < kHalves; ++k) {
+    m[k] = -INFINITY;
+    l[k] = 0.f;
+  }
+  const float bias = float(v.page_shift);  // log2 of a whole page's keys
+  const float last_bias = log2f(float(len - ((pages - 1) << v.page_shift)));
+  for (int j0 = warp * 32; j0 < pages; j0 += kWarps * 32) {
+    int id[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      id[n] = j0 + n * 8 + g < pages ? __ldg(v.table + int64_t(s) * v.max_pages + j0 + n * 8 + g) : 0;
+    uint4 kx[4][kPieces];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const bool there = uint32_t(id[n]) < uint32_t(v.num_pages);
+      if (!there) raise_error(AB_ERR_CAPACITY);  // its score is that of a zero summary
+      const __nv_bfloat16* src = a.ksum + (int64_t(id[n]) * v.Hkv + hk) * D + t * 8;
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+        kx[n][p] = there ? __ldg(reinterpret_cast<const uint4*>(src + p * 32)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float x[kHalves][8];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      float c0[4] = {}, c1[4] = {};
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        const uint4 q0 = qx[0][p], q1 = kWide ? qx[kHalves - 1][p] : make_uint4(0u, 0u, 0u, 0u), k = kx[n][p];
+        mma_16816(c0, q0.x, q1.x, q0.y, q1.y, k.x, k.y);
+        mma_16816(c1, q0.z, q1.z, q0.w, q1.w, k.z, k.w);
+      }
+#pragma unroll
+      for (int k = 0; k < kHalves; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = j0 + n * 8 + t * 2 + e;
+          x[k][2 * n + e] = j >= pages ? -INFINITY
+                                       : fmaf(c0[2 * k + e] + c1[2 * k + e], a.scale_log2, j == pages - 1 ? last_bias : bias);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kHalves; ++k) {
+      float mx = m[k];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) mx = fmaxf(mx, x[k][n]);
+      if (mx != -INFINITY) {  // this lane's maximum and sum; a quad's are joined at the end
+        l[k] *= ex2_approx(m[k] - mx);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) l[k] += ex2_approx(x[k][n] - mx);
+        m[k] = mx;
+      }
+      if (g + 8 * k < v.G) {
+        float* dst = row_smem + (g + 8 * k) * a.pitch + j0 + t * 2;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if (j0 + n * 8 + t * 2 < a.pitch) *reinterpret_cast<float2*>(dst + n * 8) = make_float2(x[k][2 * n], x[k][2 * n + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kHalves; ++k) {
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const float om = __shfl_xor_sync(0xffffffffu, m[k], o), ol = __shfl_xor_sync(0xffffffffu, l[k], o);
+      const float mm = fmaxf(m[k], om);
+      if (mm != -INFINITY) l[k] = l[k] * ex2_approx(m[k] - mm) + ol * ex2_approx(om - mm);
+      m[k] = mm;
+    }
+    if (t == 0) wpart[warp][g + 8 * k] = make_float2(m[k], l[k]);
+  }
+  __syncthreads();
+  if (threadIdx.x < v.G) {  // the head's maximum, and 1 / (G sum)
+    float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, wpart[w][threadIdx.x].x);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 z = wpart[w][threadIdx.x];
+      if (z.x != -INFINITY) ll += z.y * exp2f(z.x - mm);
+    }
+    wpart[0][threadIdx.x] = make_float2(mm, 1.f / (ll * float(v.G)));
+  }
+  __syncthreads();
+  float* P = a.P + int64_t(blockIdx.x) * v.max_pages;
+  for (int j = threadIdx.x; j < pages; j += kRowThreads) {
+    float p = 0.f;
+    for (int h = 0; h < v.G; ++h) p += ex2_approx(row_smem[h * a.pitch + j] - wpart[0][h].x) * wpart[0][h].y;
+    P[j] = p;
+  }
+}
+
 // ------------------------------------------------------------------- top-k
 // The newest min(recent, Kb) pages and the Kb minus that many others of
 // largest P, in ascending order; ties go to the lower page.  Keys are P's bits

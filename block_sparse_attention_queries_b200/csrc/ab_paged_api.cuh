@@ -334,6 +334,18 @@ ab_status run_paged_select(const ab_paged_params* p, const PagedView& v, const v
   const int sms = sm_count();
   if (!sms) return AB_ERR_CUDA;
   a.pitch = (p->max_pages + 3) / 4 * 4;
+  // One launch with a CTA per row, for tables of few pages whose summaries fit in
+  // L2: 3 x 12 rows of 47 pages 2.7 us (two launches 5.8), 64 x 8 rows of 256 7.6
+  // (13.3), of 1000 31 (33); but 512 x 40 rows of 256 pages (1.3 GB) 350 (269: there
+  // the warps of a CTA read neighbouring heads together), one row of 1000 7.2 (5.8).
+  const int64_t rows = int64_t(p->S) * p->Hkv, bytes_all = rows * p->max_pages * p->d * 2;
+  if (p->max_pages <= kRowPages && bytes_all <= kRowBytes && (p->max_pages <= 512 || rows >= 64)) {
+    auto row = p->d == 128 ? (v.G > 8 ? page_row_kernel<128, true> : page_row_kernel<128, false>)
+                           : (v.G > 8 ? page_row_kernel<64, true> : page_row_kernel<64, false>);
+    const int bytes = v.G * a.pitch * 4;
+    if (bytes > 46 * 1024 && set_smem(row, bytes) != cudaSuccess) return AB_ERR_CUDA;
+    return launch_after(row, dim3(unsigned(p->S * p->Hkv)), kRowThreads, bytes, st, a);
+  }
   const int64_t most = (int64_t(p->S) * p->Hkv * a.chunks + kSelWarps - 1) / kSelWarps;
   const unsigned grid = unsigned(most < sms ? most : sms);
   const bool wide = v.G > 8;

@@ -203,7 +203,8 @@ def test_append_bad_slots_and_positions(dev):
 
 # ------------------------------------------------------- select and top-k
 @pytest.mark.parametrize("Hq,Hkv,d,page", [(1, 1, 64, 16), (12, 12, 128, 32), (32, 8, 128, 16), (16, 1, 64, 64), (9, 1, 128, 16)])
-@pytest.mark.parametrize("lens", [[1], [16 * 128, 16 * 128 + 1, 0, 5], [40000, 77, 3000]])
+@pytest.mark.parametrize("lens", [[1], [16 * 128, 16 * 128 + 1, 0, 5], [40000, 77, 3000], [700] * 70 + [9000, 13000],
+                                  [0, 20000, 1, 0, 16384, 0]])
 def test_select(dev, Hq, Hkv, d, page, lens):
     g = torch.Generator().manual_seed(11)
     c = ref.Cache(lens, Hkv, d, page, 12)
@@ -415,6 +416,26 @@ def test_bad_entries_are_skipped(dev):
     O = ab.ab_attention_paged(pp, *args, c.table.to(dev), ints(lens, dev), idx=idx.to(dev), count=ints([[-1], [1]], dev))
     assert ab.device_error(dev) == CAPACITY and (O[0] == 0).all()
     _check_attention(O.cpu(), q, c, lists=[[[]], [[0]]])
+
+
+@pytest.mark.parametrize("max_pages", [300, 1500])
+def test_select_bad_entries(dev, max_pages):
+    # an entry out of range has the score of a zero summary; other rows are as they were
+    lens = [4700, 40, 0, 4000]
+    Hq, Hkv, d, page = 6, 2, 64, 16
+    c = ref.Cache(lens, Hkv, d, page, 73, max_pages=max_pages)
+    q = torch.randn(4, Hq, d, generator=torch.Generator().manual_seed(74)).to(BF16)
+    pp = ab.PagedParams(4, Hq, Hkv, d, page, c.num_pages, c.max_pages)
+    ksum = torch.cat([c.ksum, torch.zeros(1, Hkv, d, dtype=BF16)])
+    run = lambda pp, k, t: ab.ab_paged_select(pp, q.to(dev), k.to(dev), t.to(dev), ints(lens, dev),
+                                              out=torch.full((4, Hkv, max_pages), -1.0, device=dev)).cpu()
+    for wrong in (-1, c.num_pages, 2 ** 31 - 1):
+        table, zero = c.table.clone(), c.table.clone()
+        table[0, 5], zero[0, 5] = wrong, c.num_pages
+        got = run(pp, c.ksum, table)
+        assert ab.device_error(dev) == CAPACITY
+        want = run(ab.PagedParams(4, Hq, Hkv, d, page, c.num_pages + 1, c.max_pages), ksum, zero)
+        assert ab.device_error(dev) == 0 and torch.equal(got, want)
 
 
 # -------------------------------------------------------------- together

@@ -293,9 +293,11 @@ ab_status prepare_append(const ab_paged_params* p, const ab_norm_rope* nr, int32
     a->in[x] = view_of(in[x]);
     a->out[x] = static_cast<__nv_bfloat16*>(out[x]);
   }
-  const Span o = span_of(Q, int64_t(T) * p->Hq * p->d);
+  const int64_t cache = int64_t(p->num_pages) * p->Hkv * p->page * p->d;
+  const Span o[3] = {span_of(Q, int64_t(T) * p->Hq * p->d), span_of(Kc, cache), span_of(Vc, cache)};
   for (int x = 0; x < 3; ++x)
-    if (overlap(o, span_of(in[x], 1, T, a->heads[x], p->d))) return AB_ERR_INVALID_ARG;
+    for (const Span& y : o)
+      if (overlap(y, span_of(in[x], 1, T, a->heads[x], p->d))) return AB_ERR_INVALID_ARG;
   a->pos[0] = a->pos[1] = positions;
   a->slots = slots;
   a->page_shift = log2_of(p->page);

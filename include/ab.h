@@ -446,9 +446,9 @@ ab_status ab_paged_plan(const ab_paged_params* p, int32_t T, const int32_t* n_ne
 /*
  * Norm and rotation of T new tokens (T = 0: nothing is done), written into the cache: Q [T, Hq, d]
  * receives the queries, the tokens' slots of K and V receive keys and values.
- * q has Hq heads, k and v have Hkv (the batch strides are not used); Q must not
- * overlap them.  A token
- * with a negative slot is skipped (its row of Q is left as it was).
+ * q has Hq heads, k and v have Hkv (the batch strides are not used).  A Q or a
+ * cache that overlaps them is refused.  A token with a negative slot is skipped
+ * (its row of Q is left as it was).
  *   slots, positions  device, int32 [T], as ab_paged_plan writes them.  Slots
  *                     must be distinct: of two tokens with one slot either may
  *                     remain, in parts.

@@ -167,6 +167,19 @@ def test_append_and_forward(lib):
     assert forward(T=0) == 1 and forward(ws=16) == 6
 
 
+def test_append_refuses_tokens_inside_the_cache(lib):
+    # the cache has 100 * 2 * 16 * 128 values of 2 bytes, a step of 5 tokens 5 * 8 * 128 of queries
+    size = 100 * 2 * 16 * 128 * 2
+    at = [0x100000000 + k * 0x1000000 for k in range(6)]          # slots, positions, Q, K, V, ksum
+    apart = ab.ab_tokens(IN, 0, 8 * 128, 128)
+    for out, n in ((2, 5 * 8 * 128 * 2), (3, size), (4, size)):
+        for where in (at[out], at[out] + n - 16):
+            for k in range(3):
+                inside = ab.ab_tokens(where, 0, 8 * 128, 128)
+                tok = [inside if j == k else apart for j in range(3)]
+                assert lib.ab_paged_append(PP.c(), _nr(), 5, *tok, *at, None) == 1
+
+
 def test_forward_qkv(lib):
     p = ab.Params(B=1, H=2, L=256, d=64, q_block=64, kv_block=16, C=4).c()
     t = ab.ab_tokens(IN, 0, 128, 64)

@@ -729,18 +729,17 @@ __global__ void __launch_bounds__(kNormThreads) page_mass_kernel(const __grid_co
 #pragma unroll
       for (int k = 0; k < 4; ++k) z[k] = k0 + 32 * k < chunks ? part[k0 + 32 * k] : make_float2(-INFINITY, 0.f);
       const float mm = fmaxf(fmaxf(fmaxf(z[0].x, z[1].x), fmaxf(z[2].x, z[3].x)), m);
-      if (mm != -INFINITY) {
-        l *= exp2f(m - mm);
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      l *= exp2f(m - ref);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) l += z[k].y * exp2f(z[k].x - mm);
-        m = mm;
-      }
+      for (int k = 0; k < 4; ++k) l += z[k].y * exp2f(z[k].x - ref);
+      m = mm;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const float om = __shfl_xor_sync(0xffffffffu, m, o), ol = __shfl_xor_sync(0xffffffffu, l, o);
-      const float mm = fmaxf(m, om);
-      if (mm != -INFINITY) l = l * exp2f(m - mm) + ol * exp2f(om - mm);
+      const float mm = fmaxf(m, om), ref = mm == -INFINITY ? 0.f : mm;
+      l = l * exp2f(m - ref) + ol * exp2f(om - ref);
       m = mm;
     }
     if (lane == 0) ml[h] = make_float2(m, 1.f / (l * float(v.G)));
@@ -845,12 +844,12 @@ __global__ void __launch_bounds__(kRowThreads) page_row_kernel(const __grid_cons
       float mx = m[k];
 #pragma unroll
       for (int n = 0; n < 8; ++n) mx = fmaxf(mx, x[k][n]);
-      if (mx != -INFINITY) {  // this lane's maximum and sum; a quad's are joined at the end
-        l[k] *= ex2_approx(m[k] - mx);
+      // this lane's maximum and sum; a quad's are joined at the end
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      l[k] *= ex2_approx(m[k] - ref);
 #pragma unroll
-        for (int n = 0; n < 8; ++n) l[k] += ex2_approx(x[k][n] - mx);
-        m[k] = mx;
-      }
+      for (int n = 0; n < 8; ++n) l[k] += ex2_approx(x[k][n] - ref);
+      m[k] = mx;
       if (g + 8 * k < v.G) {
         float* dst = row_smem + (g + 8 * k) * a.pitch + j0 + t * 2;
 #pragma unroll
@@ -864,8 +863,8 @@ __global__ void __launch_bounds__(kRowThreads) page_row_kernel(const __grid_cons
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       const float om = __shfl_xor_sync(0xffffffffu, m[k], o), ol = __shfl_xor_sync(0xffffffffu, l[k], o);
-      const float mm = fmaxf(m[k], om);
-      if (mm != -INFINITY) l[k] = l[k] * ex2_approx(m[k] - mm) + ol * ex2_approx(om - mm);
+      const float mm = fmaxf(m[k], om), ref = mm == -INFINITY ? 0.f : mm;
+      l[k] = l[k] * ex2_approx(m[k] - ref) + ol * ex2_approx(om - ref);
       m[k] = mm;
     }
     if (t == 0) wpart[warp][g + 8 * k] = make_float2(m[k], l[k]);
@@ -878,7 +877,7 @@ __global__ void __launch_bounds__(kRowThreads) page_row_kernel(const __grid_cons
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float2 z = wpart[w][threadIdx.x];
-      if (z.x != -INFINITY) ll += z.y * exp2f(z.x - mm);
+      ll += z.y * exp2f(z.x - (mm == -INFINITY ? 0.f : mm));
     }
     wpart[0][threadIdx.x] = make_float2(mm, 1.f / (ll * float(v.G)));
   }

@@ -218,7 +218,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
     constexpr int kMaxPages = SM::kTile / 16;
     const int per_tile = SM::kTile >> v.page_shift;  // pages of a tile
     DecMeta meta{sh.begin, sh.n, -1, 0, 0, {0, 0, 0}};
-    if (sh.n == 0 && lane == 0) a.meta[blockIdx.x] = meta;
+    if (lane == 0) a.meta[blockIdx.x] = meta;  // what the joining kernel finds if a wait below gives up
+    __syncwarp();
     int unit = sh.unit, pos = sh.off;  // tile `base` of the share is tile `pos` from the start of unit `unit` on
     int rows = 0;  // rows begun
     bool ok = true;
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
           s4.w += ow.w * f;
         }
         if (whole) {
-          const float inv = ll > 0.f ? 1.f / ll : 0.f;
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;  // NaN stays NaN
           *reinterpret_cast<uint2*>(a.O + (row * v.G + head0 + head) * D + i) =
               make_uint2(pack_bf16x2(s4.x * inv, s4.y * inv), pack_bf16x2(s4.z * inv, s4.w * inv));
         } else {
@@ -617,14 +618,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
       x[i] = y.x;
       x[i + 1] = y.y;
     }
-    const float mm = fmaxf(m, z.x);
-    if (mm != -INFINITY) {
-      const float fa = ex2_approx(m - mm), fb = ex2_approx(z.x - mm);
-      l = l * fa + z.y * fb;
+    const float mm = fmaxf(m, z.x), ref = mm == -INFINITY ? 0.f : mm;
+    const float fa = ex2_approx(m - ref), fb = ex2_approx(z.x - ref);
+    l = l * fa + z.y * fb;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) o[i] = o[i] * fa + x[i] * fb;
-      m = mm;
-    }
+    for (int i = 0; i < kVec; ++i) o[i] = o[i] * fa + x[i] * fb;
+    m = mm;
   }
 #pragma unroll
   for (int i = 0; i < kVec; ++i) so[warp][lane * kVec + i] = o[i];
@@ -634,16 +633,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
   float mm = -INFINITY;
 #pragma unroll
   for (int k = 0; k < kJoinWarps; ++k) mm = fmaxf(mm, sml[k].x);
+  const float ref = mm == -INFINITY ? 0.f : mm;
   float ll = 0.f, oo = 0.f;
-  if (mm != -INFINITY) {
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) {
-      const float f = ex2_approx(sml[k].x - mm);
-      ll += sml[k].y * f;
-      oo += so[k][threadIdx.x] * f;
-    }
+  for (int k = 0; k < kJoinWarps; ++k) {
+    const float f = ex2_approx(sml[k].x - ref);
+    ll += sml[k].y * f;
+    oo += so[k][threadIdx.x] * f;
   }
-  a.O[(int64_t(mt.row) * a.v.G + h) * D + threadIdx.x] = __float2bfloat16(ll > 0.f ? oo / ll : 0.f);
+  a.O[(int64_t(mt.row) * a.v.G + h) * D + threadIdx.x] = __float2bfloat16(ll == 0.f ? 0.f : oo / ll);
 }
 
 }  // namespace ab

@@ -389,6 +389,57 @@ def test_attention_extreme_scores(dev):
     _check_attention(O.cpu(), q, c)
 
 
+@pytest.mark.parametrize("lists", [False, True])
+def test_not_a_number_shows(dev, lists):
+    # NaN in a valid key or a query reaches the heads that read it, in rows of one CTA and of many
+    lens = [40000, 20, 300]
+    Hq, Hkv, d, page = 6, 2, 128, 16
+    c = ref.Cache(lens, Hkv, d, page, 75)
+    q = torch.randn(3, Hq, d, generator=torch.Generator().manual_seed(76)).to(BF16)
+    pp = ab.PagedParams(3, Hq, Hkv, d, page, c.num_pages, c.max_pages)
+    more = {}
+    if lists:
+        idx = torch.arange(c.max_pages, dtype=I32).expand(3, Hkv, -1).contiguous()
+        count = torch.tensor([[ref.cdiv(n, page)] * Hkv for n in lens], dtype=I32)
+        more = dict(idx=idx.to(dev), count=count.to(dev))
+    run = lambda q, K: ab.ab_attention_paged(pp, q.to(dev), K.to(dev), c.V.to(dev), c.table.to(dev), ints(lens, dev), **more).cpu()
+    good = run(q, c.K)
+    for s in range(3):
+        K = c.K.clone()
+        K[c.table[s, lens[s] // page // 2], 1, 3, 5] = float("nan")
+        bad = run(q, K)
+        assert torch.isnan(bad[s, 3:]).all()
+        bad[s, 3:] = good[s, 3:]
+        assert torch.equal(bad, good)
+        q2 = q.clone()
+        q2[s, 4, 9] = float("nan")
+        bad = run(q2, c.K)
+        assert torch.isnan(bad[s, 4]).all()
+        bad[s, 4] = good[s, 4]
+        assert torch.equal(bad, good)
+
+
+@pytest.mark.parametrize("max_pages", [300, 1500])
+def test_select_not_a_number_shows(dev, max_pages):
+    lens = [4700, 40, 4000]
+    Hq, Hkv, d, page = 6, 2, 64, 16
+    c = ref.Cache(lens, Hkv, d, page, 77, max_pages=max_pages)
+    q = torch.randn(3, Hq, d, generator=torch.Generator().manual_seed(78)).to(BF16)
+    pp = ab.PagedParams(3, Hq, Hkv, d, page, c.num_pages, c.max_pages)
+    run = lambda q, k: ab.ab_paged_select(pp, q.to(dev), k.to(dev), c.table.to(dev), ints(lens, dev),
+                                          out=torch.full((3, Hkv, max_pages), -1.0, device=dev)).cpu()
+    good = run(q, c.ksum)
+    for s, n in enumerate(lens):
+        k = ref.cdiv(n, page)
+        q2, ksum = q.clone(), c.ksum.clone()
+        q2[s, 4, 9] = float("nan")
+        ksum[c.table[s, k // 2], 1, 60] = float("nan")
+        for bad in (run(q2, c.ksum), run(q, ksum)):
+            assert torch.isnan(bad[s, 1, :k]).all()
+            bad[s, 1, :k] = good[s, 1, :k]
+            assert torch.equal(bad, good)
+
+
 def test_bad_entries_are_skipped(dev):
     # table and list entries, counts and lengths out of range: reported, left out
     lens = [100, 40]
@@ -622,3 +673,49 @@ def test_two_graphs_share_a_workspace(dev):
         short.keys = [k[:1] for k in c.keys]
         short.values = [v[:1] for v in c.values]
         _check_attention(O.cpu(), q, short)
+
+
+def test_captured_between_copies_and_streams(dev):
+    # a graph with fills and copies before the calls, and two branches that meet again
+    lens = [3000, 50, 0, 700]
+    c = ref.Cache(lens, 2, 64, 16, 120)
+    q = torch.randn(4, 6, 64, generator=torch.Generator().manual_seed(121)).to(BF16)
+    pp = ab.PagedParams(4, 6, 2, 64, 16, c.num_pages, c.max_pages, keep_ratio=0.3, recent=1)
+    K, V, ksum, table = (t.to(dev) for t in (c.K, c.V, c.ksum, c.table))
+    source = q.to(dev)
+    Q, n = torch.zeros_like(source), torch.zeros(4, dtype=I32, device=dev)
+    lens_in = ints(lens, dev)
+    P = torch.zeros(4, 2, c.max_pages, device=dev)
+    lists = torch.zeros(4, 2, c.max_pages, dtype=I32, device=dev), torch.zeros(4, 2, dtype=I32, device=dev)
+    all_O, some_O = torch.zeros_like(source), torch.zeros_like(source)
+    ws = [ab.alloc_paged_workspace(pp, dev) for _ in range(2)]
+    side = torch.cuda.Stream(dev)
+
+    def step():
+        here = torch.cuda.current_stream(dev)
+        Q.copy_(source)
+        n.copy_(lens_in)
+        P.zero_()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            ab.ab_attention_paged(pp, Q, K, V, table, n, workspace=ws[1], out=all_O)
+        ab.ab_paged_select(pp, Q, ksum, table, n, out=P, workspace=ws[0])
+        ab.ab_paged_topk(pp, P, n, out=lists)
+        ab.ab_attention_paged(pp, Q, K, V, table, n, idx=lists[0], count=lists[1], workspace=ws[0], out=some_O)
+        here.wait_stream(side)
+        all_O.add_(some_O)
+        n.zero_()
+
+    step()
+    torch.cuda.synchronize()
+    want = all_O.clone(), some_O.clone()
+    assert all(torch.isfinite(w).all() and (w[0] != 0).any() for w in want)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        step()
+    for _ in range(3):
+        for t in (all_O, some_O, Q, P):
+            t.fill_(-3)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(all_O, want[0]) and torch.equal(some_O, want[1])

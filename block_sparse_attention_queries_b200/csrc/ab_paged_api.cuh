@@ -44,6 +44,7 @@ ab_status launch_after(void (*kern)(Params...), dim3 grid, int threads, int smem
 }
 
 // ------------------------------------------------------ norm and rotation
+constexpr int64_t kRopeSplit = 4096;                 // tokens of q, k and v together
 constexpr int64_t kRopeMaxUnits = int64_t(1) << 29;  // positions in the list of units stay in 32 bits
 
 ab_status check_norm_rope(const ab_norm_rope* nr) {
@@ -104,6 +105,18 @@ ab_status launch_norm_rope(NormRopeArgs a, int d, const ab_norm_rope* nr, cudaSt
     const bool many = heads > 16 * rows * kRopeRows;
     const int nv = many ? kRopeRowsMany : kRopeRows, stages = many ? kRopeStagesMany : kRopeStages;
     const int threads = 32 * ((heads + rows * nv - 1) / (rows * nv));
+    // Keys that need less than half the queries' warps: launches of their own, with
+    // as many warps as each needs (44 thousand tokens of 32 + 8 + 8 heads, with
+    // their page means, 240 us against 315 in one launch, of 40 + 4 + 4 241 against
+    // 373, 1500 of 32 + 8 + 8 13.5 against 15.6; but 600 10.2 against 8.7, and of
+    // 16 + 8 + 8 heads 44 thousand 178 against 180, 1500 11.7 against 10.6).
+    const int warps_kv = (a.heads[1] + rows * nv - 1) / (rows * nv);
+    if (a.tokens[0] && all > a.tokens[0] && 64 * warps_kv < threads && all >= kRopeSplit) {
+      NormRopeArgs q = a, kv = a;
+      q.tokens[1] = q.tokens[2] = kv.tokens[0] = 0;
+      const ab_status s = launch_norm_rope(q, d, nr, st);
+      return s == AB_OK ? launch_norm_rope(kv, d, nr, st) : s;
+    }
     const int smem = rope_smem_bytes(nv, stages, threads);
     // resident CTAs: as many as shared memory and the registers (96 a thread) allow
     int per_sm = 640 / threads;

@@ -185,6 +185,32 @@ def test_append(dev, Hq, Hkv, d, page, norm, interleaved):
             assert torch.equal(sc[p].view(torch.int16), c.ksum[p].view(torch.int16))
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", [(32, 8, 128), (40, 4, 128), (72, 9, 64), (160, 10, 128)])
+def test_append_many_tokens_of_few_key_heads(dev, Hq, Hkv, d):
+    g = torch.Generator().manual_seed(7)
+    page, T = 16, 1500
+    (wq, wk, cos, sin), nr = _rope("token", Hq, Hkv, d, T, True, 8, dev)
+    num_pages = ref.cdiv(T, page) + 1
+    pp = ab.PagedParams(1, Hq, Hkv, d, page, num_pages, num_pages)
+    x = torch.randn(T, Hq + 2 * Hkv, d, generator=g).to(BF16)
+    xd, at = x.to(dev), torch.arange(T)
+    slots = at + page
+    slots[700] = -1                                              # a token that is skipped
+    K, V = (torch.zeros(num_pages, Hkv, page, d, dtype=BF16, device=dev) for _ in range(2))
+    Q = ab.ab_paged_append(pp, nr, xd[:, :Hq], xd[:, Hq:Hq + Hkv], xd[:, Hq + Hkv:], ints(slots.tolist(), dev), ints(at.tolist(), dev),
+                           K, V, out=torch.full((T, Hq, d), 7.0, dtype=BF16, device=dev)).cpu()
+    assert (Q[700] == 7.0).all()
+    kept = at != 700
+    q, size = ref.norm_rotate(x[:, :Hq], "token", wq, cos, sin, at, True, 1e-6)
+    ref.assert_norm_rotate(Q[kept], q[kept], size[kept], "token", Hq * d)
+    k, size = ref.norm_rotate(x[:, Hq:Hq + Hkv], "token", wk, cos, sin, at, True, 1e-6)
+    sl = slots[kept]
+    ref.assert_norm_rotate(K.cpu()[sl // page, :, sl % page], k[kept], size[kept], "token", Hkv * d)
+    assert torch.equal(V.cpu()[sl // page, :, sl % page], x[kept, Hq + Hkv:])
+    left = 700 + page
+    assert (K[left // page, :, left % page] == 0).all() and (V[left // page, :, left % page] == 0).all()
+
+
 def test_append_bad_slots_and_positions(dev):
     # reported, and nothing is written for them
     _, nr = _rope("head", 2, 2, 64, 10, True, 1, dev)

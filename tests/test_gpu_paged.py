@@ -289,6 +289,27 @@ def test_topk_widths(dev, most):
                 assert count[s, h] == len(want) and idx[s, h, :len(want)].tolist() == want
 
 
+@pytest.mark.parametrize("same", [1, 2, 255, 256, 257, 700])
+@pytest.mark.parametrize("levels", [1, 3, 10 ** 6])
+def test_topk_close_values(dev, same, levels):
+    # `same` values of one octave's eighth, of `levels` different values, around the last that is kept
+    g = torch.Generator().manual_seed(same + levels)
+    n, Hkv = 1000, 8
+    P = torch.zeros(1, Hkv, n + 3)
+    for h in range(Hkv):
+        x = torch.rand(n, generator=g) * 0.1
+        x[:150] = 0.6 + 0.3 * torch.rand(150, generator=g)
+        x[150:150 + same] = 0.25 * (1 + (torch.rand(same, generator=g) * levels).floor() / levels * 0.124)
+        P[0, h, :n] = x[torch.randperm(n, generator=g)]
+    for kept in (149, 150, 151, 150 + same // 2, 150 + same, min(n, 151 + same)):
+        pp = ab.PagedParams(1, Hkv, Hkv, 64, 16, 4, n + 3, keep_ratio=kept / n, recent=0)
+        idx, count = ab.ab_paged_topk(pp, P.to(dev), ints([n * 16], dev))
+        for h in range(Hkv):
+            want = ref.topk(P[0, h], n, kept / n, 0)
+            assert len(want) == kept
+            assert count[0, h] == len(want) and idx[0, h, :len(want)].tolist() == want
+
+
 def test_topk_rows_beyond_shared_memory(dev):
     n, most = 24577, 30000
     P = torch.rand(2, 1, most, generator=torch.Generator().manual_seed(14))

@@ -509,7 +509,7 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 // sequences of 62 thousand tokens, 8 key heads of 4: 73 us for 401 MB (5.5 TB/s),
 // and 8 us for the normalisation.
 constexpr int kSelPages = 32;
-constexpr int kSelWarps = 8;
+constexpr int kSelWarps = 8;  // 9 to 14: the same time, with 32 key heads 437 us against 266
 __host__ __device__ constexpr int sel_stages(int D) { return D == 128 ? 3 : 6; }
 
 struct SelectArgs {

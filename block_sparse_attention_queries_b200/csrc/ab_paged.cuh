@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(256, 4)
 // row costs two for each tile and `row_cost` besides; CTA c of C takes the tiles
 // between c / C and (c + 1) / C of the whole cost, whatever the units' lengths,
 // so the load is even without the host knowing any length.  Every CTA sums the
-// units itself.
+// units itself.  With `whole` a row belongs to the CTA in whose share it begins.
 struct UnitWork {
   int rows, tiles;  // tiles of each row
 };
@@ -388,7 +388,7 @@ constexpr int kShareSums = kShareMaxUnits / 32;  // pairs of sums over 32 units 
 
 // Sums stay below 2^31: the host limits the tiles of a full table to 2^29.
 template <typename F>
-__device__ __forceinline__ Share share_work(F work, int row_cost, int n_units, int c, int C, int2* sums) {
+__device__ __forceinline__ Share share_work(F work, int row_cost, bool whole, int n_units, int c, int C, int2* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int chunks = (n_units + 31) / 32;
   auto unit_work = [&](int u) { return u < n_units ? work(u) : UnitWork{0, 0}; };
@@ -457,7 +457,7 @@ __device__ __forceinline__ Share share_work(F work, int row_cost, int n_units, i
     const int T = __shfl_sync(0xffffffffu, w[z].tiles, l), row_total = 2 * T + row_cost;
     const int row = row_total > 0 ? rest / row_total : 0, x = rest - row * row_total;
     unit[z] = chunk[z] * 32 + l;
-    off[z] = row * T + min((x + 1) / 2, T);
+    off[z] = row * T + (whole ? (x > 0 ? T : 0) : min((x + 1) / 2, T));
     at[z] = before[z] + __shfl_sync(0xffffffffu, incl_tiles - tiles, l) + off[z];
     if (p[z] >= total) {
       unit[z] = n_units;
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 1) page_score_kernel(const __g
     return query_row(v, s) < 0 ? 0 : (pages_of(v, seq_len(v, s)) + kSelPages - 1) / kSelPages;
   };
   auto work = [&](int s) { return UnitWork{v.Hkv, chunks_of(s)}; };
-  const Share sh = share_work(work, 0, v.S, blockIdx.x, gridDim.x, sums);
+  const Share sh = share_work(work, 0, false, v.S, blockIdx.x, gridDim.x, sums);
   uint4* const mine = sel_smem + size_t(warp) * kStages * 4 * kPieces * 32 + lane;
   const int n_steps = (sh.n - warp + kSelWarps - 1) / kSelWarps;  // this warp's: every 8th of the CTA's
   if (n_steps <= 0) return;

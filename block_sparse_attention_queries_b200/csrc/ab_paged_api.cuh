@@ -396,7 +396,7 @@ ab_status launch_paged_attention(const DecArgs& a, int grid, cudaStream_t st) {
   constexpr int smem = DecSmem<D>::kAlloc;
   if (set_smem(kern, smem) != cudaSuccess) return AB_ERR_CUDA;
   if (launch_after(kern, dim3(unsigned(grid)), kDecThreads, smem, st, a) != AB_OK) return AB_ERR_CUDA;
-  if (grid == 1) return AB_OK;
+  if (grid == 1 || a.whole) return AB_OK;
   return launch_after(paged_join_kernel<D>, dim3(unsigned(grid - 1), unsigned(a.v.G)), 32 * kJoinWarps, 0, st, a, grid,
                       a.v.G > 8 ? 16 : 8);
 }
@@ -420,6 +420,7 @@ ab_status run_paged_attention(const ab_paged_params* p, const PagedView& v, cons
   a.part_o = reinterpret_cast<float*>(ws + w.off_part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + w.off_ml);
   const int grid = sms < kDecMaxParts ? sms : kDecMaxParts;
+  a.whole = (int64_t(p->max_pages) * p->page + dec_tile(p->d) - 1) / dec_tile(p->d) <= kWholeTiles;
   if (p->d == 128)
     return idx ? launch_paged_attention<128, true>(a, grid, st) : launch_paged_attention<128, false>(a, grid, st);
   return idx ? launch_paged_attention<64, true>(a, grid, st) : launch_paged_attention<64, false>(a, grid, st);

@@ -13,7 +13,7 @@
 //    d = 64) and the whole list of tiles is divided evenly among persistent
 //    CTAs, whatever the lengths (share_work; a row's start and end count as half
 //    a tile); a row that several CTAs share is joined from their partial results
-//    by a second kernel;
+//    by a second kernel (short tables: rows stay whole);
 //  - one warp plans 32 tiles at a time, a lane for each: the tile's row, its
 //    pages through the lists and the block table.  All lookups of 32 tiles run
 //    side by side, so that rows of a single tile cost no more than long ones;
@@ -60,6 +60,10 @@ __host__ __device__ constexpr int dec_tile(int D) { return D == 128 ? 64 : 128; 
 // A row's start and end, in halves of a tile: 64 sequences of 1 to 16384 keys 72.6
 // us, 79.6 with 0; 512 of 1 to 600 keys 57, with 0 67, with 2 64.
 constexpr int kDecRowCost = 1;
+// Tables of at most this many tiles: no row is divided, so that there is nothing to
+// join.  12 heads of 128, 256 keys 7.9 us, divided and joined 8.2, 128 keys 6.5 and
+// 8.1; but 384 keys 9.2 and 8.5; 64 sequences of 2 heads of 64, 512 keys 10.0 and 10.8.
+constexpr int kWholeTiles = 4;
 constexpr int kDecMaxParts = 1024; // CTAs at most
 constexpr float kDecLazy = 8.f;    // log2 slack of the reference maximum
 
@@ -88,6 +92,7 @@ struct DecArgs {
   const int32_t* count;      // [S, Hkv]
   __nv_bfloat16* O;          // [S, Hq, d]
   float scale_log2;
+  bool whole;                // no row is divided
   DecMeta* meta;             // workspace: [grid]
   float* part_o;             // [grid, 2, 8 or 16 heads, d] unnormalised
   float2* part_ml;           // [grid, 2, 8 or 16 heads]
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
   pdl_trigger();
   const int n_units = kLists ? v.S * v.Hkv : v.S;
   const Share sh =
-      share_work([&](int u) { return Rows::work(a, u); }, kDecRowCost, n_units, blockIdx.x, gridDim.x, sums);
+      share_work([&](int u) { return Rows::work(a, u); }, kDecRowCost, a.whole, n_units, blockIdx.x, gridDim.x, sums);
   __syncthreads();  // the scratch has been read
 
   if (warp == kPlanWarp) {

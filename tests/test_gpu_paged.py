@@ -402,6 +402,27 @@ def test_attention_many_short_rows(dev):
     _check_attention(O.cpu(), q, c)
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,page,keys", [(8, 2, 128, 16, 256), (8, 2, 128, 16, 272), (3, 3, 64, 64, 512), (16, 1, 64, 32, 544), (40, 40, 128, 64, 64)])
+@pytest.mark.parametrize("S", [1, 3, 149, 400])
+def test_attention_short_tables(dev, Hq, Hkv, d, page, keys, S):
+    # tables around the length up to which no row is divided
+    g = torch.Generator().manual_seed(S)
+    lens = torch.randint(0, keys + 1, (S,), generator=g).tolist()
+    lens[-1] = keys
+    c = ref.Cache(lens, Hkv, d, page, 18)
+    q = torch.randn(S, Hq, d, generator=g).to(BF16)
+    pp = ab.PagedParams(S, Hq, Hkv, d, page, c.num_pages, c.max_pages)
+    args = [t.to(dev) for t in (q, c.K, c.V, c.table)] + [ints(lens, dev)]
+    _check_attention(ab.ab_attention_paged(pp, *args).cpu(), q, c)
+    lists = [[sorted(torch.randperm(ref.cdiv(n, page), generator=g)[:(s + h) % 9].tolist()) for h in range(Hkv)] for s, n in enumerate(lens)]
+    idx = torch.full((S, Hkv, c.max_pages), -1, dtype=I32)
+    for s in range(S):
+        for h in range(Hkv):
+            idx[s, h, :len(lists[s][h])] = torch.tensor(lists[s][h], dtype=I32)
+    count = ints([[len(x) for x in y] for y in lists], dev)
+    _check_attention(ab.ab_attention_paged(pp, *args, idx=idx.to(dev), count=count).cpu(), q, c, lists=lists)
+
+
 def test_attention_rows_of_new_tokens(dev):
     # cu_new: the newest token's row of Q; sequences without one are left alone
     lens = [100, 50, 0, 33]

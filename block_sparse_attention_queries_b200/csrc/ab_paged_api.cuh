@@ -44,7 +44,7 @@ ab_status launch_after(void (*kern)(Params...), dim3 grid, int threads, int smem
 }
 
 // ------------------------------------------------------ norm and rotation
-constexpr int64_t kRopeSplit = 4096;                 // tokens of q, k and v together
+constexpr int64_t kRopeSplit = int64_t(1) << 22;     // values of q
 constexpr int64_t kRopeMaxUnits = int64_t(1) << 29;  // positions in the list of units stay in 32 bits
 
 ab_status check_norm_rope(const ab_norm_rope* nr) {
@@ -105,13 +105,16 @@ ab_status launch_norm_rope(NormRopeArgs a, int d, const ab_norm_rope* nr, cudaSt
     const bool many = heads > 16 * rows * kRopeRows;
     const int nv = many ? kRopeRowsMany : kRopeRows, stages = many ? kRopeStagesMany : kRopeStages;
     const int threads = 32 * ((heads + rows * nv - 1) / (rows * nv));
-    // Keys that need less than half the queries' warps: launches of their own, with
-    // as many warps as each needs (44 thousand tokens of 32 + 8 + 8 heads, with
-    // their page means, 240 us against 315 in one launch, of 40 + 4 + 4 241 against
-    // 373, 1500 of 32 + 8 + 8 13.5 against 15.6; but 600 10.2 against 8.7, and of
-    // 16 + 8 + 8 heads 44 thousand 178 against 180, 1500 11.7 against 10.6).
-    const int warps_kv = (a.heads[1] + rows * nv - 1) / (rows * nv);
-    if (a.tokens[0] && all > a.tokens[0] && 64 * warps_kv < threads && all >= kRopeSplit) {
+    // Key heads a third of the queries' or fewer: launches of their own, with as many
+    // warps as each needs (with their page means: 44 thousand tokens of 32 + 8 + 8
+    // heads 240 us against 315 in one launch, of 40 + 4 + 4 235 against 373, of 32 + 4
+    // + 4 heads of 64 136 against 155; of 16 + 8 + 8 178 against 180, of 24 + 12 + 12
+    // 286 against 279), once the queries fill the GPU a few times (1500 tokens of 32 +
+    // 8 + 8 heads 13.5 against 15.6, but 600 10.2 against 8.7, and 1500 with heads of
+    // 64 11.1 against 10.4).
+    const int per_warp = rows * nv, warps_kv = (a.heads[1] + per_warp - 1) / per_warp;
+    if (a.tokens[0] && all > a.tokens[0] && 32 * warps_kv < threads && 3 * a.heads[1] <= a.heads[0] &&
+        int64_t(a.tokens[0]) * a.heads[0] * d >= kRopeSplit) {
       NormRopeArgs q = a, kv = a;
       q.tokens[1] = q.tokens[2] = kv.tokens[0] = 0;
       const ab_status s = launch_norm_rope(q, d, nr, st);

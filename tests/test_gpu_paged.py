@@ -185,7 +185,7 @@ def test_append(dev, Hq, Hkv, d, page, norm, interleaved):
             assert torch.equal(sc[p].view(torch.int16), c.ksum[p].view(torch.int16))
 
 
-@pytest.mark.parametrize("Hq,Hkv,d", [(32, 8, 128), (40, 4, 128), (72, 9, 64), (160, 10, 128)])
+@pytest.mark.parametrize("Hq,Hkv,d", [(32, 8, 128), (40, 4, 128), (72, 9, 64), (160, 10, 128), (48, 3, 64)])
 def test_append_many_tokens_of_few_key_heads(dev, Hq, Hkv, d):
     g = torch.Generator().manual_seed(7)
     page, T = 16, 1500

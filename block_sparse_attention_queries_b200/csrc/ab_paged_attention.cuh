@@ -4,7 +4,7 @@
 //   O[s, h] = sum_k e^{x_k} v_k / sum_k e^{x_k},  x_k = q_h . k_k / sqrt(d),
 //
 // over the keys k of sequence s and h's key/value head (of the listed pages),
-// with the running maximum and sum of the softmax in fp32.
+// with the running maximum and sums of the softmax in fp32.
 //
 // Each key and value is read once for the G query heads that share it: 2 G
 // products per 2-byte element, far below what the tensor cores need per byte,
@@ -66,6 +66,13 @@ constexpr int kDecRowCost = 1;
 constexpr int kWholeTiles = 4;
 constexpr int kDecMaxParts = 1024; // CTAs at most
 constexpr float kDecLazy = 8.f;    // log2 slack of the reference maximum
+// Tiles of a row whose P V stays in the products' own accumulators.  Their sum cuts
+// off what does not fit, to one side, so its error grows with its length (2000
+// tiles of random values in one CTA: small outputs 3 % off); behind these many tiles
+// it is taken out and added in fp32, to nearest, in shared memory.  8 sequences of
+// 122 thousand keys 295 us, 293 without, with 16 query heads a key head 302 and 295;
+// by 16 tiles 298 and 308; every tile's product added in registers 298 and 338.
+constexpr int kDecOwnSum = 64;
 
 // A CTA's share, for the joining kernel: its tiles [begin, begin + n) of the
 // list, and the row that begins in it and ends behind it (-1: none), that row's
@@ -83,7 +90,9 @@ struct DecTile {
   int flags;
   int pad[3];
 };
-enum : int { kTileFirst = 1, kTileLast = 2, kRowStart = 4, kRowEnd = 8, kTileRow = 4 /* shift: rows begun before */ };
+// of the CTA's tiles of a row: the first, the last; of the row: the first, the last;
+// every kDecOwnSum-th, one behind such a one; shift: rows begun before
+enum : int { kTileFirst = 1, kTileLast = 2, kRowStart = 4, kRowEnd = 8, kTileOut = 16, kTileMore = 32, kTileRow = 6 };
 
 struct DecArgs {
   PagedView v;
@@ -270,7 +279,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
         d.row = int(row);
         d.qrow = query_row(v, s);
         d.flags = (off == 0 || at == 0 ? kTileFirst : 0) | (off == T - 1 || at == sh.n - 1 ? kTileLast : 0) |
-                  (off == 0 ? kRowStart : 0) | (off == T - 1 ? kRowEnd : 0);
+                  (off == 0 ? kRowStart : 0) | (off == T - 1 ? kRowEnd : 0) |
+                  (min(off, at) % kDecOwnSum == kDecOwnSum - 1 ? kTileOut : 0) | (min(off, at) >= kDecOwnSum ? kTileMore : 0);
         if (at == sh.n - 1) {
           if (off < T - 1 && off <= at) {  // the row begins here and goes on behind the share
             meta.row = d.row;
@@ -538,22 +548,47 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(st));
-      if (!(flags & kTileLast)) continue;
+      if (!(flags & (kTileLast | kTileOut))) continue;
 
-      // join the four warps' results of this row
-      if (!group_sync()) break;  // the buffer's last readers are done
+      // what the accumulators hold goes to this lane's places in the group's buffer
+      if (flags & kTileMore) {  // with what is there, in terms of the maximum now
+        const float m0 = __shfl_sync(0xffffffffu, m[0], g >> 1), m1 = __shfl_sync(0xffffffffu, m[1], g >> 1);
+        const float m_g = g & 1 ? m1 : m0;
+        const float f = m_g == -INFINITY ? 0.f : ex2_approx(ml[gwarp * 8 + g].x - m_g);
+        const float* src = mrg + (gwarp * 8 + g) * SM::kPitch + 2 * t;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const float2 x = *reinterpret_cast<const float2*>(src + 8 * k);
+          o[k][0] = fmaf(x.x, f, o[k][0]);
+          o[k][1] = fmaf(x.y, f, o[k][1]);
+        }
+        __syncwarp();
+      } else if (!group_sync()) {  // its last readers are done
+        break;
+      }
+      float lsum[2] = {l[0], l[1]};
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
-        for (int z = 0; z < 2; ++z) l[z] += __shfl_xor_sync(0xffffffffu, l[z], off);
+        for (int z = 0; z < 2; ++z) lsum[z] += __shfl_xor_sync(0xffffffffu, lsum[z], off);
       if (g == 0) {
-        ml[gwarp * 8 + 2 * t] = make_float2(m[0], l[0]);
-        ml[gwarp * 8 + 2 * t + 1] = make_float2(m[1], l[1]);
+        ml[gwarp * 8 + 2 * t] = make_float2(m[0], lsum[0]);
+        ml[gwarp * 8 + 2 * t + 1] = make_float2(m[1], lsum[1]);
       }
       float* dst = mrg + (gwarp * 8 + g) * SM::kPitch + 2 * t;
 #pragma unroll
       for (int k = 0; k < D / 8; ++k)
         *reinterpret_cast<float2*>(dst + 8 * k) = make_float2(o[k][0] + o[k][2], o[k][1] + o[k][3]);
+      if (!(flags & kTileLast)) {
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
+        continue;
+      }
+
+      // join the four warps' results of this row
       if (!group_sync()) break;
       const bool whole = started && (flags & kRowEnd);
       const int64_t row = mt.z;

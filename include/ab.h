@@ -493,7 +493,9 @@ ab_status ab_paged_topk(const ab_paged_params* p, const float* P, const int32_t*
  * over the first lens[s] tokens of sequence s, or over those in the pages
  * idx[s,g,0..count[s,g]) (positions in the sequence; in any order, a page that
  * is listed twice counts twice).  O = 0 where there is no key.  What the cache
- * holds behind a sequence's end does not matter (NaN included).
+ * holds behind a sequence's end does not matter (NaN included).  Infinite and NaN
+ * values show in O; a key whose weight is below 2^-110 of its row's largest may count
+ * as one of weight 0, whose infinite value gives NaN.
  *   idx, count  device, as ab_paged_topk writes them; both NULL: all pages
  *   O           device, out, [S, Hq, d] bf16 (row s; rows of skipped sequences
  *               are left as they were)

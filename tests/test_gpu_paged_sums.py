@@ -68,3 +68,37 @@ def test_long_sums_round_both_ways(dev, Hq, d, lists):
     want = 1.0 / n
     off = (O - want).abs().max().item()
     assert off <= (ref.HALF * (1 + rounded) + rounded) * want, (off / want, rounded)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,page", [(1, 1, 64, 16), (8, 2, 128, 16), (16, 1, 128, 64), (12, 1, 64, 32)])
+@pytest.mark.parametrize("lists", [False, True])
+def test_infinite_values_show(dev, Hq, Hkv, d, page, lists):
+    # +inf, -inf and NaN values at the first key, in the middle, at the last; rows of one key, of one CTA and of many
+    lens = [1, 1, 40, 700, 30000, 90000]
+    c = ref.Cache(lens, Hkv, d, page, 31)
+    inf = float("inf")
+    for s, n in enumerate(lens):
+        for h in range(Hkv):
+            for at, dim, x in ((0, 0, inf), (n // 2, 1, -inf), (n - 1, 2, inf), (n - 1, 3, -inf), (0, 4, inf), (n - 1, 4, -inf),
+                               (n // 3, 5, float("nan")), (n // 4, 6, inf), (n // 5, 6, float("nan")), (n // 6, 7, inf)):
+                c.values[s][at, h, dim] = x
+        for j in range(ref.cdiv(n, page)):
+            m = min(page, n - j * page)
+            c.V[c.table[s, j], :, :m] = c.values[s][j * page:j * page + m].transpose(0, 1)
+    q = torch.randn(len(lens), Hq, d, generator=torch.Generator().manual_seed(32)).to(BF16)
+    pp = ab.PagedParams(len(lens), Hq, Hkv, d, page, c.num_pages, c.max_pages)
+    more = {}
+    if lists:
+        more = dict(idx=torch.arange(c.max_pages, dtype=I32).expand(len(lens), Hkv, -1).contiguous().to(dev),
+                    count=torch.tensor([[ref.cdiv(n, page)] * Hkv for n in lens], dtype=I32).to(dev))
+    O = ab.ab_attention_paged(pp, *(t.to(dev) for t in (q, c.K, c.V, c.table)), torch.tensor(lens, dtype=I32).to(dev), **more).cpu()
+    G = Hq // Hkv
+    for s, n in enumerate(lens):
+        for h in range(Hkv):
+            got = O[s, h * G:(h + 1) * G].double()
+            o, size, eps = ref.attention(q[s, h * G:(h + 1) * G], c.keys[s][:, h], c.values[s][:, h], d)
+            fine = torch.isfinite(o)
+            assert not fine[:, :8].any() or n == 1 and not fine[:, :7].all()
+            assert torch.equal(torch.isnan(got), torch.isnan(o))
+            assert torch.equal(torch.isinf(got), torch.isinf(o)) and torch.equal(got[torch.isinf(o)], o[torch.isinf(o)])
+            ref.assert_attention(torch.where(fine, got, 0.0), torch.where(fine, o, 0.0), torch.where(fine, size, 0.0), eps, n)

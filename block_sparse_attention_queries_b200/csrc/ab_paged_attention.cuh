@@ -192,6 +192,14 @@ __device__ __forceinline__ float join_parts(float upper, float lower) {
   return fabsf(upper) < INFINITY ? upper + lower : upper;
 }
 
+// As lane0_wait, and what the other side wrote before its arrival is seen by every
+// lane (a shuffle orders no memory).
+__device__ __forceinline__ bool lead_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = lane0_wait(bar, parity, abort_flag);
+  __syncwarp();
+  return ok;
+}
+
 // D: head dim.  kLists: the pages of a list instead of all.
 template <int D, bool kLists>
 __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const __grid_constant__ DecArgs a) {
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages; ++k) {
-      mbar_init(full(k), 96);
+      mbar_init(full(k), 97);  // the copies of three warps' lanes, and the tile's description
       mbar_init(empty(k), 4 * kDecGroups);
     }
     for (int k = 0; k < 2; ++k) {
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
       const uint32_t firsts = __ballot_sync(0xffffffffu, d.flags & kTileFirst);
       d.flags |= (rows + __popc(firsts & (0xffffffffu >> (31 - lane))) - 1) << kTileRow;
       rows += __popc(firsts);
-      ok = lane0_wait(plan_empty(batch & 1), ((batch >> 1) & 1) ^ 1, abort_flag);
+      ok = lead_wait(plan_empty(batch & 1), ((batch >> 1) & 1) ^ 1, abort_flag);
       if (!ok) break;
       plan[(batch & 1) * 32 + lane] = d;
       __syncwarp();
@@ -345,12 +353,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
     uint32_t use = 0;  // tiles issued
     bool ok = true;
     for (int base = 0, batch = 0; base < sh.n && ok; base += 32, ++batch) {
-      ok = lane0_wait(plan_full(batch & 1), (batch >> 1) & 1, abort_flag);
+      ok = lead_wait(plan_full(batch & 1), (batch >> 1) & 1, abort_flag);
       const int n = min(32, sh.n - base);
       for (int k = 0; k < n && ok; ++k, ++use) {
         const DecTile* d = plan + (batch & 1) * 32 + k;
         const int st = int(use % kStages);
-        ok = lane0_wait(empty(st), ((use / kStages) & 1) ^ 1, abort_flag);
+        ok = lead_wait(empty(st), ((use / kStages) & 1) ^ 1, abort_flag);
         if (!ok) break;
         const int flags = d->flags;
         const uint64_t valid = uint64_t(uint32_t(d->valid[0])) | uint64_t(uint32_t(d->valid[1])) << 32;
@@ -383,8 +391,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_attention_kernel(const _
           for (int h = row0; h < v.G; h += kStep, q += kStep * D)
             cp_async16(dst + uint32_t((h - row0) * SM::kQPitch), q);
         }
-        if (mine == 0 && lane == 0)
+        if (mine == 0 && lane == 0) {
           *reinterpret_cast<int4*>(smem + SM::kOffMeta + st * 16) = make_int4(d->valid[0], d->valid[1], d->row, flags);
+          mbar_arrive(full(st));  // the copies' arrival below orders no plain store
+        }
         cp_async_arrive(full(st));  // arrives when this lane's copies have landed
       }
       __syncwarp();

@@ -46,7 +46,7 @@ struct NormRopeArgs {
   TokenView in[3];         // q, k, v; ptr null: this one is not wanted
   __nv_bfloat16* out[3];
   const float* w[2];       // weights of q and k, null: ones
-  const int32_t* pos[2];   // positions of q's and k's tokens, null: the token's index
+  const int32_t* pos[3];   // positions of the tokens, null: the token's index (v's: in the paged destination only)
   const float *cos_t, *sin_t;  // [n_pos, d/2], both null: no rotation
   int n_pos;
   float eps;
@@ -181,6 +181,10 @@ __device__ __forceinline__ void copy_table(const NormRopeArgs& a, int pos, uint4
   }
 }
 
+// A token of the cache is refused whole where its position is out of range, its value
+// too; in the dense layout values have no positions.
+__device__ __forceinline__ bool has_position(const NormRopeArgs& a, int side) { return a.cos_t && (side < 2 || a.slots); }
+
 // Where the rows of a token go: out + h * step, `write` false where it must not.
 struct RopePlace {
   __nv_bfloat16* out;
@@ -203,7 +207,7 @@ __device__ __forceinline__ RopePlace rope_place(const NormRopeArgs& a, int side,
     r.out += (int64_t(b) * (H - 1) * len + token) * D;  // row (b H + h) len + t, token b len + t
     r.step = int64_t(len) * D;
   }
-  if (side < 2 && a.cos_t && (pos < 0 || pos >= a.n_pos)) {
+  if (has_position(a, side) && (pos < 0 || pos >= a.n_pos)) {
     if (r.write && lane == 0) raise_error(AB_ERR_CAPACITY);
     r.write = false;
   }
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_kernel(const __grid
       }
       const int b = a.len[side] == a.tokens[side] ? 0 : int(uint32_t(p.z) / uint32_t(a.len[side]));
       p.w = side | group << 2 | b << 12;
-      if (side < 2 && a.cos_t) p.x = a.pos[side] ? __ldg(a.pos[side] + p.z) : p.z - b * a.len[side];
+      if (has_position(a, side)) p.x = a.pos[side] ? __ldg(a.pos[side] + p.z) : p.z - b * a.len[side];
       if (a.slots) p.y = __ldg(a.slots + p.z);
     }
     return p;
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(640) token_norm_rope_kernel(const __grid_const
       p.z = n - (side == 0 ? 0 : a.units[side - 1]);
       const int b = a.len[side] == a.tokens[side] ? 0 : int(uint32_t(p.z) / uint32_t(a.len[side]));
       p.w = side | b << 2;
-      if (side < 2 && a.cos_t) p.x = a.pos[side] ? __ldg(a.pos[side] + p.z) : p.z - b * a.len[side];
+      if (has_position(a, side)) p.x = a.pos[side] ? __ldg(a.pos[side] + p.z) : p.z - b * a.len[side];
       if (a.slots) p.y = __ldg(a.slots + p.z);
     }
     return p;

@@ -291,11 +291,13 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 
 // -------------------------------------------------------------- summaries
 // Mean of a page's keys, for every page that a slot list touches: the last
-// slot of each run of slots in one page owns the page, and the mean is over
-// the page's keys up to that slot.  A warp takes one (page, head), a run of at
-// most 16 KB, eight heads a CTA.  Bound by memory (the page's keys are read
-// once) or, for single tokens, by latency: 2.4 us for one token of 40 heads,
-// about 25 us for 44 thousand tokens of 8 heads (90 MB).
+// written slot of each run of slots in one page owns the page, and the mean is
+// over the page's keys up to that slot, without those that the call left unwritten
+// (a position out of range).  A warp takes one (page, head), a run of at most 16 KB,
+// eight heads a CTA.  Bound by memory (the page's keys are read once) or, for
+// single tokens, by latency: 2.4 us for one token of 40 heads, about 25 us for 44
+// thousand tokens of 8 heads (90 MB).
+
 // A load that stays in its place: eight of them are under way at once.
 __device__ __forceinline__ uint4 load_16(const void* p) {
   uint4 v;
@@ -305,26 +307,41 @@ __device__ __forceinline__ uint4 load_16(const void* p) {
 
 template <int D>
 __global__ void __launch_bounds__(256, 4)
-    page_sum_kernel(const int32_t* slots, int T, int per_cta, const __nv_bfloat16* K, __nv_bfloat16* ksum, int Hkv,
-                    int page_shift, int num_pages) {
+    page_sum_kernel(const int32_t* slots, const int32_t* positions, int n_pos, int T, int per_cta, const __nv_bfloat16* K,
+                    __nv_bfloat16* ksum, int Hkv, int page_shift, int num_pages) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = blockIdx.y * 8 + warp;
   const int t0 = blockIdx.x * per_cta;
   pdl_wait();
   pdl_trigger();
   if (head >= Hkv) return;
+  // positions null: no token has one
+  auto refused = [&](int t) { return positions && uint32_t(__ldg(positions + t)) >= uint32_t(n_pos); };
   int slot = -1;
   if (lane < per_cta && t0 + lane < T) {
     slot = __ldg(slots + t0 + lane);
-    if (slot >> page_shift >= num_pages) slot = -1;  // reported where the token is written
-    if (slot >= 0 && t0 + lane + 1 < T && __ldg(slots + t0 + lane + 1) >> page_shift == slot >> page_shift) slot = -1;
+    const bool bad = refused(t0 + lane);
+    if (bad || slot >> page_shift >= num_pages) slot = -1;  // reported where the token is written
+    for (int t = t0 + lane + 1; slot >= 0 && t < T && __ldg(slots + t) >> page_shift == slot >> page_shift; ++t)
+      if (!refused(t)) slot = -1;  // a later token is in the page
   }
   uint32_t owners = __ballot_sync(0xffffffffu, slot >= 0);
   const int sub = lane % kLanes, row0 = lane / kLanes;
   for (; owners; owners &= owners - 1) {
-    const int sl = __shfl_sync(0xffffffffu, slot, __ffs(owners) - 1);
+    const int owner = t0 + __ffs(owners) - 1, sl = __shfl_sync(0xffffffffu, slot, owner - t0);
     const int64_t id = sl >> page_shift;
     const int n = (sl & ((1 << page_shift) - 1)) + 1;
+    // the up to 63 tokens before it in the list, for those of its page that were refused
+    int before[2] = {-1, -1}, at[2] = {0, 0};
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const int t = owner - 1 - lane - 32 * z;
+      if (positions && t >= 0 && 32 * z < n - 1) {
+        before[z] = __ldg(slots + t);
+        at[z] = __ldg(positions + t);
+      }
+    }
+    uint64_t holes = 0;  // of the page's keys
     const __nv_bfloat16* src = K + (((id * Hkv + head) << page_shift) * D) + sub * 8;
     float acc[8] = {};
     for (int r0 = 0; r0 < n; r0 += 8 * kRows) {
@@ -333,6 +350,22 @@ __global__ void __launch_bounds__(256, 4)
       for (int k = 0; k < 8; ++k) {
         const int r = r0 + k * kRows + row0;
         x[k] = r < n ? load_16(src + int64_t(r) * D) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (r0 == 0) {
+        uint64_t mine = 0;
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+          if (before[z] < sl && before[z] >> page_shift == sl >> page_shift && uint32_t(at[z]) >= uint32_t(n_pos))
+            mine |= uint64_t(1) << (before[z] & ((1 << page_shift) - 1));
+        holes = uint64_t(__reduce_or_sync(0xffffffffu, uint32_t(mine))) |
+                uint64_t(__reduce_or_sync(0xffffffffu, uint32_t(mine >> 32))) << 32;
+      }
+      if (holes) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = r0 + k * kRows + row0;
+          if (r < n && (holes >> r) & 1) x[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -348,7 +381,7 @@ __global__ void __launch_bounds__(256, 4)
     for (int e = 0; e < 8; ++e) {
 #pragma unroll
       for (int o = kLanes; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
-      acc[e] /= float(n);
+      acc[e] /= float(n - __popcll(holes));
     }
     if (row0 == 0)
       *reinterpret_cast<uint4*>(ksum + (id * Hkv + head) * D + sub * 8) =

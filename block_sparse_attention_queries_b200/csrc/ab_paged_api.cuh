@@ -314,7 +314,7 @@ ab_status prepare_append(const ab_paged_params* p, const ab_norm_rope* nr, int32
   for (int x = 0; x < 3; ++x)
     for (const Span& y : o)
       if (overlap(y, span_of(in[x], 1, T, a->heads[x], p->d))) return AB_ERR_INVALID_ARG;
-  a->pos[0] = a->pos[1] = positions;
+  a->pos[0] = a->pos[1] = a->pos[2] = positions;
   a->slots = slots;
   a->page_shift = log2_of(p->page);
   a->num_pages = p->num_pages;
@@ -333,8 +333,8 @@ ab_status run_append(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T
   const dim3 grid(unsigned((T + per_cta - 1) / per_cta), unsigned((p->Hkv + 7) / 8));
   const auto* kc = static_cast<const __nv_bfloat16*>(Kc);
   auto* ks = static_cast<__nv_bfloat16*>(ksum);
-  return launch_after(p->d == 128 ? page_sum_kernel<128> : page_sum_kernel<64>, grid, 256, 0, st, a.slots, T, per_cta, kc,
-                      ks, p->Hkv, a.page_shift, a.num_pages);
+  return launch_after(p->d == 128 ? page_sum_kernel<128> : page_sum_kernel<64>, grid, 256, 0, st, a.slots,
+                      a.cos_t ? a.pos[1] : nullptr, a.n_pos, T, per_cta, kc, ks, p->Hkv, a.page_shift, a.num_pages);
 }
 
 ab_status run_paged_select(const ab_paged_params* p, const PagedView& v, const void* Q, const void* ksum, float* P,

@@ -447,15 +447,17 @@ ab_status ab_paged_plan(const ab_paged_params* p, int32_t T, const int32_t* n_ne
  * Norm and rotation of T new tokens (T = 0: nothing is done), written into the cache: Q [T, Hq, d]
  * receives the queries, the tokens' slots of K and V receive keys and values.
  * q has Hq heads, k and v have Hkv (the batch strides are not used).  A Q or a
- * cache that overlaps them is refused.  A token with a negative slot is skipped
- * (its row of Q is left as it was).
+ * cache that overlaps them is refused.  A token with a negative slot is skipped, and
+ * one whose slot or (with a rotation) position is out of range: its row of Q and its
+ * place in the cache are left as they were.
  *   slots, positions  device, int32 [T], as ab_paged_plan writes them.  Slots
  *                     must be distinct: of two tokens with one slot either may
  *                     remain, in parts.
- *   ksum              device, in/out, or NULL: for every page that the slots
- *                     touch, the mean of its keys up to the page's last slot
- *                     in the list (slots of one page stand together, in
- *                     ascending order, as ab_paged_plan writes them).
+ *   ksum              device, in/out, or NULL: for every page that tokens are
+ *                     written to, the mean of its keys up to the last of them,
+ *                     without the places of this call's skipped positions (slots
+ *                     of one page stand together, in ascending order, as
+ *                     ab_paged_plan writes them).
  */
 ab_status ab_paged_append(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T, const ab_tokens* q,
                           const ab_tokens* k, const ab_tokens* v, const int32_t* slots, const int32_t* positions,

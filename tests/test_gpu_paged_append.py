@@ -1,0 +1,107 @@
+"""Tokens that the append into the paged cache skips, and long lists of slots, on
+the GPU against a plain reference in 64 bits."""
+import pytest
+
+import paged_reference as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import block_sparse_attention_queries_b200 as ab  # noqa: E402
+
+BF16, I32 = torch.bfloat16, torch.int32
+CAPACITY = 4
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.fail("no CUDA device")
+    from block_sparse_attention_queries_b200 import build as abbuild
+    abbuild.build()
+    ab.lib()
+    return torch.device("cuda:0")
+
+
+@pytest.fixture(autouse=True)
+def _clean(dev):
+    ab.device_error(dev)
+    yield
+    assert ab.device_error(dev) == 0
+
+
+def _norm_rope(norm, Hq, Hk, d, n_pos, interleaved, seed, dev):
+    g = torch.Generator().manual_seed(seed)
+    shape = {"none": None, "head": lambda H: (d,), "token": lambda H: (H, d)}[norm]
+    wq, wk = (None, None) if shape is None else (1 + 0.3 * torch.randn(shape(H), generator=g) for H in (Hq, Hk))
+    a = torch.rand(n_pos, d // 2, generator=g) * 20
+    up = lambda t: None if t is None else t.to(dev)  # noqa: E731
+    return (wq, wk, a.cos(), a.sin()), ab.NormRope(norm, interleaved, 1e-6, up(wq), up(wk), up(a.cos()), up(a.sin()))
+
+
+def _same_bits(a, b):
+    return torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))
+
+
+def _append_and_check(dev, pp, norm, interleaved, n_pos, slots, pos, seed, error=0):
+    """The call's outputs against the reference; the cache holds NaN before it."""
+    T, Hq, Hkv, d, page = len(slots), pp.Hq, pp.Hkv, pp.d, pp.page
+    (wq, wk, cos, sin), nr = _norm_rope(norm, Hq, Hkv, d, n_pos, interleaved, seed, dev)
+    x = torch.randn(T, Hq + 2 * Hkv, d, generator=torch.Generator().manual_seed(seed + 1)).to(BF16)
+    xd = x.to(dev)
+    nan = float("nan")
+    K, V = (torch.full((pp.num_pages, Hkv, page, d), nan, dtype=BF16, device=dev) for _ in range(2))
+    ksum = torch.full((pp.num_pages, Hkv, d), nan, dtype=BF16, device=dev)
+    old = K.cpu(), ksum.cpu()
+    Q = torch.full((T, Hq, d), 7.0, dtype=BF16, device=dev)
+    ab.ab_paged_append(pp, nr, xd[:, :Hq], xd[:, Hq:Hq + Hkv], xd[:, Hq + Hkv:], torch.tensor(slots, dtype=I32).to(dev),
+                       torch.tensor(pos, dtype=I32).to(dev), K, V, ksum=ksum, out=Q)
+    assert ab.device_error(dev) == error
+    Q, K, V, ksum = (t.cpu() for t in (Q, K, V, ksum))
+    sl, at = torch.tensor(slots), torch.tensor(pos)
+    ok = (sl >= 0) & (sl < pp.num_pages * page) & (at >= 0) & (at < n_pos)
+    assert (Q[~ok] == 7.0).all()
+    sl, at, x = sl[ok], at[ok], x[ok]
+    q, size = ref.norm_rotate(x[:, :Hq], norm, wq, cos, sin, at, interleaved, 1e-6)
+    ref.assert_norm_rotate(Q[ok], q, size, norm, Hq * d)
+    k, size = ref.norm_rotate(x[:, Hq:Hq + Hkv], norm, wk, cos, sin, at, interleaved, 1e-6)
+    ref.assert_norm_rotate(K[sl // page, :, sl % page], k, size, norm, Hkv * d)
+    assert torch.equal(V[sl // page, :, sl % page], x[:, Hq + Hkv:])
+    written = torch.zeros(pp.num_pages, page, dtype=torch.bool)
+    written[sl // page, sl % page] = True
+    for t in (K, V):
+        assert _same_bits(t.transpose(1, 2)[~written], old[0].transpose(1, 2)[~written])
+    touched = written.any(1)
+    assert _same_bits(ksum[~touched], old[1][~touched])
+    w = written[:, None, :, None]
+    n = written.sum(1).double()[:, None, None].clamp(min=1)
+    keys = torch.where(w, K.double(), 0.0)
+    mean, size = keys.sum(2) / n, keys.abs().sum(2) / n
+    # a sum of up to 64 terms in fp32, a division, one rounding to bf16
+    off = (ksum.double() - mean).abs() - (ref.HALF * mean.abs() + (page + 2) * ref.U * 1.01 * size)
+    assert off[touched].max().item() <= 0
+
+
+@pytest.mark.parametrize("norm,interleaved", [("none", True), ("head", False), ("token", True)])
+@pytest.mark.parametrize("Hq,Hkv,d,page", [(4, 2, 64, 16), (9, 9, 128, 64), (8, 1, 128, 32)])
+@pytest.mark.parametrize("pages", [3, 90])
+def test_skipped_tokens_leave_no_trace(dev, norm, interleaved, Hq, Hkv, d, page, pages):
+    # positions out of range at a page's first, middle and last tokens, at all of them, beside slots out of range; the means
+    # are those of what was written (the cache is new: the other places hold NaN)
+    n_pos, T = 50, pages * page
+    slots = [page + t for t in range(T)]
+    pos = [t % n_pos for t in range(T)]
+    for p in range(0, pages, 3):
+        pos[p * page] = -1
+        pos[p * page + page // 2] = n_pos
+        pos[p * page + page - 1] = 2 ** 31 - 1
+    for t in range(page, 2 * page):
+        pos[t] = n_pos + t
+    if pages > 3:
+        for t in range(6 * page, 7 * page):
+            pos[t] = 3 if t == 6 * page + 5 else -5               # one is left
+        for t in range(8 * page + page // 2, 9 * page):
+            slots[t] = -1                                          # behind a sequence's last token
+        slots[11 * page - 1] = 2 ** 31 - 1
+    pp = ab.PagedParams(1, Hq, Hkv, d, page, pages + 2, pages + 2)
+    _append_and_check(dev, pp, norm, interleaved, n_pos, slots, pos, 40, CAPACITY)

@@ -138,8 +138,8 @@ class NormRope:
             if t is not None and t.dim() != (2 if norm == "token" else 1):
                 raise ValueError(f"weights of norm {norm!r} have shape [{'heads, ' if norm == 'token' else ''}d], "
                                  f"got {tuple(t.shape)}")
-        if cos is not None and (cos.dim() != 2 or cos.shape != sin.shape):
-            raise ValueError("cos and sin must be [n_pos, d/2]")
+        if cos is not None and (cos.dim() != 2 or cos.shape != sin.shape or cos.shape[0] < 1):
+            raise ValueError("cos and sin must be [n_pos, d/2], with one row at least")
         self.norm, self.interleaved, self.eps = norm, bool(interleaved), float(eps)
         self.wq, self.wk, self.cos, self.sin = wq, wk, cos, sin
         self.device = tensors[0].device if tensors else None

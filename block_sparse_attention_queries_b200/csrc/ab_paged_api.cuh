@@ -52,6 +52,8 @@ ab_status check_norm_rope(const ab_norm_rope* nr) {
   if (nr->norm < 0 || nr->norm > 2 || (nr->interleaved != 0 && nr->interleaved != 1)) return AB_ERR_INVALID_ARG;
   if (!(nr->eps >= 0.f) || nr->n_pos < 0) return AB_ERR_INVALID_ARG;
   if ((nr->cos_table == nullptr) != (nr->sin_table == nullptr)) return AB_ERR_INVALID_ARG;
+  // a position out of range is reported by a token that has copied row 0
+  if (nr->cos_table && nr->n_pos < 1) return AB_ERR_INVALID_ARG;
   const void* ptrs[] = {nr->wq, nr->wk, nr->cos_table, nr->sin_table};
   for (const void* q : ptrs)
     if (!aligned16(q)) return AB_ERR_INVALID_ARG;

@@ -337,7 +337,7 @@ typedef struct {
   int32_t norm;           /* 0, 1 or 2 */
   int32_t interleaved;    /* 0 or 1 */
   float eps;              /* >= 0 */
-  int32_t n_pos;          /* rows of the tables */
+  int32_t n_pos;          /* rows of the tables, at least 1 where there are tables */
   const float* wq;        /* device, weights of the queries' norm: [d] (norm 1), [heads, d] (norm 2); NULL: ones */
   const float* wk;        /* the keys' */
   const float* cos_table; /* device, [n_pos, d/2]; both tables NULL: no rotation */

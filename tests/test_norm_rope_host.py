@@ -1,0 +1,60 @@
+"""Refusals and arguments of the norm and rotation that the library and the
+binding decide on the host (pointers here are never read)."""
+import pytest
+
+import block_sparse_attention_queries_b200 as ab
+from block_sparse_attention_queries_b200 import build as abbuild
+
+GOOD, IN = 0x1000, 0x40000000
+OUT = (0x1000, 0x1000000, 0x2000000)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    abbuild.build()
+    return ab.lib()
+
+
+def _nr(**kw):
+    a = dict(norm=1, interleaved=0, eps=1e-6, n_pos=100, wq=GOOD, wk=None, cos_table=GOOD, sin_table=GOOD)
+    a.update(kw)
+    return ab.ab_norm_rope(*a.values())
+
+
+def test_tables_without_rows_are_refused(lib):
+    p = ab.Params(B=1, H=4, L=5, d=64, q_block=64, kv_block=16, C=4)
+    t = ab.ab_tokens(IN, 0, 256, 64)
+    empty = _nr(n_pos=0)
+    assert lib.ab_qk_norm_rope(p.c(), empty, t, None, None, GOOD, None, *OUT, None) == 1
+    assert lib.ab_forward_qkv(p.c(), empty, t, t, t, GOOD, GOOD, *OUT, *[GOOD] * 6, 1 << 45, None) == 1
+    pp = ab.PagedParams(S=4, Hq=4, Hkv=4, d=64, page=16, num_pages=100, max_pages=20)
+    assert lib.ab_paged_append(pp.c(), empty, 5, t, t, t, *[GOOD] * 6, None) == 1
+    assert lib.ab_paged_append(pp.c(), empty, 0, None, None, None, *[None] * 6, None) == 1
+    assert lib.ab_paged_forward(pp.c(), empty, 5, t, t, t, *[GOOD] * 14, 1 << 45, None) == 1
+
+
+class _OnDevice:
+    """What NormRope looks at in a tensor, without a GPU."""
+
+    def __init__(self, *shape):
+        import torch
+        self.shape, self.dtype, self.device, self.is_cuda = torch.Size(shape), torch.float32, "cuda:0", True
+
+    def is_contiguous(self):
+        return True
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return GOOD if self.shape.numel() else 0
+
+
+def test_binding_refuses_tables_without_rows():
+    pytest.importorskip("torch")
+    assert ab.NormRope("none", cos=_OnDevice(1, 32), sin=_OnDevice(1, 32)).n_pos == 1
+    with pytest.raises(ValueError, match="row"):  # their address is null, as if there were no rotation
+        ab.NormRope("none", cos=_OnDevice(0, 32), sin=_OnDevice(0, 32))

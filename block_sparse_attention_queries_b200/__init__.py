@@ -120,14 +120,24 @@ class NormRope:
     heads); ``wq`` and ``wk`` fp32 weights [d] or [heads, d] (None: ones);
     ``cos`` and ``sin`` fp32 [n_pos, d/2] (both None: no rotation);
     ``interleaved``: pairs (2i, 2i+1), else (i, i + d/2).  All tensors are
-    contiguous on one CUDA device and are kept."""
+    contiguous on one CUDA device and are kept; their values may change, a
+    NormRope's attributes cannot."""
 
     def __init__(self, norm="head", interleaved=True, eps=1e-6, wq=None, wk=None, cos=None, sin=None):
-        import torch
         if norm not in NORMS:
             raise ValueError(f"norm must be one of {sorted(NORMS)}, got {norm!r}")
         if (cos is None) != (sin is None):
             raise ValueError("cos and sin come together")
+        self.__dict__.update(norm=norm, interleaved=bool(interleaved), eps=float(eps), wq=wq, wk=wk, cos=cos, sin=sin)
+        self._bind()
+
+    def _addresses(self):
+        return tuple(0 if t is None else t.data_ptr() for t in (self.wq, self.wk, self.cos, self.sin))
+
+    def _bind(self):
+        """The library's copy, from the tensors as they are."""
+        import torch
+        wq, wk, cos, sin = self.wq, self.wk, self.cos, self.sin
         tensors = [t for t in (wq, wk, cos, sin) if t is not None]
         for t in tensors:
             if t.dtype != torch.float32 or not t.is_contiguous() or not t.is_cuda:
@@ -135,22 +145,26 @@ class NormRope:
             if t.device != tensors[0].device:
                 raise ValueError("weights and tables must be on one device")
         for t in (wq, wk):
-            if t is not None and t.dim() != (2 if norm == "token" else 1):
-                raise ValueError(f"weights of norm {norm!r} have shape [{'heads, ' if norm == 'token' else ''}d], "
+            if t is not None and t.dim() != (2 if self.norm == "token" else 1):
+                raise ValueError(f"weights of norm {self.norm!r} have shape [{'heads, ' if self.norm == 'token' else ''}d], "
                                  f"got {tuple(t.shape)}")
         if cos is not None and (cos.dim() != 2 or cos.shape != sin.shape or cos.shape[0] < 1):
             raise ValueError("cos and sin must be [n_pos, d/2], with one row at least")
-        self.norm, self.interleaved, self.eps = norm, bool(interleaved), float(eps)
-        self.wq, self.wk, self.cos, self.sin = wq, wk, cos, sin
-        self.device = tensors[0].device if tensors else None
-        self._index = tensors[0].get_device() if tensors else None
-        self._fits = None
-        self.n_pos = 0 if cos is None else cos.shape[0]
-        self._c = ab_norm_rope(NORMS[norm], int(self.interleaved), self.eps, self.n_pos,
-                               *(0 if t is None else t.data_ptr() for t in (wq, wk, cos, sin)))
+        at, n_pos = self._addresses(), 0 if cos is None else cos.shape[0]
+        self.__dict__.update(
+            n_pos=n_pos, device=tensors[0].device if tensors else None, _index=tensors[0].get_device() if tensors else None,
+            _fits=None, _at=at, _c=ab_norm_rope(NORMS[self.norm], int(self.interleaved), self.eps, n_pos, *at))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"cannot assign to {name!r}: make another NormRope")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"cannot delete {name!r}: make another NormRope")
 
     def check(self, Hq: int, Hk: int, d: int, index: int):
         """The weights and tables belong to Hq query and Hk key heads of d on CUDA device `index`."""
+        if self._at != self._addresses():  # a tensor has other storage now (`.data = ...`)
+            self._bind()
         if self._fits == (Hq, Hk, d, index):
             return
         for t, H in ((self.wq, Hq), (self.wk, Hk)):
@@ -160,7 +174,7 @@ class NormRope:
             raise ValueError(f"cos and sin have {self.cos.shape[1]} columns, {d // 2} expected")
         if self._index is not None and self._index != index:
             raise ValueError(f"weights and tables are on {self.device}, the tokens on cuda:{index}")
-        self._fits = (Hq, Hk, d, index)
+        self.__dict__["_fits"] = (Hq, Hk, d, index)
 
 
 @dataclass(frozen=True)

@@ -49,8 +49,10 @@ class _OnDevice:
     def get_device(self):
         return 0
 
+    at = GOOD
+
     def data_ptr(self):
-        return GOOD if self.shape.numel() else 0
+        return self.at if self.shape.numel() else 0
 
 
 def test_binding_refuses_tables_without_rows():
@@ -58,3 +60,34 @@ def test_binding_refuses_tables_without_rows():
     assert ab.NormRope("none", cos=_OnDevice(1, 32), sin=_OnDevice(1, 32)).n_pos == 1
     with pytest.raises(ValueError, match="row"):  # their address is null, as if there were no rotation
         ab.NormRope("none", cos=_OnDevice(0, 32), sin=_OnDevice(0, 32))
+
+
+def test_a_norm_rope_does_not_change():
+    # the library's copy holds the tensors' addresses: another table would be ignored, and the first one freed
+    pytest.importorskip("torch")
+    nr = ab.NormRope("none", cos=_OnDevice(3, 32), sin=_OnDevice(3, 32))
+    for name, value in (("cos", _OnDevice(9, 32)), ("sin", None), ("wq", _OnDevice(64)), ("eps", 1e-5), ("norm", "head"), ("n_pos", 9)):
+        with pytest.raises(AttributeError):
+            setattr(nr, name, value)
+    with pytest.raises(AttributeError):
+        del nr.cos
+    nr.check(4, 2, 64, 0)
+    assert nr.n_pos == 3 and nr._c.n_pos == 3
+
+
+def test_a_tensor_with_other_storage():
+    # as after `.data = ...`: the address and the checks are those of the storage that the call meets
+    pytest.importorskip("torch")
+    w, cos, sin = _OnDevice(64), _OnDevice(3, 32), _OnDevice(3, 32)
+    nr = ab.NormRope("head", wq=w, cos=cos, sin=sin)
+    nr.check(4, 2, 64, 0)
+    w.at = 0x5000
+    cos.at, cos.shape, sin.at, sin.shape = 0x6000, type(cos.shape)((9, 32)), 0x7000, type(cos.shape)((9, 32))
+    nr.check(4, 2, 64, 0)
+    assert (nr._c.wq, nr._c.cos_table, nr._c.sin_table, nr._c.n_pos, nr.n_pos) == (0x5000, 0x6000, 0x7000, 9, 9)
+    w.at, w.shape = 0x8000, type(w.shape)((32,))
+    with pytest.raises(ValueError, match="fit"):
+        nr.check(4, 2, 64, 0)
+    w.at, w.is_cuda = 0x9000, False
+    with pytest.raises(ValueError, match="CUDA"):
+        nr.check(4, 2, 64, 0)

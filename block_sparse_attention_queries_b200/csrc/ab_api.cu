@@ -49,14 +49,21 @@ int budget_of(int Nkv, double keep) {
   return int(kb);
 }
 
-// Host-side validation shared by every entry point.  `need_method` also checks
-// the fields only the sparse path uses.
-ab_status check_params(const ab_params* p, bool need_method, Dims* out) {
+// B, H, L, L_kv and d: what every entry point uses.
+ab_status check_sizes(const ab_params* p) {
   if (!p) return AB_ERR_INVALID_ARG;
   if (p->B < 1 || p->H < 1 || p->L < 1 || p->L > (1 << 24)) return AB_ERR_INVALID_ARG;
   if (p->L_kv < 0 || p->L_kv > (1 << 24)) return AB_ERR_INVALID_ARG;
   if (int64_t(p->B) * p->H > (int64_t(1) << 20)) return AB_ERR_INVALID_ARG;
   if (p->d != 64 && p->d != 128) return p->d > 0 ? AB_ERR_UNSUPPORTED : AB_ERR_INVALID_ARG;
+  return AB_OK;
+}
+
+// Host-side validation shared by every entry point that works on query blocks.
+// `need_method` also checks the fields only the sparse path uses.
+ab_status check_params(const ab_params* p, bool need_method, Dims* out) {
+  const ab_status s = check_sizes(p);
+  if (s != AB_OK) return s;
   if (p->q_block != 64 && p->q_block != 128) return p->q_block > 0 ? AB_ERR_UNSUPPORTED : AB_ERR_INVALID_ARG;
   if (need_method) {
     if (p->kv_block != 16 && p->kv_block != 32 && p->kv_block != 64)

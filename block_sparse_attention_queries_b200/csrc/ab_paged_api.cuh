@@ -196,39 +196,40 @@ void set_norm_rope(NormRopeArgs* a, const ab_norm_rope* nr) {
 }
 
 // Arguments of the dense call.
-ab_status prepare_norm_rope(const Dims& d, const ab_norm_rope* nr, const ab_tokens* q, const ab_tokens* k,
+ab_status prepare_norm_rope(const ab_params& p, const ab_norm_rope* nr, const ab_tokens* q, const ab_tokens* k,
                             const ab_tokens* v, const int32_t* pos_q, const int32_t* pos_k, void* Q, void* K, void* V,
                             NormRopeArgs* a) {
   const ab_status s = check_norm_rope(nr);
   if (s != AB_OK) return s;
   if (!q && !k && !v) return AB_ERR_INVALID_ARG;
+  const int Lk = p.L_kv > 0 ? p.L_kv : p.L;
   const ab_tokens* in[3] = {q, k, v};
   void* out[3] = {Q, K, V};
   const int32_t* pos[2] = {pos_q, pos_k};
   *a = NormRopeArgs{};
   for (int x = 0; x < 3; ++x) {
-    const int len = x == 0 ? d.L : d.Lk;
+    const int len = x == 0 ? p.L : Lk;
     if (!in[x]) continue;
-    if (check_tokens(in[x], d.B, len, d.H) != AB_OK || !out[x] || !aligned16(out[x])) return AB_ERR_INVALID_ARG;
+    if (check_tokens(in[x], p.B, len, p.H) != AB_OK || !out[x] || !aligned16(out[x])) return AB_ERR_INVALID_ARG;
     if (x < 2) {
       if (pos[x] && !aligned16(pos[x])) return AB_ERR_INVALID_ARG;
       if (nr->cos_table && !pos[x] && len > nr->n_pos) return AB_ERR_INVALID_ARG;
       a->pos[x] = pos[x];
     }
-    if (int64_t(d.B) * len > kRopeMaxUnits) return AB_ERR_UNSUPPORTED;
-    a->heads[x] = d.H;
+    if (int64_t(p.B) * len > kRopeMaxUnits) return AB_ERR_UNSUPPORTED;
+    a->heads[x] = p.H;
     a->len[x] = len;
-    a->tokens[x] = d.B * len;
+    a->tokens[x] = p.B * len;
     a->in[x] = view_of(in[x]);
     a->out[x] = static_cast<__nv_bfloat16*>(out[x]);
   }
-  if (d.H > rope_max_heads(d.d)) return AB_ERR_UNSUPPORTED;
+  if (p.H > rope_max_heads(p.d)) return AB_ERR_UNSUPPORTED;
   for (int x = 0; x < 3; ++x) {
     if (!in[x]) continue;
-    const Span o = span_of(out[x], int64_t(a->tokens[x]) * d.H * d.d);
+    const Span o = span_of(out[x], int64_t(a->tokens[x]) * p.H * p.d);
     for (int y = 0; y < 3; ++y) {
-      if (in[y] && overlap(o, span_of(in[y], d.B, a->len[y], d.H, d.d))) return AB_ERR_INVALID_ARG;
-      if (in[y] && y < x && overlap(o, span_of(out[y], int64_t(a->tokens[y]) * d.H * d.d))) return AB_ERR_INVALID_ARG;
+      if (in[y] && overlap(o, span_of(in[y], p.B, a->len[y], p.H, p.d))) return AB_ERR_INVALID_ARG;
+      if (in[y] && y < x && overlap(o, span_of(out[y], int64_t(a->tokens[y]) * p.H * p.d))) return AB_ERR_INVALID_ARG;
     }
   }
   set_norm_rope(a, nr);
@@ -438,14 +439,13 @@ extern "C" {
 ab_status ab_qk_norm_rope(const ab_params* p, const ab_norm_rope* nr, const ab_tokens* q, const ab_tokens* k,
                           const ab_tokens* v, const int32_t* pos_q, const int32_t* pos_k, void* Q, void* K, void* V,
                           void* stream) {
-  Dims d;
   NvtxRange nvtx("ab_qk_norm_rope");
-  ab_status s = check_params(p, false, &d);
+  ab_status s = check_sizes(p);
   if (s != AB_OK) return s;
   NormRopeArgs a;
-  s = prepare_norm_rope(d, nr, q, k, v, pos_q, pos_k, Q, K, V, &a);
+  s = prepare_norm_rope(*p, nr, q, k, v, pos_q, pos_k, Q, K, V, &a);
   if (s != AB_OK) return s;
-  return launch_norm_rope(a, d.d, nr, static_cast<cudaStream_t>(stream));
+  return launch_norm_rope(a, p->d, nr, static_cast<cudaStream_t>(stream));
 }
 
 ab_status ab_forward_qkv(const ab_params* p, const ab_norm_rope* nr, const ab_tokens* q, const ab_tokens* k,
@@ -460,7 +460,7 @@ ab_status ab_forward_qkv(const ab_params* p, const ab_norm_rope* nr, const ab_to
   s = check_path_args(Q, K, V, P, idx, pi_q32, count, O, workspace, ws_bytes, workspace_layout(d).total);
   if (s != AB_OK) return s;
   NormRopeArgs a;
-  s = prepare_norm_rope(d, nr, q, k, v, pos_q, pos_k, Q, K, V, &a);
+  s = prepare_norm_rope(*p, nr, q, k, v, pos_q, pos_k, Q, K, V, &a);
   if (s != AB_OK) return s;
   s = launch_norm_rope(a, d.d, nr, static_cast<cudaStream_t>(stream));
   if (s != AB_OK) return s;

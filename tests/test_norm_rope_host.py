@@ -33,6 +33,18 @@ def test_tables_without_rows_are_refused(lib):
     assert lib.ab_paged_forward(pp.c(), empty, 5, t, t, t, *[GOOD] * 14, 1 << 45, None) == 1
 
 
+@pytest.mark.parametrize("rest", [dict(q_block=0), dict(q_block=96), dict(q_block=-5),
+                                  dict(kv_block=7, C=3, kmeans_iters=-1, keep_ratio=9.0),
+                                  dict(q_block=0, kv_block=0, C=0, kmeans_iters=0, keep_ratio=0.0)])
+def test_only_the_documented_sizes_count(lib, rest):
+    # B, H, L, L_kv and d: what is refused here is refused for what stands behind them (too few rows: 1, too many heads: 2)
+    t = ab.ab_tokens(IN, 50 * 256, 256, 64)
+    p = ab.Params(B=2, H=4, L=50, d=64, **rest).c()
+    assert lib.ab_qk_norm_rope(p, _nr(n_pos=49), t, None, None, None, None, *OUT, None) == 1
+    p = ab.Params(B=2, H=257, L=50, d=128, **rest).c()
+    assert lib.ab_qk_norm_rope(p, _nr(), t, None, None, None, None, *OUT, None) == 2
+
+
 class _OnDevice:
     """What NormRope looks at in a tensor, without a GPU."""
 

@@ -698,7 +698,8 @@ def ab_paged_append(pp: PagedParams, nr: NormRope, q, k, v, slots, positions, K,
     """Norm and rotation of new tokens q [T, Hq, d], k and v [T, Hkv, d] bf16
     (strides as for ab_qk_norm_rope), keys and values written to their slots of
     the cache, the touched pages' means to ksum (None: not kept); returns the
-    queries Q [T, Hq, d] (`out` if given)."""
+    queries Q [T, Hq, d] (`out` if given; rows of skipped tokens are left as they
+    were, in a new Q not set)."""
     import torch
     bf16, i32 = torch.bfloat16, torch.int32
     dev, T, tok = _paged_tokens(pp, nr, q, k, v)
@@ -722,7 +723,7 @@ def ab_paged_select(pp: PagedParams, Q, ksum, table, lens, cu_new=None, workspac
     """Every page's estimated share P [S, Hkv, max_pages] fp32 of the attention
     mass of each sequence's newest token (entries behind a sequence's last page
     are left as they were, 0 in a new P).  Q [S, Hq, d], or [T, Hq, d] with
-    cu_new [S + 1] as ab_paged_plan returns it."""
+    cu_new [S + 1] as ab_paged_plan returns it (T = 0: nothing is done)."""
     import torch
     bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     dev, T = _cuda_index(Q), _query_rows(pp, Q, cu_new)
@@ -733,7 +734,8 @@ def ab_paged_select(pp: PagedParams, Q, ksum, table, lens, cu_new=None, workspac
     ptrs = _m().tensors(dev, Q, bf16, (T, pp.Hq, pp.d), "Q", ksum, bf16, (pp.num_pages, pp.Hkv, pp.d), "ksum",
                         table, i32, (pp.S, pp.max_pages), "table", lens, i32, (pp.S,), "lens", cu_new, i32, (pp.S + 1,), "cu_new",
                         P, f32, shape, "P", ws, torch.uint8, (n,), "workspace")
-    _call("ab_paged_select", dev, pp.c(), T, *ptrs, n)
+    if T:
+        _call("ab_paged_select", dev, pp.c(), T, *ptrs, n)
     return P
 
 
@@ -770,7 +772,8 @@ def ab_attention_paged(pp: PagedParams, Q, K, V, table, lens, idx=None, count=No
                         table, i32, (pp.S, pp.max_pages), "table", lens, i32, (pp.S,), "lens", cu_new, i32, (pp.S + 1,), "cu_new",
                         idx, i32, lists, "idx", count, i32, lists[:2], "count", O, bf16, shape, "O",
                         ws, torch.uint8, (n,), "workspace")
-    _call("ab_attention_paged", dev, pp.c(), T, *ptrs, n)
+    if T:
+        _call("ab_attention_paged", dev, pp.c(), T, *ptrs, n)
     return O
 
 
@@ -791,7 +794,7 @@ def ab_paged_forward(pp: PagedParams, nr: NormRope, q, k, v, cache: PagedCache, 
                      bufs: PagedBuffers | None = None) -> PagedBuffers:
     """One step of sparse attention over the cache for new tokens q [T, Hq, d], k
     and v [T, Hkv, d], after ab_paged_plan: append, select, top-k, attention of
-    each sequence's newest token."""
+    each sequence's newest token.  T = 0 (requests only end): nothing is done."""
     import torch
     bf16, i32 = torch.bfloat16, torch.int32
     if cu_new is None:
@@ -805,7 +808,8 @@ def ab_paged_forward(pp: PagedParams, nr: NormRope, q, k, v, cache: PagedCache, 
                         b.Q, bf16, (T, pp.Hq, pp.d), "Q", c.K, bf16, kv, "K", c.V, bf16, kv, "V",
                         c.ksum, bf16, (pp.num_pages, pp.Hkv, pp.d), "ksum", b.P, torch.float32, shape, "P", b.idx, i32, shape, "idx",
                         b.count, i32, shape[:2], "count", b.O, bf16, (pp.S, pp.Hq, pp.d), "O", c.ws, torch.uint8, (n,), "workspace")
-    _call("ab_paged_forward", dev, pp.c(), nr._c, T, *tok, *ptrs, n)
+    if T:
+        _call("ab_paged_forward", dev, pp.c(), nr._c, T, *tok, *ptrs, n)
     return b
 
 

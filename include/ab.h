@@ -395,7 +395,8 @@ ab_status ab_forward_qkv(const ab_params* p, const ab_norm_rope* nr, const ab_to
  * Where a call takes cu_new (device, int32 [S + 1], as ab_paged_plan writes
  * it), sequence s's query is row cu_new[s + 1] - 1 of Q [T, Hq, d], its newest
  * token, and a sequence without new tokens is skipped; with cu_new NULL its
- * query is row s and T must be S.
+ * query is row s and T must be S.  With no new token at all (T = 0) there is no
+ * query: the calls that take Q refuse it, but ab_paged_append, which does nothing.
  * Entries out of range (a length, a table or list entry, a count, a slot, a
  * position) raise AB_ERR_CAPACITY on the device and their work is skipped.
  */

@@ -105,3 +105,37 @@ def test_skipped_tokens_leave_no_trace(dev, norm, interleaved, Hq, Hkv, d, page,
         slots[11 * page - 1] = 2 ** 31 - 1
     pp = ab.PagedParams(1, Hq, Hkv, d, page, pages + 2, pages + 2)
     _append_and_check(dev, pp, norm, interleaved, n_pos, slots, pos, 40, CAPACITY)
+
+
+def test_steps_without_a_new_token(dev):
+    # requests that end and none that goes on: the step gives pages back and leaves everything else alone
+    pp = ab.PagedParams(3, 4, 2, 64, 16, 20, 10, keep_ratio=0.5)
+    _, nr = _norm_rope("head", 4, 2, 64, 160, True, 60, dev)
+    cache = ab.PagedCache(pp, dev)
+    cache.K.zero_(), cache.V.zero_(), cache.ksum.zero_()
+    x = torch.randn(40, 8, 64, generator=torch.Generator().manual_seed(61)).to(BF16).to(dev)
+
+    def step(n_new, T, bufs):
+        lists = ab.ab_paged_plan(pp, torch.tensor(n_new, dtype=I32).to(dev), cache.lens, cache.table, cache.free_pages,
+                                 cache.free_count, T=T)
+        y = x[:T]
+        return lists, ab.ab_paged_forward(pp, nr, y[:, :4], y[:, 4:6], y[:, 6:], cache, *lists, bufs=bufs)
+
+    step([20, 17, 3], 40, None)
+    bufs = ab.PagedBuffers(pp, 0, dev)
+    for t in (bufs.P, bufs.O):
+        t.fill_(5)
+    for t in (bufs.idx, bufs.count):
+        t.fill_(5)
+    before = [t.clone() for t in (cache.K, cache.V, cache.ksum)]
+    (cu, slots, pos), got = step([-1, 0, -1], 0, bufs)
+    assert got is bufs and all((t == 5).all() for t in (bufs.P, bufs.O, bufs.idx, bufs.count))
+    assert all(torch.equal(a, b) for a, b in zip(before, (cache.K, cache.V, cache.ksum)))
+    assert cache.lens.tolist() == [0, 17, 0] and cache.free_count.item() == 18 and cu.tolist() == [0] * 4
+    new = step([0, 0, -1], 0, None)[1]
+    assert new.Q.shape == (0, 4, 64) and not new.O.any() and not new.count.any()
+    Q = torch.zeros(0, 4, 64, dtype=BF16, device=dev)
+    assert not ab.ab_paged_select(pp, Q, cache.ksum, cache.table, cache.lens, cu_new=cu).any()
+    assert not ab.ab_attention_paged(pp, Q, cache.K, cache.V, cache.table, cache.lens, cu_new=cu).any()
+    with pytest.raises(ValueError):
+        ab.ab_paged_select(pp, Q, cache.ksum, cache.table, cache.lens)

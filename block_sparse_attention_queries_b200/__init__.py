@@ -512,11 +512,13 @@ def _m():
     """The built checks of tensors (csrc/marshal.cpp)."""
     global _marshal_module
     if _marshal_module is None:
-        import torch  # noqa: F401  (its libraries are loaded first)
+        import torch  # its libraries are loaded first
         try:
             from . import _marshal
         except ImportError as e:
             raise RuntimeError("_marshal.so not built; run block_sparse_attention_queries_b200/build.py") from e
+        if getattr(_marshal, "built_for", None) != f"AB_TORCH={torch.__version__};":
+            raise RuntimeError("_marshal.so was built for another torch; run block_sparse_attention_queries_b200/build.py")
         _marshal_module = _marshal
     return _marshal_module
 

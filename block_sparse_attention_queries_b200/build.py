@@ -40,32 +40,56 @@ def needs_build() -> bool:
     return _older(LIB, DEPS)
 
 
+def torch_version() -> str | None:
+    """None: without torch, which only the binding needs."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch.__version__
+
+
+def needs_marshal() -> bool:
+    """_marshal.so is missing, older than its source, or made for another torch (whose tensors it would misread)."""
+    if _older(MARSHAL, [MARSHAL_SRC, HEADER]):
+        return True
+    with open(MARSHAL, "rb") as f:
+        return f"AB_TORCH={torch_version()};".encode() not in f.read()
+
+
 def marshal_command() -> list:
     import torch
     base = os.path.dirname(torch.__file__)
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DAB_TORCH="{torch.__version__}"',
             "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(base, "include"),
             "-isystem", sysconfig.get_paths()["include"], MARSHAL_SRC, "-L", os.path.join(base, "lib"), "-ltorch_python",
             "-ltorch_cpu", "-lc10", "-o", MARSHAL + ".tmp"]
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    jobs = []
-    if force or needs_build():
-        jobs.append(([nvcc(), *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-o", LIB + ".tmp", SRC], LIB))
-    if force or _older(MARSHAL, [MARSHAL_SRC, HEADER]):
-        jobs.append((marshal_command(), MARSHAL))
-    running = []
-    for cmd, target in jobs:
+    """Brings both libraries up to date; without torch libab.so alone.  What can be built is, whatever fails."""
+    running, errors = [], []
+
+    def start(cmd, target):
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
-        running.append((subprocess.Popen(cmd), cmd, target))
+        try:
+            running.append((subprocess.Popen(cmd), cmd, target))
+        except OSError as e:
+            errors.append(e)
+
+    if force or needs_build():
+        start([nvcc(), *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-o", LIB + ".tmp", SRC], LIB)
+    if torch_version() is not None and (force or needs_marshal()):
+        start(marshal_command(), MARSHAL)
     for p, cmd, target in running:
         if p.wait() == 0:
             os.replace(target + ".tmp", target)
-    for p, cmd, target in running:
-        if p.returncode != 0:
-            raise subprocess.CalledProcessError(p.returncode, cmd)
+        else:
+            errors.append(subprocess.CalledProcessError(p.returncode, cmd))
+    if errors:
+        raise errors[0]
     return LIB
 
 

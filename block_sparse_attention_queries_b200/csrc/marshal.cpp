@@ -118,6 +118,16 @@ PyMethodDef methods[] = {
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
+// The torch whose headers this was built with, for the build and for the binding.
+const char kTorch[] = "AB_TORCH=" AB_TORCH ";";
+
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", kTorch) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -661,7 +661,8 @@ def ab_paged_plan(pp: PagedParams, n_new, lens, table, free_pages, free_count, T
                   free_count_out=None, out=None):
     """Block tables and slot maps of one step: n_new [S] int32 new tokens per
     sequence (-1: the sequence has ended), lens [S], table [S, max_pages],
-    free_pages [num_pages], free_count [1] int32.  Updates table and free_pages,
+    free_pages [num_pages], free_count [1] int32; no page may stand in two rows
+    of the table, or in one and the list of free pages.  Updates table and free_pages,
     lens and free_count too (or writes lens_out, free_count_out instead);
     returns (cu_new [S + 1], slots [T], positions [T]).  T: length of the slot
     map (at least the number of new tokens; None with `out`: that of out's

@@ -389,7 +389,13 @@ ab_status ab_forward_qkv(const ab_params* p, const ab_norm_rope* nr, const ab_to
  *   table   device, int32 [S, max_pages]: page of the j-th `page` tokens of
  *           sequence s, j < ceil(lens[s] / page); the rest is not read
  *   lens    device, int32 [S]: tokens of each sequence in the cache
- * Several sequences may share pages.  A slot is page id * page + offset.
+ * A slot is page id * page + offset.  Sequences may share pages for the calls that
+ * read the cache (ab_paged_select, ab_attention_paged).  ab_paged_plan knows no
+ * sharing: it takes every page of the tables and of the list of free pages to stand
+ * there once, gives all pages of an ended sequence back, also those that another one
+ * still holds, and lets sequences go on in their last page.  Callers who share pages
+ * keep table, lens, slots and free pages by themselves, and append no token to a
+ * page that another sequence reads.
  * Sequence lengths live on the device: no call needs them on the host, and
  * every call can be captured in a CUDA graph and replayed for other lengths.
  * Where a call takes cu_new (device, int32 [S + 1], as ab_paged_plan writes
@@ -422,7 +428,8 @@ ab_status ab_paged_workspace_size(const ab_paged_params* p, int32_t with_select,
  * it has ended.  The pages of ended sequences (in order of s, then j) go on top
  * of the list of free pages; then the sequences take the pages they need, in
  * order of s, then j, from the top of the list.  A sequence that would exceed
- * max_pages pages is not served.  Where the pages or the T slots do not
+ * max_pages pages is not served.  Every page belongs to one sequence or to the list
+ * of free pages (see above for pages that are shared).  Where the pages or the T slots do not
  * suffice, the first sequence that does not fit and all after it are not
  * served.  A sequence that is not served keeps its length (ended ones are
  * still released) and AB_ERR_CAPACITY is raised on the device.

@@ -139,3 +139,38 @@ def test_steps_without_a_new_token(dev):
     assert not ab.ab_attention_paged(pp, Q, cache.K, cache.V, cache.table, cache.lens, cu_new=cu).any()
     with pytest.raises(ValueError):
         ab.ab_paged_select(pp, Q, cache.ksum, cache.table, cache.lens)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,page", [(4, 2, 64, 16), (16, 1, 128, 64)])
+def test_reading_calls_share_pages(dev, Hq, Hkv, d, page):
+    # two sequences on one beginning, each with pages of its own behind it: as if the shared pages were copied, and a token
+    # of one of them, appended to its own page, changes nothing for the other
+    shared, own = 5, (3, 7)
+    lens = [(shared + k) * page - 5 for k in own]
+    c = ref.Cache(lens, Hkv, d, page, 70)
+    table = c.table.clone()
+    table[1, :shared] = table[0, :shared]
+    K, V, ksum = c.K.clone(), c.V.clone(), c.ksum.clone()
+    K[c.table[1, :shared].long()] = K[c.table[0, :shared].long()]
+    V[c.table[1, :shared].long()] = V[c.table[0, :shared].long()]
+    ksum[c.table[1, :shared].long()] = ksum[c.table[0, :shared].long()]
+    pp = ab.PagedParams(2, Hq, Hkv, d, page, c.num_pages, c.max_pages, keep_ratio=0.4)
+    g = torch.Generator().manual_seed(71)
+    q = torch.randn(2, Hq, d, generator=g).to(BF16).to(dev)
+    up = lambda *t: [x.to(dev) for x in t]  # noqa: E731
+    K, V, ksum, copied, table, n = up(K, V, ksum, c.table, table, torch.tensor(lens, dtype=I32))
+
+    def read(table, n):
+        P = ab.ab_paged_select(pp, q, ksum, table, n)
+        idx, count = ab.ab_paged_topk(pp, P, n)
+        return P, idx, ab.ab_attention_paged(pp, q, K, V, table, n), ab.ab_attention_paged(pp, q, K, V, table, n, idx=idx, count=count)
+
+    want = read(copied, n)
+    assert all(torch.equal(a, b) for a, b in zip(read(table, n), want))
+    x = torch.randn(1, Hq + 2 * Hkv, d, generator=g).to(BF16).to(dev)
+    slot = int(c.table[0, (lens[0]) // page]) * page + lens[0] % page
+    ab.ab_paged_append(pp, ab.NormRope("none"), x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], torch.tensor([slot], dtype=I32).to(dev),
+                       torch.tensor([lens[0]], dtype=I32).to(dev), K, V, ksum=ksum)
+    n[0] += 1
+    for a, b in zip(read(table, n), want):
+        assert torch.equal(a[1], b[1]) and not torch.equal(a[0].float(), b[0].float()) or a.dtype == I32

@@ -274,7 +274,11 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const Entry e = i == gtid ? entry0 : new_entry(i);
     a.table[e.at] = e.page;
   }
-  for (int64_t i = gtid; i < n_rel; i += gstep) a.free_pages[F0 + i] = i == gtid ? back0 : given_back(int(i));
+  for (int64_t i = gtid; i < n_rel; i += gstep) {
+    const int page = i == gtid ? back0 : given_back(int(i));
+    if (uint32_t(page) >= uint32_t(a.num_pages)) raise_error(AB_ERR_CAPACITY);  // no token can be put there either
+    a.free_pages[F0 + i] = page;
+  }
 
   // every CTA has read lens and free_count
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");

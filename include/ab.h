@@ -432,7 +432,9 @@ ab_status ab_paged_workspace_size(const ab_paged_params* p, int32_t with_select,
  * of free pages (see above for pages that are shared).  Where the pages or the T slots do not
  * suffice, the first sequence that does not fit and all after it are not
  * served.  A sequence that is not served keeps its length (ended ones are
- * still released) and AB_ERR_CAPACITY is raised on the device.
+ * still released) and AB_ERR_CAPACITY is raised on the device.  It is raised too
+ * where a page out of range is given back or handed out: it stays in its list, and
+ * its tokens get slot -1.
  *   n_new           device, int32 [S], >= -1
  *   lens, lens_out  device, int32 [S]: lengths before and after the step (may
  *                   be one buffer)

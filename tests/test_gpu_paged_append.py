@@ -174,3 +174,17 @@ def test_reading_calls_share_pages(dev, Hq, Hkv, d, page):
     n[0] += 1
     for a, b in zip(read(table, n), want):
         assert torch.equal(a[1], b[1]) and not torch.equal(a[0].float(), b[0].float()) or a.dtype == I32
+
+
+@pytest.mark.parametrize("wrong", [-1, 8, 2 ** 31 - 1])
+def test_plan_reports_bad_pages_that_come_back(dev, wrong):
+    # an ended sequence whose table names a page that the cache does not have; handed out again, its tokens have no slot
+    pp = ab.PagedParams(2, 1, 1, 64, 16, 8, 4)
+    up = lambda v: torch.tensor(v, dtype=I32).to(dev)  # noqa: E731
+    table, free, count, lens = up([[3, wrong, -9, -9], [-9] * 4]), up([0, 1, -5, -5, -5, -5, -5, -5]), up([2]), up([20, 0])
+    cu, slots, pos = ab.ab_paged_plan(pp, up([-1, 0]), lens, table, free, count, T=4)
+    assert ab.device_error(dev) == CAPACITY
+    assert free.tolist()[:4] == [0, 1, 3, wrong] and count.item() == 4 and lens.tolist() == [0, 0] and slots.tolist() == [-1] * 4
+    cu, slots, pos = ab.ab_paged_plan(pp, up([20, 0]), lens, table, free, count, T=24)
+    assert ab.device_error(dev) == CAPACITY
+    assert slots.tolist() == [-1] * 16 + [48, 49, 50, 51] + [-1] * 4 and table.tolist()[0][:2] == [wrong, 3]

@@ -140,3 +140,30 @@ def test_forward_qkv(dev, Lk):
     again = ab.ab_forward_qkv(p, nr, q, k, v, bufs=bufs)
     assert again is bufs and torch.equal(bufs.O, want.O)
     assert ab.device_error(dev) == 0
+
+
+@pytest.mark.parametrize("norm", ["none", "head"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("B,H,L,Lk,d", [(1, 17, 3900, 3900, 64), (2, 9, 1500, 2050, 128),             # units of one step, many a warp
+                                        (1, 5, 5000, 5000, 64), (2, 9, 6200, 6200, 128), (1, 40, 12500, 12500, 64),
+                                        (3, 17, 3000, 800, 64), (1, 19, 2600, 11000, 128)])           # units of a whole token
+def test_many_units_a_warp(dev, norm, interleaved, B, H, L, Lk, d):
+    # more units than warps: rows, tables and weights of one unit behind another's, with tokens of q, k and v in turn
+    # (as many of each) or one list after the other, and head counts that leave a step's rows idle
+    g = torch.Generator(device=dev).manual_seed(20)
+    n_pos = 300
+    w, cos, sin = _setup(norm, H, d, n_pos, 21)
+    nr = _nr(norm, interleaved, 1e-6, w, cos, sin, dev)
+    w, cos, sin = [None if t is None else t.to(dev) for t in w], cos.to(dev), sin.to(dev)
+    p = ab.Params(B=B, H=H, L=L, d=d, L_kv=Lk)
+    q = torch.randn(B, L, H, d, generator=g, device=dev).to(BF16)
+    kv = torch.randn(B, Lk, 2, H, d, generator=g, device=dev).to(BF16)
+    k, v = kv[:, :, 0], kv[:, :, 1]
+    pos = [torch.randint(0, n_pos, (B, n), generator=g, dtype=torch.int32, device=dev) for n in (L, Lk)]
+    Q, K, V = ab.ab_qk_norm_rope(p, nr, q, k, v, *pos)
+    assert torch.equal(V, v.transpose(1, 2))
+    for got, x, side in ((Q, q, 0), (K, k, 1)):
+        for b in range(B):
+            y, size = ref.norm_rotate(x[b], norm, w[side], cos, sin, pos[side][b], interleaved, 1e-6)
+            ref.assert_norm_rotate(got[b].transpose(0, 1), y, size, norm, H * d)
+    assert ab.device_error(dev) == 0

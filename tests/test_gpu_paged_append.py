@@ -43,8 +43,8 @@ def _same_bits(a, b):
     return torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))
 
 
-def _append_and_check(dev, pp, norm, interleaved, n_pos, slots, pos, seed, error=0):
-    """The call's outputs against the reference; the cache holds NaN before it."""
+def _append_and_check(dev, pp, norm, interleaved, n_pos, slots, pos, seed, error=0, fill=()):
+    """The call's outputs against the reference; the cache holds NaN before it, and keys in the slots `fill`."""
     T, Hq, Hkv, d, page = len(slots), pp.Hq, pp.Hkv, pp.d, pp.page
     (wq, wk, cos, sin), nr = _norm_rope(norm, Hq, Hkv, d, n_pos, interleaved, seed, dev)
     x = torch.randn(T, Hq + 2 * Hkv, d, generator=torch.Generator().manual_seed(seed + 1)).to(BF16)
@@ -52,7 +52,9 @@ def _append_and_check(dev, pp, norm, interleaved, n_pos, slots, pos, seed, error
     nan = float("nan")
     K, V = (torch.full((pp.num_pages, Hkv, page, d), nan, dtype=BF16, device=dev) for _ in range(2))
     ksum = torch.full((pp.num_pages, Hkv, d), nan, dtype=BF16, device=dev)
-    old = K.cpu(), ksum.cpu()
+    fill = torch.tensor(fill, dtype=torch.long)
+    K[(fill // page).to(dev), :, (fill % page).to(dev)] = torch.randn(len(fill), Hkv, d, generator=torch.Generator().manual_seed(seed + 2)).to(BF16).to(dev)
+    old = K.cpu(), V.cpu(), ksum.cpu()
     Q = torch.full((T, Hq, d), 7.0, dtype=BF16, device=dev)
     ab.ab_paged_append(pp, nr, xd[:, :Hq], xd[:, Hq:Hq + Hkv], xd[:, Hq + Hkv:], torch.tensor(slots, dtype=I32).to(dev),
                        torch.tensor(pos, dtype=I32).to(dev), K, V, ksum=ksum, out=Q)
@@ -69,10 +71,11 @@ def _append_and_check(dev, pp, norm, interleaved, n_pos, slots, pos, seed, error
     assert torch.equal(V[sl // page, :, sl % page], x[:, Hq + Hkv:])
     written = torch.zeros(pp.num_pages, page, dtype=torch.bool)
     written[sl // page, sl % page] = True
-    for t in (K, V):
-        assert _same_bits(t.transpose(1, 2)[~written], old[0].transpose(1, 2)[~written])
+    for t, t0 in ((K, old[0]), (V, old[1])):
+        assert _same_bits(t.transpose(1, 2)[~written], t0.transpose(1, 2)[~written])
     touched = written.any(1)
-    assert _same_bits(ksum[~touched], old[1][~touched])
+    assert _same_bits(ksum[~touched], old[2][~touched])
+    written[fill // page, fill % page] = True
     w = written[:, None, :, None]
     n = written.sum(1).double()[:, None, None].clamp(min=1)
     keys = torch.where(w, K.double(), 0.0)
@@ -188,3 +191,45 @@ def test_plan_reports_bad_pages_that_come_back(dev, wrong):
     cu, slots, pos = ab.ab_paged_plan(pp, up([20, 0]), lens, table, free, count, T=24)
     assert ab.device_error(dev) == CAPACITY
     assert slots.tolist() == [-1] * 16 + [48, 49, 50, 51] + [-1] * 4 and table.tolist()[0][:2] == [wrong, 3]
+
+
+@pytest.mark.parametrize("norm", ["none", "head", "token"])
+@pytest.mark.parametrize("Hq,Hkv,d,page,T", [(3, 1, 64, 64, 1500), (9, 9, 128, 16, 2500), (2, 1, 64, 32, 40000), (2, 1, 64, 64, 40000)])
+def test_long_lists_of_slots(dev, norm, Hq, Hkv, d, page, T):
+    # several pages a CTA of the means, and pages whose slots lie in two CTAs' parts of the list; sequences of all lengths in
+    # pages in random order, that begin inside a page, and slots without a token behind them
+    g = torch.Generator().manual_seed(80)
+    pages = torch.randperm(T // page * 3, generator=g).tolist()
+    num_pages = len(pages)
+    slots, pos = [], []
+    for n in [1, page - 1, page, page + 1, 5, 3 * page + 7] * (T // (9 * page) + 1) + [T]:
+        at = int(torch.randint(0, page, (1,), generator=g))       # keys that the sequence has
+        for i in range(at, at + n):
+            if i == at or i % page == 0:
+                first = pages.pop() * page
+            slots.append(first + i % page)
+            pos.append(i % 200)
+        if len(slots) > T - 20:
+            break
+    slots, pos = slots[:T - 20] + [-1] * 20, pos[:T - 20] + [0] * 20
+    # the keys before a sequence's first are in its first page's mean: written, in a call before
+    before = [(s, i) for s in range(T - 20) if s == 0 or slots[s] != slots[s - 1] + 1 and slots[s] % page for i in range(slots[s] % page)]
+    pp = ab.PagedParams(1, Hq, Hkv, d, page, num_pages, num_pages)
+    fill = [slots[s] - slots[s] % page + i for s, i in before]
+    _append_and_check(dev, pp, norm, True, 200, slots, pos, 81, fill=fill)
+
+
+def test_page_means_beyond_32_bits(dev):
+    # K of 2.3e9 elements: the mean of the last page's keys
+    num_pages, Hkv, page, d = 70000, 4, 64, 128
+    K, V = (torch.zeros(num_pages, Hkv, page, d, dtype=BF16, device=dev) for _ in range(2))
+    ksum = torch.zeros(num_pages, Hkv, d, dtype=BF16, device=dev)
+    K[-1] = torch.randn(Hkv, page, d, generator=torch.Generator().manual_seed(90)).to(BF16).to(dev)
+    pp = ab.PagedParams(1, 8, Hkv, d, page, num_pages, 10)
+    x = torch.randn(1, 16, d, generator=torch.Generator().manual_seed(91)).to(BF16).to(dev)
+    ab.ab_paged_append(pp, ab.NormRope("none"), x[:, :8], x[:, 8:12], x[:, 12:], torch.tensor([num_pages * page - 1], dtype=I32).to(dev),
+                       torch.zeros(1, dtype=I32, device=dev), K, V, ksum=ksum)
+    assert torch.equal(K[-1, :, -1], x[0, 8:12])
+    keys = K[-1].double()
+    off = (ksum[-1].double() - keys.mean(1)).abs() - (ref.HALF * keys.mean(1).abs() + (page + 2) * ref.U * 1.01 * keys.abs().mean(1))
+    assert off.max().item() <= 0 and not ksum[:-1].any()

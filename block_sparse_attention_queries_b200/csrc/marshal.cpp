@@ -21,6 +21,14 @@
 
 namespace {
 
+// Whole numbers in every place of a shape.
+bool is_shape(PyObject* shape) {
+  if (!PyTuple_Check(shape)) return false;
+  for (Py_ssize_t k = 0; k < PyTuple_GET_SIZE(shape); ++k)
+    if (!PyLong_Check(PyTuple_GET_ITEM(shape, k))) return false;
+  return true;
+}
+
 bool same_shape(const at::Tensor& t, PyObject* shape) {
   const auto sizes = t.sizes();
   if (Py_ssize_t(sizes.size()) != PyTuple_GET_SIZE(shape)) return false;
@@ -48,7 +56,7 @@ PyObject* refuse(PyObject* obj, const char* want, at::ScalarType type, PyObject*
 bool on_device(const at::Tensor& t, long index) { return t.is_cuda() && t.device().index() == index; }
 
 PyObject* tensors(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n < 1 || (n - 1) % 4 != 0) {
+  if (n < 1 || (n - 1) % 4 != 0 || !PyLong_Check(args[0])) {
     PyErr_SetString(PyExc_TypeError, "tensors(index, (tensor, dtype, shape, name) ...)");
     return nullptr;
   }
@@ -60,7 +68,7 @@ PyObject* tensors(PyObject*, PyObject* const* args, Py_ssize_t n) {
     for (Py_ssize_t k = 0; k < count; ++k) {
       PyObject* const* a = args + 1 + 4 * k;
       PyObject* item = nullptr;
-      if (!THPDtype_Check(a[1]) || !PyTuple_Check(a[2]) || !PyUnicode_Check(a[3])) {
+      if (!THPDtype_Check(a[1]) || !is_shape(a[2]) || !PyUnicode_Check(a[3])) {
         PyErr_SetString(PyExc_TypeError, "tensors: dtype, shape tuple and name expected");
       } else if (a[0] == Py_None) {
         Py_INCREF(Py_None);
@@ -91,7 +99,7 @@ PyObject* tensors(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 PyObject* tokens(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != 4 || !PyTuple_Check(args[2]) || !PyUnicode_Check(args[3])) {
+  if (n != 4 || !PyLong_Check(args[0]) || !is_shape(args[2]) || !PyUnicode_Check(args[3])) {
     PyErr_SetString(PyExc_TypeError, "tokens(index, tensor, shape, name)");
     return nullptr;
   }

@@ -294,6 +294,13 @@ ab_status check_rows(const ab_paged_params* p, const int32_t* cu_new, int32_t T)
   return AB_OK;
 }
 
+// O is written while other CTAs still read queries, keys and values.
+bool output_overlaps(const ab_paged_params* p, int32_t T, const void* Q, const void* K, const void* V, const void* O) {
+  const int64_t cache = int64_t(p->num_pages) * p->Hkv * p->page * p->d;
+  const Span o = span_of(O, int64_t(p->S) * p->Hq * p->d);
+  return overlap(o, span_of(Q, int64_t(T) * p->Hq * p->d)) || overlap(o, span_of(K, cache)) || overlap(o, span_of(V, cache));
+}
+
 ab_status prepare_append(const ab_paged_params* p, const ab_norm_rope* nr, int32_t T, const ab_tokens* q,
                          const ab_tokens* k, const ab_tokens* v, const int32_t* slots, const int32_t* positions,
                          void* Q, void* Kc, void* Vc, void* ksum, NormRopeArgs* a) {
@@ -543,6 +550,7 @@ ab_status ab_attention_paged(const ab_paged_params* p, int32_t T, const void* Q,
   s = check_rows(p, cu_new, T);
   if (s != AB_OK) return s;
   if (ws_bytes < paged_workspace(p).attend) return AB_ERR_WORKSPACE;
+  if (output_overlaps(p, T, Q, K, V, O)) return AB_ERR_INVALID_ARG;
   return run_paged_attention(p, paged_view(p, table, lens, cu_new, T), Q, K, V, idx, count, O,
                              static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream));
 }
@@ -563,6 +571,7 @@ ab_status ab_paged_forward(const ab_paged_params* p, const ab_norm_rope* nr, int
   if (s != AB_OK) return s;
   const PagedWorkspace w = paged_workspace(p);
   if (ws_bytes < w.select || ws_bytes < w.attend) return AB_ERR_WORKSPACE;
+  if (output_overlaps(p, T, Q, K, V, O)) return AB_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const PagedView view = paged_view(p, table, lens, cu_new, T);

@@ -510,7 +510,7 @@ ab_status ab_paged_topk(const ab_paged_params* p, const float* P, const int32_t*
  * as one of weight 0, whose infinite value gives NaN.
  *   idx, count  device, as ab_paged_topk writes them; both NULL: all pages
  *   O           device, out, [S, Hq, d] bf16 (row s; rows of skipped sequences
- *               are left as they were)
+ *               are left as they were); refused where it overlaps Q, K or V
  * The work is divided evenly over the GPU whatever the lengths are, and the
  * parts of a row are joined in a fixed order: results are the same each time.
  */

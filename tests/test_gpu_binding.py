@@ -127,3 +127,20 @@ def test_workspace_too_small(dev):
     with pytest.raises(ab.AbError) as e:
         ab.ab_attention_paged(PP, z(S, HQ, D, dtype=BF16), kv, kv, z(S, COLS), z(S), workspace=small)
     assert e.value.status == 6
+
+
+def test_an_output_over_its_inputs_is_refused(dev):
+    z = lambda *shape, dtype=I32: torch.zeros(*shape, dtype=dtype, device=dev)  # noqa: E731
+    Q, K, V = z(S, HQ, D, dtype=BF16), z(PAGES, HKV, PAGE, D, dtype=BF16), z(PAGES, HKV, PAGE, D, dtype=BF16)
+    more = dict(idx=z(S, HKV, COLS), count=z(S, HKV))
+    for out in (Q, K.view(-1)[-S * HQ * D:].view(S, HQ, D), V.view(-1)[:S * HQ * D].view(S, HQ, D)):
+        for kw in ({}, more):
+            with pytest.raises(ab.AbError) as e:
+                ab.ab_attention_paged(PP, Q, K, V, z(S, COLS), z(S), out=out, **kw)
+            assert e.value.status == 1
+    cache, bufs = ab.PagedCache(PP, dev), ab.PagedBuffers(PP, S, dev)
+    bufs.O = bufs.Q
+    with pytest.raises(ab.AbError) as e:
+        ab.ab_paged_forward(PP, ab.NormRope("none"), Q.clone(), z(S, HKV, D, dtype=BF16), z(S, HKV, D, dtype=BF16), cache, z(S + 1),
+                            z(S) - 1, z(S), bufs=bufs)
+    assert e.value.status == 1

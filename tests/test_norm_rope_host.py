@@ -103,3 +103,17 @@ def test_a_tensor_with_other_storage():
     w.at, w.is_cuda = 0x9000, False
     with pytest.raises(ValueError, match="CUDA"):
         nr.check(4, 2, 64, 0)
+
+
+def test_attention_output_over_its_inputs(lib):
+    # addresses alone: refused on the host, whatever part overlaps
+    pp = ab.PagedParams(S=4, Hq=8, Hkv=2, d=128, page=16, num_pages=100, max_pages=20)
+    n, cache, big = 4 * 8 * 128 * 2, 100 * 2 * 16 * 128 * 2, 1 << 45
+    Q, K, V = 0x10000000, 0x20000000, 0x30000000
+    for at, size in ((Q, n), (K, cache), (V, cache)):
+        for O in (at, at - n + 16, at + size - 16):
+            assert lib.ab_attention_paged(pp.c(), 4, Q, K, V, GOOD, GOOD, None, None, None, O, GOOD, big, None) == 1
+            assert lib.ab_attention_paged(pp.c(), 4, Q, K, V, GOOD, GOOD, None, GOOD, GOOD, O, GOOD, big, None) == 1
+            t = ab.ab_tokens(0x50000000, 0, 8 * 128, 128)
+            assert lib.ab_paged_forward(pp.c(), _nr(), 4, t, t, t, GOOD, GOOD, GOOD, GOOD, GOOD, Q, K, V, 0x60000000, GOOD, GOOD, GOOD,
+                                        O, GOOD, big, None) == 1

@@ -131,9 +131,6 @@ class NormRope:
         self.__dict__.update(norm=norm, interleaved=bool(interleaved), eps=float(eps), wq=wq, wk=wk, cos=cos, sin=sin)
         self._bind()
 
-    def _addresses(self):
-        return tuple(0 if t is None else t.data_ptr() for t in (self.wq, self.wk, self.cos, self.sin))
-
     def _bind(self):
         """The library's copy, from the tensors as they are."""
         import torch
@@ -150,10 +147,12 @@ class NormRope:
                                  f"got {tuple(t.shape)}")
         if cos is not None and (cos.dim() != 2 or cos.shape != sin.shape or cos.shape[0] < 1):
             raise ValueError("cos and sin must be [n_pos, d/2], with one row at least")
-        at, n_pos = self._addresses(), 0 if cos is None else cos.shape[0]
+        n_pos = 0 if cos is None else cos.shape[0]
+        at = [0 if t is None else t.data_ptr() for t in (wq, wk, cos, sin)]
         self.__dict__.update(
             n_pos=n_pos, device=tensors[0].device if tensors else None, _index=tensors[0].get_device() if tensors else None,
-            _fits=None, _at=at, _c=ab_norm_rope(NORMS[self.norm], int(self.interleaved), self.eps, n_pos, *at))
+            _fits=None, _where=[t.data_ptr for t in tensors], _at=[t.data_ptr() for t in tensors],
+            _c=ab_norm_rope(NORMS[self.norm], int(self.interleaved), self.eps, n_pos, *at))
 
     def __setattr__(self, name, value):
         raise AttributeError(f"cannot assign to {name!r}: make another NormRope")
@@ -163,7 +162,7 @@ class NormRope:
 
     def check(self, Hq: int, Hk: int, d: int, index: int):
         """The weights and tables belong to Hq query and Hk key heads of d on CUDA device `index`."""
-        if self._at != self._addresses():  # a tensor has other storage now (`.data = ...`)
+        if self._at != [where() for where in self._where]:  # a tensor has other storage now (`.data = ...`)
             self._bind()
         if self._fits == (Hq, Hk, d, index):
             return

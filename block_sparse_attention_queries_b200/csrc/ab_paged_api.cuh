@@ -363,7 +363,7 @@ ab_status run_paged_select(const ab_paged_params* p, const PagedView& v, const v
   if (!sms) return AB_ERR_CUDA;
   a.pitch = (p->max_pages + 3) / 4 * 4;
   // One launch with a CTA per row, for tables of few pages whose summaries fit in
-  // L2: 3 x 12 rows of 47 pages 2.7 us (two launches 5.8), 64 x 8 rows of 256 7.6
+  // L2: 3 x 12 rows of 47 pages 2.6 us (two launches 5.9), 64 x 8 rows of 256 7.6
   // (13.3), of 1000 31 (33); but 512 x 40 rows of 256 pages (1.3 GB) 350 (269: there
   // the warps of a CTA read neighbouring heads together), one row of 1000 7.2 (5.8).
   const int64_t rows = int64_t(p->S) * p->Hkv, bytes_all = rows * p->max_pages * p->d * 2;

@@ -40,9 +40,13 @@
 // join_parts.)  V rows that lie behind the sequence's end are set to zero in the
 // operand, since 0 times what an unwritten page holds may be NaN.
 //
-// Measured: 8 sequences of 122 thousand keys, 4 key heads of 8 query heads, 290 us
-// (6.9 TB/s of keys and values; 16 query heads each 311), 64 sequences of 1 to
-// 16384 keys 72 us (5.8 TB/s), one of 777 keys 9.5 us with the join.
+// Fewer bits than fp32 elsewhere: exponentials by ex2.approx (2^-22, as in the
+// selection and the joins), and the accumulators of the products, which cut off
+// (kDecOwnSum).
+//
+// Measured: 8 sequences of 122 thousand keys, 4 key heads of 8 query heads, 295 us
+// (6.8 TB/s of keys and values; 16 query heads each 300), 64 sequences of 1 to
+// 16384 keys 72 us (5.8 TB/s), one of 777 keys 9.2 us with the join.
 #pragma once
 
 #include <type_traits>
